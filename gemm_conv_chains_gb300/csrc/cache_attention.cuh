@@ -1,0 +1,668 @@
+// cache_attention.cuh -- attention over a paged e4m3 cache for a few query rows per sequence
+// and kv head (single tokens, drafts), split along the context; right for any number of rows.
+//
+// out = softmax(z) V with z = cap tanh(q k scale / cap) + slope (j - i) over the keys j <= i
+// of a sequence (cap and bias optional), k and v = code * the page's scale.  Each cached byte
+// is read once for all query heads that share it, so the bound is HBM: 2 D bytes per token and
+// kv head.  Every SM has to turn ~24 bytes per clock into fp16 and multiply them with all rows,
+// more than its fp32 lanes can; warp-level tensor-core products (m16n8k16) have the rate, and
+// with so few rows the 128-row tcgen05 tile would be nearly empty.
+//
+// The tokens are the M side of both products (S^T = K Q^T, O^T = V^T P^T) and the query rows
+// the N side, in tiles of 8, so that up to 8 rows (a usual group of query heads) waste nothing.
+// The order of the summed index is free as long as both operands share it, which removes every
+// transposition of 8-bit data: a lane loads 16-byte runs of the channels of its own fragment
+// rows (keys: tokens g and g + 8, channel run t; values: tokens 2t, 2t + 1, 2t + 8, 2t + 9,
+// channel run g; lane = 4 g + t), and only P^T crosses lanes (movmatrix).  So each lane reads
+// back exactly what it copied itself: the shared-memory ring needs no barrier, only the
+// lane's own cp.async groups.
+//
+// Work is cut evenly: the tiles of 64 tokens of all (sequence, kv head, row tile) are numbered
+// in a row and each CTA takes an equal run of them, found from the lengths on the device; runs
+// that split a row tile leave fp32 partial results (normalised, with their log2 sums) that a
+// second small kernel joins.  A CTA's four warps take the 16-token strips in turn, each with a
+// running maximum and sum of its own, joined in shared memory.
+//
+// Precision: codes, and with a per-row power of two also bf16 queries, are exact in fp16; the
+// products sum in fp32; the softmax is fp32; P is rounded to fp16 (11 bits, finer than a bf16
+// output, and of the order of an fp16 output's own rounding); the value scales go into P before
+// that rounding, relative to a running power of two, so that they cannot under- or overflow it.
+#pragma once
+
+#include "decoder_device.cuh"
+
+namespace b2b {
+
+constexpr int kAttendWarps = 4;
+constexpr int kTileTokens = 64;        // tokens per numbered tile: one strip per warp
+constexpr int kStrip = 16;
+constexpr float kNoMax = -1e30f;       // "no key seen": finite, so that no inf - inf arises
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma_m16n8k16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int BYTES>
+__device__ __forceinline__ void load_words(uint32_t addr, uint32_t* w) {
+  if constexpr (BYTES == 16)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
+                 : "memory");
+  else if constexpr (BYTES == 8)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+}
+
+// A query row's fp16 form: bf16 rows are divided by the power of two of their largest
+// magnitude (put back into the scores in fp32), fp16 rows are taken as they are.
+__device__ __forceinline__ float row_unit_of(float amax, bool bf16, float& inv) {
+  inv = 1.f;
+  if (!bf16) return 1.f;
+  uint32_t e = (__float_as_uint(amax) >> 23) & 0xFFu;
+  if (e == 0u || e >= 253u) return 1.f;          // zero, subnormal, huge, infinite or NaN
+  inv = __uint_as_float((254u - e) << 23);
+  return __uint_as_float(e << 23);
+}
+
+template <int D_>
+struct CacheDims {
+  static constexpr int D = D_;
+  static constexpr int kKBytes = D / 4;                                   // per lane and token
+  static constexpr int kVBytes = D / 8;
+  static constexpr int kKRun = kKBytes % 16 == 0 ? 16 : 8;                // bytes per copy
+  static constexpr int kVRun = kVBytes % 16 == 0 ? 16 : kVBytes % 8 == 0 ? 8 : 4;
+  static constexpr int kStage = kStrip * 2 * D;                           // bytes per warp
+  // about 96 KB per CTA, two CTAs per SM: ~160 KB in flight, several times what the HBM
+  // latency asks for
+  static constexpr int kStages = D <= 64 ? 8 : D <= 96 ? 7 : D <= 128 ? 6 : D <= 192 ? 4 : 3;
+  static constexpr int kRing = kStages * kStage;
+};
+
+template <int D, int NT>
+constexpr int attend_smem() {
+  constexpr int ring = kAttendWarps * CacheDims<D>::kRing;
+  constexpr int join = kAttendWarps * NT * 8 * (D + 2) * 4;
+  return (ring > join ? ring : join) + kAttendWarps * CacheDims<D>::kStages * 8 +
+         (NT > 1 ? D / 16 * NT * 256 : 0) + NT * 8 * 4;
+}
+
+template <int D, int NT, bool MODS>
+__global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_kernel(const AttendParams p) {
+  using C = CacheDims<D>;
+  constexpr int RT = NT * 8;
+  constexpr int KS = D / 16;           // k steps of S^T, m tiles of O^T
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const CacheView& c = p.c;
+
+  constexpr int kJoin = kAttendWarps * RT * (D + 2) * 4;
+  constexpr int kBody = kAttendWarps * C::kRing > kJoin ? kAttendWarps * C::kRing : kJoin;
+  uint8_t* ring = smem + warp * C::kRing;
+  const uint32_t ring_at = smem_u32(ring);
+  float2* stage_scales = reinterpret_cast<float2*>(smem + kBody) + warp * C::kStages;
+  uint2* q_frags = reinterpret_cast<uint2*>(smem + kBody + kAttendWarps * C::kStages * 8);
+  float* row_units = reinterpret_cast<float*>(smem + kBody + kAttendWarps * C::kStages * 8 +
+                                              (NT > 1 ? KS * NT * 256 : 0));
+
+  // ---- this CTA's run of tiles ----
+  auto work_of = [&](const Sequence& s) -> int64_t {
+    if (s.n <= 0) return 0;
+    const int64_t row_tiles = (static_cast<int64_t>(s.n) * p.group + RT - 1) / RT;
+    const int64_t tiles = p.whole ? 1 : (s.len + kTileTokens - 1) / kTileTokens;
+    return row_tiles * c.heads * tiles;
+  };
+  int64_t total = 0;
+  for (int b = lane; b < c.B; b += 32) total += work_of(load_sequence(c, b, DK_ATTEND));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  if (!p.whole && per < p.min_tiles) per = p.min_tiles;
+  int64_t at = blockIdx.x * per;
+  const int64_t run_end = at + per < total ? at + per : total;
+  const bool scribe = p.meta != nullptr && blockIdx.x == 0 && warp == 0;
+  if (scribe && lane == 0) p.meta[0] = per;            // for the kernel that joins the runs
+  grid_launch_dependents();
+  if (at >= run_end && !scribe) return;
+
+  // the sequence that holds tile `at`
+  int b = 0;
+  int64_t base = 0;                    // number of sequence b's first tile
+  {
+    int64_t before = 0;
+    bool found = false;
+    for (int b0 = 0; b0 < c.B; b0 += 32) {
+      int64_t w = 0;
+      if (b0 + lane < c.B) w = work_of(load_sequence(c, b0 + lane, DK_ATTEND));
+      int64_t upto = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      upto += before;
+      if (scribe && b0 + lane < c.B) p.meta[1 + b0 + lane] = upto - w;
+      const uint32_t hit = __ballot_sync(0xffffffffu, upto > at);
+      if (hit != 0u && !found) {
+        const int src = __ffs(hit) - 1;
+        b = b0 + src;
+        base = __shfl_sync(0xffffffffu, upto - w, src);
+        found = true;
+        if (!scribe) break;
+      }
+      before = __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+
+  Sequence s = at < run_end ? load_sequence(c, b, DK_ATTEND) : Sequence{0, 0, 0};
+  while (at < run_end) {
+    // ---- the next piece: (sequence b, kv head h, row tile rt), tiles [t0, t1) of it ----
+    int64_t work = work_of(s);
+    while (at >= base + work) {
+      base += work;
+      s = load_sequence(c, ++b, DK_ATTEND);
+      work = work_of(s);
+    }
+    const int rows = s.n * p.group;
+    const int row_tiles = (rows + RT - 1) / RT;
+    const int64_t tiles = p.whole ? 1 : (s.len + kTileTokens - 1) / kTileTokens;
+    const int64_t piece = (at - base) / tiles;
+    const int h = static_cast<int>(piece / row_tiles), rt = static_cast<int>(piece % row_tiles);
+    const int64_t t0 = at - base - piece * tiles;
+    int64_t t1 = t0 + (run_end - at);
+    if (t1 > tiles) t1 = tiles;
+    const bool partial = t0 != 0 || t1 != tiles;
+    const int slot = (t0 == 0 && at != blockIdx.x * per) ? 1 : 0;
+    at += t1 - t0;
+
+    const int row0 = rt * RT;
+    const int last_row = row0 + RT - 1 < rows ? row0 + RT - 1 : rows - 1;
+    const int start = s.len - s.n;
+    const int low_limit = start + row0 / p.group;         // last key of the tile's first row
+    const int high_limit = start + last_row / p.group;    // and of its last
+    int strip = static_cast<int>(p.whole ? 0 : t0 * (kTileTokens / kStrip)) + warp;
+    const int strips_all = high_limit / kStrip + 1;
+    const int64_t strips_run = p.whole ? strips_all : t1 * (kTileTokens / kStrip);
+    const int strip_end = static_cast<int>(strips_run < strips_all ? strips_run : strips_all);
+
+    // ---- page numbers and scales of this warp's next 32 strips, one per lane ----
+    const int32_t* pages_of = c.page_table + static_cast<int64_t>(b) * c.max_pages;
+    const int page_strips_shift = c.page_shift - 4;
+    auto fetch_page = [&](int first) -> int {
+      const int st = first + lane * kAttendWarps;
+      if (st >= strip_end) return -2;
+      return __ldg(pages_of + (st >> page_strips_shift));
+    };
+    auto fetch_scales = [&](int& id, float2& sc) {
+      sc = make_float2(0.f, 0.f);
+      if (id == -2) return;
+      if (id < 0 || id >= c.pages) {
+        index_error(c.err, DK_ATTEND, DEC_ERR_PAGE, static_cast<uint32_t>(b));
+        id = 0;                          // in bounds; its NaN scale shows in the output
+        sc = make_float2(__uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u));
+        return;
+      }
+      const int64_t at_scale = static_cast<int64_t>(id) * c.heads + h;
+      sc = make_float2(__ldg(c.k_scale + at_scale), __ldg(c.v_scale + at_scale));
+    };
+    int issue_strip = strip, issue_n = 0;            // next strip to copy, and its count
+    int ids = fetch_page(strip), next_ids;
+    float2 scs, next_scs = make_float2(0.f, 0.f);
+    fetch_scales(ids, scs);
+    next_ids = fetch_page(strip + 32 * kAttendWarps);
+
+    const int64_t head_bytes = static_cast<int64_t>(D) << c.page_shift;
+    auto issue = [&]() {
+      if (issue_strip < strip_end) {
+        const int k = issue_n & 31;
+        const int id = __shfl_sync(0xffffffffu, ids, k);
+        const float ks = __shfl_sync(0xffffffffu, scs.x, k);
+        const float vs = __shfl_sync(0xffffffffu, scs.y, k);
+        const int stage = issue_n % C::kStages;
+        if (lane == 0) stage_scales[stage] = make_float2(ks, vs);
+        const int slot0 = (issue_strip << 4) & ((1 << c.page_shift) - 1);
+        const int64_t off = (static_cast<int64_t>(id) * c.heads + h) * head_bytes + slot0 * D;
+        const uint8_t* kp = c.k + off;
+        const uint8_t* vp = c.v + off;
+        uint32_t dst = ring_at + stage * C::kStage;
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int j = 0; j < C::kKBytes / C::kKRun; ++j) {
+            copy_async<C::kKRun>(dst + lane * C::kKRun, kp + (g + 8 * half) * D + C::kKRun * (t + 4 * j));
+            dst += 32 * C::kKRun;
+          }
+#pragma unroll
+        for (int tok = 0; tok < 4; ++tok)
+#pragma unroll
+          for (int j = 0; j < C::kVBytes / C::kVRun; ++j) {
+            copy_async<C::kVRun>(dst + lane * C::kVRun,
+                                 vp + (2 * t + (tok & 1) + 8 * (tok >> 1)) * D + C::kVRun * (g + 8 * j));
+            dst += 32 * C::kVRun;
+          }
+        ++issue_n;
+        issue_strip += kAttendWarps;
+        if ((issue_n & 31) == 0) {                   // the prefetched 32 take over
+          ids = next_ids;
+          fetch_scales(ids, scs);
+          next_ids = fetch_page(issue_strip + 32 * kAttendWarps);
+        }
+      }
+      copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) issue();
+
+    // ---- the query rows as fp16 fragments ----
+    // k step u, lane (g, t): row 8 nt + g, channels kKRun * (t + 4 j) + 4 * (u mod run) + 0..3
+    uint32_t qf[NT == 1 ? KS : 1][2];
+    float qfactor[NT][2];                            // of rows 8 nt + 2 t, + 1
+    int limit[NT][2];                                // last key each of them sees
+    float slope[NT][2];
+    {
+      __syncthreads();                               // q_frags, row_units: the last piece is done
+      constexpr int kPerRun = C::kKRun / 4;          // k steps per run of channels
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (NT > 1 && nt % kAttendWarps != warp && NT >= kAttendWarps) continue;
+        if (NT > 1 && NT < kAttendWarps && nt != warp) continue;
+        const int r = row0 + 8 * nt + g;
+        uint32_t raw[KS][2];
+        float amax = 0.f;
+        const bool valid = r < rows;
+        const int tq = valid ? r / p.group : 0;
+        const uint16_t* src = p.q + (s.row + static_cast<int64_t>(tq)) * p.ldq +
+                              static_cast<int64_t>(h * p.group + (valid ? r - tq * p.group : 0)) * D;
+#pragma unroll
+        for (int u = 0; u < KS; ++u) {
+          const int d = C::kKRun * (t + 4 * (u / kPerRun)) + 4 * (u % kPerRun);
+          uint2 w = make_uint2(0u, 0u);
+          if (valid) w = __ldg(reinterpret_cast<const uint2*>(src + d));
+          raw[u][0] = w.x;
+          raw[u][1] = w.y;
+          const float2 a = p.is_bf16 ? widen2<true>(w.x) : widen2<false>(w.x);
+          const float2 z = p.is_bf16 ? widen2<true>(w.y) : widen2<false>(w.y);
+          amax = fmaxf(amax, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(z.x), fabsf(z.y))));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        float inv;
+        const float unit = row_unit_of(amax, p.is_bf16 != 0, inv);
+        if (NT == 1 ? warp == 0 : true)
+          if (t == 0) row_units[8 * nt + g] = unit;
+#pragma unroll
+        for (int u = 0; u < KS; ++u) {
+          uint32_t w[2] = {raw[u][0], raw[u][1]};
+          if (p.is_bf16) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float2 a = widen2<true>(w[i]);
+              w[i] = narrow2<false>(a.x * inv, a.y * inv);
+            }
+          }
+          if constexpr (NT == 1) {
+            qf[u][0] = w[0];
+            qf[u][1] = w[1];
+          } else {
+            q_frags[(u * NT + nt) * 32 + lane] = make_uint2(w[0], w[1]);
+          }
+        }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = row0 + 8 * nt + 2 * t + i;
+        const bool valid = r < rows;
+        const int tq = valid ? r / p.group : 0;
+        qfactor[nt][i] = row_units[8 * nt + 2 * t + i] * p.scale * (MODS ? 1.f : kLog2e);
+        limit[nt][i] = valid ? start + tq : 0x7FFFFFFF;
+        slope[nt][i] = 0.f;
+        if (MODS && p.slopes != nullptr && valid)
+          slope[nt][i] = __ldg(p.slopes + h * p.group + (r - tq * p.group));
+      }
+
+    float o[KS][NT][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = kNoMax;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+    float vref = 0.f, vref_inv = 0.f;
+
+    // ---- the strips ----
+    for (int n = 0; strip < strip_end; ++n, strip += kAttendWarps) {
+      copy_wait<C::kStages - 2>();
+      __syncwarp();
+      const int stage = n % C::kStages;
+      const float2 sc = stage_scales[stage];
+      uint32_t src = ring_at + stage * C::kStage;
+      float x[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[nt][e] = 0.f;
+      {
+        uint32_t kw[2][C::kKBytes / 4];
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int j = 0; j < C::kKBytes / C::kKRun; ++j) {
+            load_words<C::kKRun>(src + lane * C::kKRun, kw[half] + j * (C::kKRun / 4));
+            src += 32 * C::kKRun;
+          }
+#pragma unroll
+        for (int u = 0; u < KS; ++u) {
+          uint32_t a[4];
+          e4m3x4_to_f16(kw[0][u], a[0], a[2]);
+          e4m3x4_to_f16(kw[1][u], a[1], a[3]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            uint2 q;
+            if constexpr (NT == 1) q = make_uint2(qf[u][0], qf[u][1]);
+            else q = q_frags[(u * NT + nt) * 32 + lane];
+            mma_m16n8k16(x[nt], a, q.x, q.y);
+          }
+        }
+      }
+      const int tok0 = strip * kStrip + g;           // of x[.][0], x[.][1]; + 8: x[.][2], x[.][3]
+      const bool edge = strip * kStrip + kStrip - 1 > low_limit;
+      // scores in the log2 domain
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float z = x[nt][e] * (qfactor[nt][e & 1] * sc.x);
+          if (MODS) {
+            if (p.softcap > 0.f)                     // cap tanh(z / cap); tanh y = 1 - 2 / (e^2y + 1)
+              z = p.softcap - 2.f * p.softcap *
+                      rcp_fast(exp2_fast(z * (2.f * kLog2e / p.softcap)) + 1.f);
+            z += slope[nt][e & 1] * static_cast<float>(tok0 + 8 * (e >> 1) - limit[nt][e & 1]);
+            z *= kLog2e;
+          }
+          if (edge && tok0 + 8 * (e >> 1) > limit[nt][e & 1]) z = -INFINITY;
+          x[nt][e] = z;
+        }
+      // The running maximum is only a reference: it moves when a score is more than 2^8 above
+      // it (P stays below 2^8, well inside fp16), so most strips neither reduce nor rescale.
+      bool above = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) above |= x[nt][e] > m[nt][e & 1] + 8.f;
+      if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float top = fmaxf(x[nt][i], x[nt][i + 2]);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const float now = fmaxf(m[nt][i], top);
+            const float f = exp2_fast(m[nt][i] - now);
+            m[nt][i] = now;
+            l[nt][i] *= f;
+#pragma unroll
+            for (int u = 0; u < KS; ++u) {
+              o[u][nt][i] *= f;
+              o[u][nt][i + 2] *= f;
+            }
+          }
+      }
+      if (!(sc.y <= vref)) {                         // the same for the value scales
+        const float old = vref;
+        vref = __uint_as_float((__float_as_uint(sc.y) & 0x7F800000u) + 0x00800000u);
+        vref_inv = 1.f / vref;
+        const float f = old * vref_inv;
+#pragma unroll
+        for (int u = 0; u < KS; ++u)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[u][nt][e] *= f;
+      }
+      const float vs = sc.y * vref_inv;
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e[i] = exp2_fast(x[nt][i] - m[nt][i & 1]);
+          l[nt][i & 1] += e[i];
+        }
+        pf[nt][0] = transpose8x8(narrow2<false>(e[0] * vs, e[1] * vs));
+        pf[nt][1] = transpose8x8(narrow2<false>(e[2] * vs, e[3] * vs));
+      }
+      // ---- O^T += V^T P^T ----
+      uint32_t vw[4][C::kVBytes / 4];
+#pragma unroll
+      for (int tok = 0; tok < 4; ++tok)
+#pragma unroll
+        for (int j = 0; j < C::kVBytes / C::kVRun; ++j) {
+          load_words<C::kVRun>(src + lane * C::kVRun, vw[tok] + j * (C::kVRun / 4));
+          src += 32 * C::kVRun;
+        }
+      auto value_tile = [&](int i, uint32_t (&a)[4]) {
+        const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+        e4m3x4_to_f16(__byte_perm(vw[0][i / 2], vw[1][i / 2], sel), a[0], a[1]);
+        e4m3x4_to_f16(__byte_perm(vw[2][i / 2], vw[3][i / 2], sel), a[2], a[3]);
+      };
+      if (edge) {
+        // Slots past every row's reach may hold anything, a NaN too (0 * NaN is one): they are
+        // taken as zeros.  A NaN in a token that only some rows reach is taken out as well and
+        // put into the rows that do reach it.
+        uint32_t nan = 0;
+#pragma unroll
+        for (int tok = 0; tok < 4; ++tok) {
+          const int at_tok = strip * kStrip + 2 * t + (tok & 1) + 8 * (tok >> 1);
+#pragma unroll
+          for (int w = 0; w < C::kVBytes / 4; ++w) {
+            if (at_tok > high_limit) vw[tok][w] = 0u;
+            nan |= ((vw[tok][w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+          }
+        }
+        if (__any_sync(0xffffffffu, nan != 0u)) {
+          uint32_t seen[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              seen[nt][i] = transpose8x8((tok0 + 8 * i <= limit[nt][0] ? 0x3C00u : 0u) |
+                                         (tok0 + 8 * i <= limit[nt][1] ? 0x3C000000u : 0u));
+          uint32_t keep[4][C::kVBytes / 4];
+#pragma unroll
+          for (int tok = 0; tok < 4; ++tok)
+#pragma unroll
+            for (int w = 0; w < C::kVBytes / 4; ++w) {
+              const uint32_t bad =
+                  ((((vw[tok][w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu;
+              keep[tok][w] = vw[tok][w] & ~bad;
+              vw[tok][w] = bad & 0x38383838u;        // e4m3 1.0 where a NaN was
+            }
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            uint32_t a[4];
+            value_tile(i, a);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float hits[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_m16n8k16(hits, a, seen[nt][0], seen[nt][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (hits[e] > 0.f) o[i][nt][e] = __uint_as_float(0x7FC00000u);
+            }
+          }
+#pragma unroll
+          for (int tok = 0; tok < 4; ++tok)
+#pragma unroll
+            for (int w = 0; w < C::kVBytes / 4; ++w) vw[tok][w] = keep[tok][w];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        uint32_t a[4];
+        value_tile(i, a);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_m16n8k16(o[i][nt], a, pf[nt][0], pf[nt][1]);
+      }
+      issue();
+    }
+    copy_wait<0>();
+
+    // ---- the four warps' results joined ----
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 4);
+        l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 8);
+        l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 16);
+      }
+    __syncthreads();                                 // every ring is drained
+    float* join = reinterpret_cast<float*>(smem);
+    float* mine = join + warp * RT * D;
+    float2* stats = reinterpret_cast<float2*>(join + kAttendWarps * RT * D);
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      const int w = i / 2;
+      const int d = C::kVRun * (g + 8 * (4 * w / C::kVRun)) + (4 * w) % C::kVRun + 2 * (i & 1);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = 8 * nt + 2 * t;
+        *reinterpret_cast<float2*>(mine + r * D + d) =
+            make_float2(o[i][nt][0] * vref, o[i][nt][2] * vref);
+        *reinterpret_cast<float2*>(mine + (r + 1) * D + d) =
+            make_float2(o[i][nt][1] * vref, o[i][nt][3] * vref);
+      }
+    }
+    if (g == 0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          stats[warp * RT + 8 * nt + 2 * t + i] = make_float2(m[nt][i], l[nt][i]);
+    }
+    __syncthreads();
+    float* part = nullptr;
+    if (partial) part = p.part + (2 * static_cast<int64_t>(blockIdx.x) + slot) * RT * (D + 1);
+    for (int j = threadIdx.x; j < RT * D / 4; j += kAttendWarps * 32) {
+      const int r = j / (D / 4), d = 4 * (j % (D / 4));
+      if (row0 + r >= rows) break;
+      float2 st[kAttendWarps];
+      float top = kNoMax;
+#pragma unroll
+      for (int w = 0; w < kAttendWarps; ++w) {
+        st[w] = stats[w * RT + r];
+        top = fmaxf(top, st[w].x);
+      }
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kAttendWarps; ++w) {
+        const float f = exp2_fast(st[w].x - top);
+        sum += f * st[w].y;
+        const float4 v = *reinterpret_cast<const float4*>(join + (w * RT + r) * D + d);
+        acc.x += f * v.x;
+        acc.y += f * v.y;
+        acc.z += f * v.z;
+        acc.w += f * v.w;
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;     // a row that sees no key is zero
+      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      if (partial) {
+        *reinterpret_cast<float4*>(part + r * D + d) = acc;
+        if (d == 0) part[RT * D + r] = sum == 0.f ? kNoMax : top + log2f(sum);
+      } else {
+        const int tq = (row0 + r) / p.group;
+        uint16_t* dst = p.out + ((s.row + static_cast<int64_t>(tq)) * p.q_heads + h * p.group +
+                                 (row0 + r - tq * p.group)) * D + d;
+        *reinterpret_cast<uint2*>(dst) =
+            p.is_bf16 ? make_uint2(narrow2<true>(acc.x, acc.y), narrow2<true>(acc.z, acc.w))
+                      : make_uint2(narrow2<false>(acc.x, acc.y), narrow2<false>(acc.z, acc.w));
+      }
+    }
+    __syncthreads();                                 // the ring may be filled again
+  }
+}
+
+template <int D, int NT, bool MODS>
+cudaError_t launch_attend_one(const AttendParams& p, cudaStream_t s) {
+  constexpr int smem = attend_smem<D, NT>();
+  static_assert(smem <= 113 * 1024, "two CTAs per SM");
+  auto* fn = attend_kernel<D, NT, MODS>;
+  // per device: a process that moves between devices sets it again, which is harmless
+  static thread_local int set_on = -1;
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (set_on != dev) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    set_on = dev;
+  }
+  fn<<<p.grid, kAttendWarps * 32, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_attend_d(int nt, const AttendParams& p, cudaStream_t s) {
+  const bool mods = p.softcap > 0.f || p.slopes != nullptr;
+  if (nt == 1)
+    return mods ? launch_attend_one<D, 1, true>(p, s) : launch_attend_one<D, 1, false>(p, s);
+  if constexpr (D <= 128) {
+    if (nt == 4)
+      return mods ? launch_attend_one<D, 4, true>(p, s) : launch_attend_one<D, 4, false>(p, s);
+  }
+  return mods ? launch_attend_one<D, 2, true>(p, s) : launch_attend_one<D, 2, false>(p, s);
+}
+
+}  // namespace b2b

@@ -1,0 +1,90 @@
+// decoder.h -- internal interface of the decoder-block operators (rotary positions, the
+// append to a paged e4m3 cache, the attention over it): launch parameters and launchers.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace b2b {
+
+// Error word of these operators: {code, kernel, what, index}; the first error wins.
+enum DecoderError : uint32_t {
+  DEC_ERR_POSITION = 1,   // a position outside the rotary table
+  DEC_ERR_PAGE = 2,       // a page number outside the pool
+  DEC_ERR_LENGTH = 3,     // a length that is below its new tokens or above its page table
+  DEC_ERR_STARTS = 4      // starts that decrease, leave the rows or exceed max_new
+};
+enum DecoderKernel : uint32_t { DK_ROTARY = 32, DK_APPEND = 33, DK_ATTEND = 34, DK_PROMPT = 35 };
+constexpr uint32_t kCodeIndex = 2;   // B2B_ERR_SHAPE: a length, page number or position out of range
+
+constexpr float kE4m3Max = 448.f;
+constexpr float kScaleMin = 5.421010862427522e-20f;   // 2^-64
+
+struct RotaryParams {
+  const uint16_t* x;
+  uint16_t* out;
+  const float2* table;        // (cos, sin) of [positions][rot / 2]
+  const int32_t* positions;
+  int64_t T, ldx, ldo, table_len;
+  int32_t H, D, rot;
+  int32_t interleaved, inverse;
+  uint32_t* err;
+};
+
+// The cache and how the sequences of a call lie in it.
+struct CacheView {
+  uint8_t* k;                 // [pages][heads][page][D]
+  uint8_t* v;
+  float* k_scale;             // [pages][heads]
+  float* v_scale;
+  const int32_t* page_table;  // [B][max_pages]
+  const int32_t* lens;        // [B], new tokens included
+  const int32_t* starts;      // [B + 1] or null: T / B rows each
+  int64_t T;
+  int32_t pages, heads, page_shift, D;
+  int32_t B, max_pages, max_new;
+  uint32_t* err;
+};
+
+struct AppendParams {
+  CacheView c;
+  const uint16_t* k;          // [T] rows of heads x D
+  const uint16_t* v;
+  const uint16_t* q;          // [T] rows of q_heads x D, or null
+  uint16_t* q_out;
+  const float2* table;        // or null: no rotation
+  int64_t ldk, ldv, ldq, ldqo, table_len;
+  int32_t q_heads, rot, interleaved;
+};
+
+struct AttendParams {
+  CacheView c;
+  const uint16_t* q;
+  uint16_t* out;              // [T][q_heads][D]
+  const float* slopes;        // [q_heads] or null
+  int64_t ldq;
+  int32_t q_heads, group, is_bf16;
+  float scale, softcap;       // softcap 0: none
+  int32_t grid, min_tiles, whole;
+  float* part;                // split workspace: see cache_attention.cuh
+  int64_t* meta;
+  uint64_t wait_limit_ns;
+};
+
+cudaError_t launch_rotary(bool bf16, const RotaryParams& p, cudaStream_t s);
+cudaError_t launch_rotary_table(float2* table, int64_t n, int32_t half, const double* params,
+                                cudaStream_t s);
+cudaError_t launch_append(bool bf16, const AppendParams& p, cudaStream_t s);
+
+// Rows of queries per tile of the split kernel for `rows` query rows per sequence and head.
+int attend_row_tiles(int D, int64_t rows);
+int attend_ctas_per_sm();
+cudaError_t launch_attend_64(int nt, const AttendParams& p, cudaStream_t s);
+cudaError_t launch_attend_96(int nt, const AttendParams& p, cudaStream_t s);
+cudaError_t launch_attend_128(int nt, const AttendParams& p, cudaStream_t s);
+cudaError_t launch_attend_192(int nt, const AttendParams& p, cudaStream_t s);
+cudaError_t launch_attend_256(int nt, const AttendParams& p, cudaStream_t s);
+cudaError_t launch_attend_combine(const AttendParams& p, int nt, int threads, cudaStream_t s);
+
+}  // namespace b2b

@@ -25,6 +25,16 @@ _lock = threading.Lock()
 _lib = None
 
 
+class _Cache(ctypes.Structure):
+    """b2b_cache (include/b2b.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("batch", ctypes.c_int32), ("page_table", ctypes.c_void_p),
+                ("max_pages", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("lens", ctypes.c_void_p), ("starts", ctypes.c_void_p)]
+
+
 class B2BError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -100,6 +110,17 @@ def lib() -> ctypes.CDLL:
         L.b2b_get_tune_record.argtypes = [i32, p64, i32, ctypes.POINTER(i32), i32,
                                           ctypes.POINTER(i32)]
         L.b2b_get_tune_record.restype = ci
+        vpi, f32, f64 = ctypes.POINTER(_Cache), ctypes.c_float, ctypes.c_double
+        L.b2b_rotary_table.argtypes = [i64, i32, f64, ci, f64, i64, f64, f64, f64, vp, vp]
+        L.b2b_rotary.argtypes = [ci, i64, i32, i32, i32, ci, i32, vp, i64, vp, i64, vp, vp, i64, vp]
+        L.b2b_cache_append.argtypes = [ci, vpi, i64, vp, i64, vp, i64, vp, i64, i32, ci, vp, i64,
+                                       i32, vp, i64, vp]
+        L.b2b_cache_attention_workspace.argtypes = [vpi, i64, i32, ctypes.POINTER(i64)]
+        L.b2b_cache_attention.argtypes = [ci, vpi, i64, vp, i64, i32, f32, f32, vp, vp, vp, i64, vp]
+        L.b2b_get_cache_error.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
+        for name in ("b2b_rotary_table", "b2b_rotary", "b2b_cache_append",
+                     "b2b_cache_attention_workspace", "b2b_cache_attention", "b2b_get_cache_error"):
+            getattr(L, name).restype = ci
         _lib = L
         return L
 
@@ -393,6 +414,239 @@ def maxpool2x2_nhwc(x, out=None, stream=None):
         _raise(lib().maxpool2x2_nhwc(_dtype_code(x), N, H, W, C, _ptr(x), _ptr(out),
                                      _stream(stream, dev)), "maxpool2x2_nhwc")
     return out
+
+
+# ------------------------------------------------------------------------------------
+# decoder block: rotary positions, the paged 8-bit cache and the attention over it
+# ------------------------------------------------------------------------------------
+
+LAYOUTS = {"half": 0, "interleaved": 1}
+SCALINGS = {"plain": 0, "linear": 1, "blend": 2}
+
+
+def _rows(t, name, dt, T, H, D) -> int:
+    """Checks a [T, H, D] operand whose heads and channels are dense and returns its token
+    stride in elements."""
+    if t.dtype != dt:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dt}")
+    if t.shape != (T, H, D):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, H, D)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    ld, sh, sd = t.stride()
+    if sd != 1 or (H > 1 and sh != D):
+        raise ValueError(f"{name} must have dense heads and channels, got strides {t.stride()}")
+    return ld if T > 1 else H * D
+
+
+def _table_of(table, D):
+    """Checks a rotary table [positions, rot / 2, 2] and returns rot."""
+    if table.dtype != torch.float32:
+        raise TypeError(f"table has dtype {table.dtype}, expected torch.float32")
+    if table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError(f"table has shape {tuple(table.shape)}, expected [positions, rot / 2, 2]")
+    if not table.is_cuda or not table.is_contiguous():
+        raise ValueError("table must be a contiguous CUDA tensor")
+    return 2 * table.shape[1]
+
+
+def _layout(layout) -> int:
+    try:
+        return LAYOUTS[layout]
+    except KeyError:
+        raise ValueError(f"unknown layout {layout!r}; expected one of {list(LAYOUTS)}") from None
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor for work on `stream` (None: the current one), from that stream's memory."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+class _on_device:
+    """torch.cuda.device(dev), without its cost where dev is already current."""
+
+    def __init__(self, dev):
+        self.inner = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.inner is not None:
+            self.inner.__enter__()
+
+    def __exit__(self, *exc):
+        if self.inner is not None:
+            self.inner.__exit__(*exc)
+
+
+def rotary_table(positions, rot, base=10000.0, scaling="plain", factor=1.0, original=0, low=1.0,
+                 high=32.0, gain=1.0, device="cuda", stream=None):
+    """(cos, sin) of every position below `positions` for heads that rotate their first `rot`
+    channels: float32 [positions, rot / 2, 2] (b2b_rotary_table).  scaling "linear" divides the
+    frequencies by `factor`; "blend" only those that turn fewer than `low` times over the
+    `original` length, with a linear change up to `high` turns."""
+    if scaling not in SCALINGS:
+        raise ValueError(f"unknown scaling {scaling!r}; expected one of {list(SCALINGS)}")
+    device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError(f"device must be a CUDA device, got {device}")
+    out = _empty((positions, rot // 2, 2), torch.float32, device, stream)
+    with _on_device(out.device):
+        _raise(lib().b2b_rotary_table(positions, rot, base, SCALINGS[scaling], factor, original,
+                                      low, high, gain, out.data_ptr(),
+                                      _stream(stream, out.device)), "b2b_rotary_table")
+    return out
+
+
+def rotary(x, table, positions, layout="half", inverse=False, out=None, stream=None):
+    """x [T, H, D] (token stride free) with the first rot channels of each head turned by the
+    angles of positions [T] (int32), table [P, rot / 2, 2] (rotary_table); the inverse turns
+    back, which is the gradient.  out may be x (b2b_rotary)."""
+    dt = x.dtype
+    T, H, D = x.shape
+    code = _dtype_code(x)
+    ldx = _rows(x, "x", dt, T, H, D)
+    rot = _table_of(table, D)
+    _check_tensor(positions, "positions", torch.int32, (T,))
+    if out is None:
+        out = _empty((T, H, D), dt, x.device, stream)
+    ldo = _rows(out, "out", dt, T, H, D)
+    dev = _common_device(x=x, table=table, positions=positions, out=out)
+    with _on_device(dev):
+        _raise(lib().b2b_rotary(code, T, H, D, rot, _layout(layout), 1 if inverse else 0,
+                                x.data_ptr(), ldx, table.data_ptr(), table.shape[0],
+                                positions.data_ptr(), out.data_ptr(), ldo, _stream(stream, dev)),
+               "b2b_rotary")
+    return out
+
+
+def _cache_of(T, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts, max_new) -> _Cache:
+    """Checks the cache's tensors and describes them (b2b_cache)."""
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected "
+                         "[pages, heads, page size, head size]")
+    pages, heads, page, D = shape = k_cache.shape
+    _check_tensor(k_cache, "k_cache", torch.float8_e4m3fn, shape)
+    _check_tensor(v_cache, "v_cache", torch.float8_e4m3fn, shape)
+    _check_tensor(k_scale, "k_scale", torch.float32, (pages, heads))
+    _check_tensor(v_scale, "v_scale", torch.float32, (pages, heads))
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [sequences, pages]")
+    B, max_pages = page_table.shape
+    _check_tensor(page_table, "page_table", torch.int32, (B, max_pages))
+    _check_tensor(lens, "lens", torch.int32, (B,))
+    if starts is not None:
+        _check_tensor(starts, "starts", torch.int32, (B + 1,))
+    if max_new is None:
+        max_new = T if starts is not None else T // max(B, 1)
+    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                  pages, heads, page, D, B, page_table.data_ptr(), max_pages, max_new,
+                  lens.data_ptr(), None if starts is None else starts.data_ptr())
+
+
+def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts=None,
+                 max_new=None, table=None, layout="half", q=None, q_out=None, stream=None):
+    """Appends the new tokens' keys and values, k and v [T, heads, D] (token strides free), to
+    the paged e4m3 cache k_cache, v_cache [pages, heads, page size, D] with scales [pages, heads],
+    in place; with `table`, keys are rotated on the way, and queries q [T, q heads, D] into
+    q_out (new unless given; may be q), which is returned (b2b_cache_append).
+
+    page_table [B, pages per sequence], lens [B] (the new tokens included) and starts [B + 1]
+    (rows of each sequence among the T; None: T / B each) are int32; max_new is the most new
+    tokens of a sequence (default: T, or T / B without starts)."""
+    dt = k.dtype
+    code = _dtype_code(k)
+    T = k.shape[0]
+    c = _cache_of(T, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts, max_new)
+    heads, D = c.heads, c.head_dim
+    ldk = _rows(k, "k", dt, T, heads, D)
+    ldv = _rows(v, "v", dt, T, heads, D)
+    rot = 0 if table is None else _table_of(table, D)
+    ldq = ldqo = q_heads = 0
+    if q is not None:
+        if table is None:
+            raise ValueError("q is given to be rotated: it needs a table")
+        q_heads = q.shape[1]
+        ldq = _rows(q, "q", dt, T, q_heads, D)
+        if q_out is None:
+            q_out = _empty((T, q_heads, D), dt, q.device, stream)
+        ldqo = _rows(q_out, "q_out", dt, T, q_heads, D)
+    elif q_out is not None:
+        raise ValueError("q_out is given without q")
+    dev = _common_device(k=k, v=v, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale,
+                         v_scale=v_scale, page_table=page_table, lens=lens, starts=starts,
+                         table=table, q=q, q_out=q_out)
+    with _on_device(dev):
+        _raise(lib().b2b_cache_append(
+            code, c, T, k.data_ptr(), ldk, v.data_ptr(), ldv,
+            None if table is None else table.data_ptr(), 0 if table is None else table.shape[0],
+            rot, _layout(layout), None if q is None else q.data_ptr(), ldq, q_heads,
+            None if q is None else q_out.data_ptr(), ldqo, _stream(stream, dev)),
+            "b2b_cache_append")
+    return q_out
+
+
+def cache_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts=None,
+                    max_new=None, scale=None, softcap=0.0, slopes=None, out=None, workspace=None,
+                    stream=None):
+    """Attention of the new tokens' queries q [T, q heads, D] (token stride free) over their
+    sequences' cached tokens, causal within the new ones: [T, q heads, D] (b2b_cache_attention).
+    The cache and its sequences as in cache_append; scale defaults to D^-1/2; softcap caps the
+    scores by a tanh, slopes [q heads] (float32) add slope * (key position - query position).
+    workspace (uint8, at least cache_attention_workspace's bytes): allocated when not given."""
+    dt = q.dtype
+    code = _dtype_code(q)
+    T, q_heads, D = q.shape
+    c = _cache_of(T, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts, max_new)
+    if D != c.head_dim:
+        raise ValueError(f"q has head size {D}, the cache {c.head_dim}")
+    ldq = _rows(q, "q", dt, T, q_heads, D)
+    if slopes is not None:
+        _check_tensor(slopes, "slopes", torch.float32, (q_heads,))
+    if out is None:
+        out = _empty((T, q_heads, D), dt, q.device, stream)
+    _check_tensor(out, "out", dt, (T, q_heads, D))
+    dev = _common_device(q=q, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                         page_table=page_table, lens=lens, starts=starts, slopes=slopes, out=out,
+                         workspace=workspace)
+    with _on_device(dev):
+        if workspace is None:
+            need = ctypes.c_int64(0)
+            _raise(lib().b2b_cache_attention_workspace(c, T, q_heads, ctypes.byref(need)),
+                   "b2b_cache_attention_workspace")
+            if need.value > 0:
+                workspace = _empty(need.value, torch.uint8, dev, stream)
+        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise TypeError("workspace must be a contiguous uint8 tensor")
+        _raise(lib().b2b_cache_attention(
+            code, c, T, q.data_ptr(), ldq, q_heads, D ** -0.5 if scale is None else scale, softcap,
+            None if slopes is None else slopes.data_ptr(), out.data_ptr(),
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel(), _stream(stream, dev)),
+            "b2b_cache_attention")
+    return out
+
+
+def cache_attention_workspace(T, q_heads, k_cache, v_cache, k_scale, v_scale, page_table, lens,
+                              starts=None, max_new=None) -> int:
+    """Bytes of workspace that cache_attention takes for these arguments (0: none)."""
+    c = _cache_of(T, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts, max_new)
+    need = ctypes.c_int64(0)
+    with _on_device(k_cache.device):
+        _raise(lib().b2b_cache_attention_workspace(c, T, q_heads, ctypes.byref(need)),
+               "b2b_cache_attention_workspace")
+    return need.value
+
+
+def get_cache_error():
+    """(status, info[4]) of the decoder-block operators' error word; reads and clears it
+    (synchronises; b2b_get_cache_error)."""
+    info = (ctypes.c_uint32 * 4)()
+    st = lib().b2b_get_cache_error(info)
+    return int(st), [int(v) for v in info]
 
 
 # ------------------------------------------------------------------------------------

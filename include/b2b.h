@@ -205,6 +205,111 @@ b2b_status maxpool2x2_nhwc(b2b_dtype dt, int32_t N, int32_t H, int32_t W, int32_
                            const void* x, void* y, void* stream);
 
 /* ------------------------------------------------------------------------------------ */
+/* Decoder block: rotary positions, and attention over a paged 8-bit key/value cache     */
+/* ------------------------------------------------------------------------------------ */
+/* What a decoder block needs around its GEMMs and its FFN chain (b2b_gemm): positions, the
+ * cache and the attention over it, itself a chain of two products whose intermediate (the
+ * scores) stays on chip.  Conventions as above, with these differences: rows of q, k, v, x
+ * may be strided (ld elements between tokens, a multiple of 8, at least the row's length;
+ * heads and channels are dense within a row), since they are usually slices of one fused
+ * projection; and numbers that only the device knows (lengths, page numbers, positions) are
+ * checked there: one out of range is never followed, but recorded in an error word of these
+ * operators (b2b_get_cache_error), and the outputs that depend on it are unspecified. */
+
+/* The rotation's channel pairs: HALF pairs channel i with i + rot / 2, INTERLEAVED pairs 2i
+ * with 2i + 1; i < rot / 2 in both. */
+typedef enum b2b_rotary_layout { B2B_ROTARY_HALF = 0, B2B_ROTARY_INTERLEAVED = 1 } b2b_rotary_layout;
+
+/* Frequencies of a rotary table, f_i = base^(-2i / rot) scaled for contexts longer than the
+ * `original` one: PLAIN f_i; LINEAR f_i / factor; BLEND keeps f_i for pairs that turn more than
+ * `high` times over the original length, takes f_i / factor for those below `low` turns and a
+ * linear share of both between, and multiplies (cos, sin) by `gain` in every kind (1: none). */
+typedef enum b2b_rotary_scaling {
+    B2B_ROTARY_PLAIN = 0, B2B_ROTARY_LINEAR = 1, B2B_ROTARY_BLEND = 2
+} b2b_rotary_scaling;
+
+/* table[position][i] = (cos, sin)(position * f_i) * gain, fp32 pairs [positions][rot / 2][2],
+ * computed in fp64 and rounded once.  rot: a multiple of 16. */
+b2b_status b2b_rotary_table(int64_t positions, int32_t rot, double base, b2b_rotary_scaling scaling,
+                            double factor, int64_t original, double low, double high, double gain,
+                            float* table, void* stream);
+
+/* out[t][h][:] = x[t][h][:] with each pair (a, b) of the first `rot` channels turned by the
+ * table's (c, s) of position positions[t]:  a' = a c - b s,  b' = b c + a s  in fp32, rounded
+ * once; channels past rot are copied.  inverse = 1 turns back (s -> -s), which is also the
+ * gradient: dx = inverse rotation of dy (exactly so for gain 1; with another gain both carry
+ * it).  x, out: T rows of H x D, strides ldx, ldo; out may be x (same stride) for an in-place
+ * rotation, and must not overlap it otherwise.  positions: device int32 [T].
+ * D a multiple of 8, rot a multiple of 16, rot <= D. */
+b2b_status b2b_rotary(b2b_dtype dt, int64_t T, int32_t H, int32_t D, int32_t rot,
+                      b2b_rotary_layout layout, int32_t inverse, const void* x, int64_t ldx,
+                      const float* table, int64_t positions_in_table, const int32_t* positions,
+                      void* out, int64_t ldo, void* stream);
+
+/* A paged cache and the sequences of one call.  Codes are e4m3 (no infinities, one NaN); the
+ * value of a code is code * scale, one fp32 scale per page and kv head.  Position j of sequence
+ * s lies in slot j % page_size of page page_table[s][j / page_size].  The call's new tokens are
+ * rows [starts[s], starts[s + 1]) of its inputs, positions lens[s] - n .. lens[s] - 1.  Page
+ * numbers of positions at or past lens[s] are not read.  Every array is a device array. */
+typedef struct b2b_cache {
+    void* k;                    /* e4m3 [pages][heads][page_size][head_dim] */
+    void* v;                    /* the same */
+    float* k_scale;             /* [pages][heads] */
+    float* v_scale;             /* [pages][heads] */
+    int64_t pages;
+    int32_t heads;              /* kv heads */
+    int32_t page_size;          /* a power of two from 16 to 256 */
+    int32_t head_dim;           /* 64, 96, 128, 192 or 256 */
+    int32_t batch;              /* sequences */
+    const int32_t* page_table;  /* [batch][max_pages] */
+    int32_t max_pages;
+    int32_t max_new;            /* the most new tokens of any sequence (1 <= max_new <= T) */
+    const int32_t* lens;        /* [batch]: cached tokens, this call's new ones included */
+    const int32_t* starts;      /* [batch + 1], or NULL: T / batch new tokens each */
+} b2b_cache;
+
+/* Writes the T new tokens' keys and values into the cache; keys are rotated by their positions
+ * on the way when table is given (as b2b_rotary, in fp32, not rounded in between), and so are
+ * the queries q -> q_out when q is given (q_out may be q).  For each page touched and kv head,
+ * A the largest finite magnitude of its new values and s its scale if it already holds older
+ * tokens of the sequence (else 0):
+ *   s' = max(s, A / 448, 2^-64),   new codes = e4m3(y / s'),
+ *   and where s' > s the page's older codes become e4m3(code * (s / s'))
+ * in fp32, to nearest even, saturating (an infinity becomes +-448 s'; a NaN stays one).  Calling
+ * again with the same arguments changes nothing.  Pages that are written belong to one
+ * sequence.  k, v: T rows of heads x head_dim, strides ldk, ldv. */
+b2b_status b2b_cache_append(b2b_dtype dt, const b2b_cache* cache, int64_t T, const void* k,
+                            int64_t ldk, const void* v, int64_t ldv, const float* table,
+                            int64_t positions_in_table, int32_t rot, b2b_rotary_layout layout,
+                            const void* q, int64_t ldq, int32_t q_heads, void* q_out, int64_t ldqo,
+                            void* stream);
+
+/* out[t][h] = sum_j softmax_j(z) v_j over the keys j <= i of its sequence, i the position of
+ * row t, kv head h / (q_heads / heads):
+ *   z_j = cap(scale * q . k_j) + slopes[h] * (j - i),   cap(x) = softcap * tanh(x / softcap)
+ * (softcap 0: none; slopes NULL: no bias; slopes: device fp32 [q_heads]).  A row that sees no
+ * key is zero.  Sums, softmax and bias in fp32; the probabilities are rounded to fp16 before
+ * the second product (11 bits, relative to the row's maximum), out once to dt.
+ * q: T rows of q_heads x head_dim, stride ldq; out: dense [T][q_heads][head_dim], not q.
+ * Nothing past a row's reach enters it, whatever its slots hold.
+ * workspace: device memory of at least the bytes that b2b_cache_attention_workspace gives for
+ * the same cache, T and q_heads (16-byte aligned; NULL where that is 0), free again when the
+ * call's work on `stream` is done; its contents need no preparation. */
+b2b_status b2b_cache_attention_workspace(const b2b_cache* cache, int64_t T, int32_t q_heads,
+                                         int64_t* bytes);
+b2b_status b2b_cache_attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, const void* q,
+                               int64_t ldq, int32_t q_heads, float scale, float softcap,
+                               const float* slopes, void* out, void* workspace,
+                               int64_t workspace_bytes, void* stream);
+
+/* Reads and clears these operators' error word on the current device (synchronises it):
+ * B2B_OK, B2B_ERR_SHAPE for a position outside the rotary table (info[2] = 1), a page number
+ * outside the pool (2), a length below its new tokens or above its page table (3) or starts
+ * that decrease, leave the T rows or exceed max_new (4), B2B_ERR_TIMEOUT for a wait given up.
+ * info[1] = kernel, info[3] = sequence (rotary: row).  info may be NULL. */
+b2b_status b2b_get_cache_error(uint32_t info[4]);
+
+/* ------------------------------------------------------------------------------------ */
 /* Diagnostics                                                                           */
 /* ------------------------------------------------------------------------------------ */
 
