@@ -77,14 +77,14 @@ cudaError_t launch_rotary_table(float2* table, int64_t n, int32_t half, const do
                                 cudaStream_t s);
 cudaError_t launch_append(bool bf16, const AppendParams& p, cudaStream_t s);
 
-// Rows of queries per tile of the split kernel for `rows` query rows per sequence and head.
-int attend_row_tiles(int D, int64_t rows);
-int attend_ctas_per_sm();
+// The split kernel with row tiles of 8 nt query rows, per head size.
 cudaError_t launch_attend_64(int nt, const AttendParams& p, cudaStream_t s);
 cudaError_t launch_attend_96(int nt, const AttendParams& p, cudaStream_t s);
 cudaError_t launch_attend_128(int nt, const AttendParams& p, cudaStream_t s);
 cudaError_t launch_attend_192(int nt, const AttendParams& p, cudaStream_t s);
 cudaError_t launch_attend_256(int nt, const AttendParams& p, cudaStream_t s);
+// The tcgen05 kernel for prompts (head sizes 64, 96, 128).
+cudaError_t launch_prompt(const AttendParams& p, cudaStream_t s);
 cudaError_t launch_attend_combine(const AttendParams& p, int nt, int threads, cudaStream_t s);
 
 }  // namespace b2b

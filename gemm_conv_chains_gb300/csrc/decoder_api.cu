@@ -110,13 +110,19 @@ CacheView view_of(const b2b_cache* c, int64_t T, uint32_t* err) {
 // How the split kernel runs a call: row tiles of 8 nt rows, the grid, whether row tiles are
 // cut along the context, and the workspace that this takes.
 struct SplitChoice {
-  int nt, grid, whole;
+  int nt, grid, whole, prompt;
   int64_t bytes;
 };
 
 // The shortest run of 64-token tiles that is worth a CTA of its own: a cut costs the joining
 // kernel about as long as 512 tokens take one CTA.
 constexpr int kMinTiles = 8;
+
+// Query rows per sequence and kv head from which the tcgen05 kernel takes a call.
+constexpr int64_t kPromptFrom = 64;
+
+// The limit of each on-chip wait of the tcgen05 kernel.
+constexpr uint64_t kDecoderWaitNs = 1000000000ull;
 
 SplitChoice split_of(const b2b_cache* c, int32_t q_heads, int num_sms) {
   SplitChoice s;
@@ -125,7 +131,8 @@ SplitChoice split_of(const b2b_cache* c, int32_t q_heads, int num_sms) {
   s.grid = 2 * num_sms;
   const int64_t most = static_cast<int64_t>(c->max_pages) * c->page_size;
   s.whole = most <= kMinTiles * 64 ? 1 : 0;
-  s.bytes = s.whole ? 0
+  s.prompt = c->head_dim <= 128 && rows >= kPromptFrom ? 1 : 0;
+  s.bytes = s.whole || s.prompt ? 0
                     : 16 * ((static_cast<int64_t>(c->batch) + 2) / 2) +
                           static_cast<int64_t>(s.grid) * 2 * s.nt * 8 * (c->head_dim + 1) * 4;
   return s;
@@ -303,8 +310,9 @@ b2b_status b2b_cache_attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, 
   p.part = sc.whole ? nullptr
                     : reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                                16 * ((static_cast<int64_t>(cache->batch) + 2) / 2));
-  p.wait_limit_ns = 0;
+  p.wait_limit_ns = kDecoderWaitNs;
   auto s = static_cast<cudaStream_t>(stream);
+  if (sc.prompt) return launched(launch_prompt(p, s));
   cudaError_t e = cudaErrorInvalidValue;
   switch (cache->head_dim) {
     case 64: e = launch_attend_64(sc.nt, p, s); break;

@@ -20,7 +20,10 @@ def cache(**kw):
     a = dict(k=FAKE, v=FAKE, k_scale=FAKE, v_scale=FAKE, pages=10, heads=2, page_size=16,
              head_dim=64, batch=2, page_table=FAKE, max_pages=4, max_new=1, lens=FAKE, starts=None)
     a.update(kw)
-    return ops._Cache(*[a[n] for n, _ in ops._Cache._fields_])
+    values = [a[n] for n, _ in ops._Cache._fields_]
+    packed = ops._pack_cache(*[0 if x is None else x for x in values])
+    assert packed == bytes(ops._Cache(*values))              # the two forms of the struct agree
+    return packed
 
 
 def attend(L, c=None, dt=0, T=2, q=FAKE, ldq=256, q_heads=4, scale=0.1, cap=0.0, slopes=None,
@@ -43,7 +46,7 @@ CACHE_REFUSALS = [
 @pytest.mark.parametrize("kw,expect", CACHE_REFUSALS)
 def test_cache_refusals(L, kw, expect):
     c = cache(**kw)
-    assert attend(L, c, q_heads=4, ldq=4 * c.head_dim) == expect
+    assert attend(L, c, q_heads=4, ldq=4 * kw.get("head_dim", 64)) == expect
     assert L.b2b_cache_append(0, c, 2, FAKE, 2 * 512, FAKE, 2 * 512, None, 0, 0, 0, None, 0, 0, None,
                               0, None) == expect
 
@@ -127,10 +130,10 @@ def test_binding_refusals():
         ops.rotary(x, torch.zeros(4, 32, 2), torch.zeros(2, dtype=torch.int32))
     with pytest.raises(TypeError):
         ops.rotary(x.float(), torch.zeros(4, 32, 2), torch.zeros(2, dtype=torch.int32))
-    with pytest.raises(ValueError):
-        ops._rows(x.transpose(0, 1), "x", x.dtype, 2, 2, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        ops._rows(x, "x", x.dtype, (2, 2, 64), -1)
     with pytest.raises(ValueError, match="shape"):
-        ops._rows(x, "x", x.dtype, 2, 3, 64)
+        ops._rows(x, "x", x.dtype, (2, 3, 64), 0)
     with pytest.raises(ValueError, match="layout"):
         ops._layout("pairs")
     with pytest.raises(ValueError, match="scaling"):
@@ -140,5 +143,5 @@ def test_binding_refusals():
     k = torch.zeros(3, 2, 16, 64).to(torch.float8_e4m3fn)
     s = torch.zeros(3, 2)
     with pytest.raises(ValueError, match="CUDA"):
-        ops._cache_of(2, k, k, s, s, torch.zeros(2, 4, dtype=torch.int32),
+        ops._cache_of(2, 0, k, k, s, s, torch.zeros(2, 4, dtype=torch.int32),
                       torch.zeros(2, dtype=torch.int32), None, None)
