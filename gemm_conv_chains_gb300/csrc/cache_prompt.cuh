@@ -8,8 +8,9 @@
 // turned into fp16 once for all of them, and walks the keys in tiles of 128:
 //
 //   warps 0-3, 4-7   softmax of row tile A, B (one row per thread); stage Q, write the output
-//   warps 8-11       producers: e4m3 pages -> fp16 K and V tiles, 128B-swizzled, two of each
-//   warp 12          TMEM, MMA issue:  S = Q K^T,  O += P V
+//   warps 8-11       keys:   e4m3 pages -> fp16 tiles, 128B-swizzled, two of them; the scales
+//   warps 12-15      values: the same
+//   warp 16          TMEM, MMA issue:  S = Q K^T,  O += P V   (17-19 only complete its warpgroup)
 //
 // TMEM: S and O of both row tiles (4 x 128 columns); P (fp16 pairs) lies over the first half of
 // its S.  The two row tiles alternate: while one is in its softmax the tensor core works on the
@@ -22,13 +23,18 @@
 // moves when it is exceeded by 2^8, and O, in TMEM, is rescaled only then.
 #pragma once
 
+#include <type_traits>
+
 #include "decoder_device.cuh"
 
 namespace b2b {
 
 constexpr int kPromptRows = 256;       // query rows of a CTA: two M = 128 tiles
 constexpr int kPromptKeys = 128;       // keys per tile
-constexpr int kPromptThreads = 13 * 32;
+constexpr int kPromptThreads = 640;
+// Registers per thread of the softmax, producer and MMA warpgroups: 2 x 152 + 2 x 72 + 32 <= 5 x 96,
+// what 640 threads are launched with.
+constexpr int kSoftmaxRegs = 152, kProducerRegs = 72, kIssueRegs = 32;
 constexpr int kGranule = 16;           // tokens that surely share a page
 constexpr int kGranules = kPromptKeys / kGranule;
 // The region in which some rows of a CTA see a token and others do not: at most 256 tokens,
@@ -103,6 +109,42 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two fp32 lanes per instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// A page's value scale relative to the reference (log2), not below 2^-60: a scale of zero stands
+// for that (its codes' share vanishes, the row's sum does not); a NaN stays one.
+__device__ __forceinline__ float low_of(float lv) { return lv < -60.f ? -60.f : lv; }
+
 // What a CTA works on: up to 256 query rows of one sequence and kv head.
 struct PromptUnit {
   Sequence s;
@@ -135,51 +177,63 @@ __device__ __forceinline__ bool prompt_unit(const AttendParams& p, int units_per
 // ------------------------------------------------------------------------------------
 template <int D>
 struct PromptProducer {
-  static constexpr int kPieces = D / 16;          // 16-byte runs of codes per token
-  static constexpr int kEach = 128 * kPieces / 128;
-  int64_t off[kEach];                             // byte offset of this thread's runs, -1: none
+  static constexpr int kPieces = D / 16;              // 16-byte runs of codes per token
+  static constexpr int kLanes = kPieces > 4 ? 8 : 4;  // threads per token
+  static constexpr int kTokens = 128 / kLanes;        // tokens of the warpgroup's one load
+  static constexpr int kEach = kLanes;                // loads per thread and tile
+  int page[kEach];                                    // page numbers of the next tile's runs
+  uint32_t tid;
 
-  __device__ __forceinline__ void locate(const AttendParams& p, const PromptUnit& u, int tile,
-                                         int tid) {
+  // The thread's run in load j: token j kTokens + tid / kLanes, of which the 16-token granule (and
+  // so the page) is the same for the whole load, or half of it.
+  __device__ __forceinline__ int token(int j) const { return j * kTokens + tid / kLanes; }
+  __device__ __forceinline__ uint32_t piece() const { return tid % kLanes; }
+
+  // Reads the page numbers of a tile (used a tile later, so that nothing waits for them).
+  __device__ __forceinline__ void locate(const AttendParams& p, const PromptUnit& u, int tile) {
     const CacheView& c = p.c;
+    const int32_t* pages = c.page_table + static_cast<int64_t>(u.b) * c.max_pages;
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
-      const int run = j * 128 + tid, token = run / kPieces, piece = run % kPieces;
-      const int at = tile * kPromptKeys + token;
-      off[j] = -1;
-      if (at < u.kv_end) {
-        int id = __ldg(c.page_table + static_cast<int64_t>(u.b) * c.max_pages + (at >> c.page_shift));
-        if (id < 0 || id >= c.pages) id = 0;      // recorded, and its scales made NaN, below
-        off[j] = (((static_cast<int64_t>(id) * c.heads + u.h) << c.page_shift) +
-                  (at & ((1 << c.page_shift) - 1))) * D + 16 * piece;
-      }
+      const int at = tile * kPromptKeys + token(j);
+      page[j] = at < u.kv_end ? __ldg(pages + (at >> c.page_shift)) : -1;
     }
   }
-  __device__ __forceinline__ void fetch(const uint8_t* pool, uint4 (&raw)[kEach]) const {
-#pragma unroll
-    for (int j = 0; j < kEach; ++j)
-      raw[j] = off[j] >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool + off[j]))
-                           : make_uint4(0u, 0u, 0u, 0u);
-  }
-  static __device__ __forceinline__ void store(const uint4 (&raw)[kEach], uint32_t tile_at, int tid) {
+  // Starts the loads of this thread's runs of the located tile.
+  __device__ __forceinline__ void fetch(const AttendParams& p, const PromptUnit& u, int tile,
+                                        const uint8_t* pool, uint4 (&raw)[kEach]) const {
+    const CacheView& c = p.c;
+    const int mask = (1 << c.page_shift) - 1;
+    const int64_t page_bytes = (static_cast<int64_t>(c.heads) << c.page_shift) * D;
+    const uint8_t* head = pool + ((static_cast<int64_t>(u.h) << c.page_shift) * D) + 16 * piece();
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
-      const int run = j * 128 + tid, token = run / kPieces, piece = run % kPieces;
-      uint32_t h[8];
-      e4m3x4_to_f16(raw[j].x, h[0], h[1]);
-      e4m3x4_to_f16(raw[j].y, h[2], h[3]);
-      e4m3x4_to_f16(raw[j].z, h[4], h[5]);
-      e4m3x4_to_f16(raw[j].w, h[6], h[7]);
-      // the two 16-byte units of the run; pieces of the second 64 channels store theirs in the
-      // other order, so that the eight lanes of a token fill eight different units of a row
-      const uint32_t row = tile_at + (piece / 4) * 16384 + token * 128;
-      const uint32_t unit = (piece % 4) * 2, sw = token & 7;
-      const bool flip = piece >= 4;
-      const uint32_t a0 = row + ((unit ^ sw) << 4), a1 = row + (((unit + 1) ^ sw) << 4);
-      st_shared16(flip ? a1 : a0, flip ? h[4] : h[0], flip ? h[5] : h[1], flip ? h[6] : h[2],
-                  flip ? h[7] : h[3]);
-      st_shared16(flip ? a0 : a1, flip ? h[0] : h[4], flip ? h[1] : h[5], flip ? h[2] : h[6],
-                  flip ? h[3] : h[7]);
+      // a number outside the pool (-1: past the end) loads zeros; it is recorded with the scales,
+      // which become NaN
+      const int slot = (tile * kPromptKeys + token(j)) & mask;
+      raw[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (static_cast<uint32_t>(page[j]) < static_cast<uint32_t>(c.pages) && piece() < kPieces)
+        raw[j] = __ldg(reinterpret_cast<const uint4*>(head + page[j] * page_bytes + slot * D));
+    }
+  }
+  // A run is two 16-byte units of a row.  Runs of the second 64 channels store theirs in the other
+  // order, so that the eight lanes of a token fill eight different units at a time.
+  __device__ __forceinline__ void store(const uint4 (&raw)[kEach], uint32_t tile_at) const {
+    const bool flip = piece() >= 4;
+    const uint32_t unit = ((piece() % 4) * 2 + (flip ? 1 : 0)) ^ (token(0) & 7);
+    const uint32_t row = tile_at + (piece() / 4) * 16384 + token(0) * 128;
+    if (piece() >= kPieces) return;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const uint32_t w0 = flip ? raw[j].z : raw[j].x, w1 = flip ? raw[j].w : raw[j].y;
+      const uint32_t w2 = flip ? raw[j].x : raw[j].z, w3 = flip ? raw[j].y : raw[j].w;
+      uint32_t h[4];
+      e4m3x4_to_f16(w0, h[0], h[1]);
+      e4m3x4_to_f16(w1, h[2], h[3]);
+      st_shared16(row + j * (kTokens * 128) + (unit << 4), h[0], h[1], h[2], h[3]);
+      e4m3x4_to_f16(w2, h[0], h[1]);
+      e4m3x4_to_f16(w3, h[2], h[3]);
+      st_shared16(row + j * (kTokens * 128) + ((unit ^ 1u) << 4), h[0], h[1], h[2], h[3]);
     }
   }
 };
@@ -216,7 +270,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
     fence_barrier_init();
   }
   for (int i = threadIdx.x; i < kEdgeTokens * (D / 32); i += kPromptThreads) nan_bits[i] = 0u;
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(smem_u32(&bars->tmem), 512);
     tmem_relinquish();
   }
@@ -234,6 +288,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
   const int edge0 = (u.start + u.row0 / p.group + 1) / kPromptKeys * kPromptKeys;
 
   if (warp < 8) {
+    more_registers<kSoftmaxRegs>();
     // ================= softmax =================
     const int t = warp >> 2;
     const int row = u.row0 + 128 * t + (threadIdx.x & 127);
@@ -296,7 +351,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       const int low_limit = u.start + (u.row0 + 128 * t) / p.group;
       const float slope = MODS && p.slopes != nullptr && valid ? __ldg(p.slopes + head) : 0.f;
       const float cap2 = MODS && p.softcap > 0.f ? 2.f * 1.4426950408889634f / p.softcap : 0.f;
-      float m = -1e30f, l = 0.f, vref = 0.f, lvref = 0.f;
+      float m = -1e30f, l = 0.f, lvref = -1e30f;
       bool ok = true;
 
       for (int i = 0; i < u.tiles && ok; ++i) {
@@ -306,6 +361,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
         ok = wait(&bars->sfull[t], i & 1, PS_SFULL);
         if (!ok) break;
         tc_fence_after_sync();
+        auto tile = [&](auto scores) {
+        constexpr bool SCORES = decltype(scores)::value;
         // a score in the log2 domain
         auto score = [&](uint32_t raw, float f, int tok) -> float {
           float z = __uint_as_float(raw) * f;
@@ -319,10 +376,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
           }
           return z;
         };
-        // ---- pass 1: the tile's largest score ----
+        // ---- the tile's largest score; capped, biased or masked scores go back to TMEM ----
         uint32_t r[32];
-        float top = -INFINITY, vtop = 0.f;
-#pragma unroll
+        float top = -INFINITY, lvtop = -INFINITY;
+#pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           tmem_load32(tm + s_col + 32 * q, r);
           tmem_wait32(r);
@@ -330,22 +387,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
           for (int g = 0; g < 2; ++g) {
             const float2 s2 = sc[2 * q + g];
             const float f = fac * s2.x;
-            vtop = fmaxf(vtop, s2.y);
-            if (MODS || edge) {
+            lvtop = fmaxf(lvtop, s2.y);
+            uint32_t* x = &r[16 * g];
+            if constexpr (SCORES) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const int tok = tok0 + 32 * q + 16 * g + e;
-                const float z = score(r[16 * g + e], f, tok);
-                top = fmaxf(top, tok > limit ? -INFINITY : z);
+                const float z = tok > limit ? -INFINITY : score(x[e], f, tok);
+                x[e] = __float_as_uint(z);
+                top = fmaxf(top, z);
               }
             } else {
-              float raw_top = -INFINITY;
+              float a = __uint_as_float(x[0]);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) raw_top = fmaxf(raw_top, __uint_as_float(r[16 * g + e]));
-              top = fmaxf(top, raw_top * f);
+              for (int e = 1; e + 1 < 16; e += 2)
+                a = max3(a, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+              top = fmaxf(top, fmaxf(a, __uint_as_float(x[15])) * f);
             }
           }
+          if constexpr (SCORES) tmem_st32(tm + s_col + 32 * q, r);
         }
+        if constexpr (SCORES) tmem_wait_st();
         // ---- the references, and what O has to be scaled by for them ----
         float f = 1.f;
         if (top > m + 8.f) {
@@ -353,11 +415,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
           m = top;
           l *= f;
         }
-        if (vtop > vref) {
-          const float now = __uint_as_float((__float_as_uint(vtop) & 0x7F800000u) + 0x00800000u);
-          f *= vref / now;
-          vref = now;
-          lvref = log2f(now);
+        if (lvtop > lvref) {
+          const float now = floorf(lvtop) + 1.f;
+          f *= ex2(lvref - now);
+          lvref = now;
         }
         if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
@@ -369,8 +430,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
             tmem_st32(tm + o_col + 32 * q, r);
           }
         }
-        // ---- pass 2: P, and the row's sum ----
-#pragma unroll
+        // ---- P, and the row's sum ----
+#pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           tmem_load32(tm + s_col + 32 * q, r);
           tmem_wait32(r);
@@ -378,30 +439,69 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             const float2 s2 = sc[2 * q + g];
-            const float fg = fac * s2.x;
-            // log2 of the page's value scale relative to vref; 2^-60 stands for zero (its codes'
-            // share vanishes, the row's sum does not)
-            float lv = log2f(s2.y) - lvref;
-            if (lv < -60.f) lv = -60.f;
+            const float fg = SCORES ? 1.f : fac * s2.x;
+            const float lv = low_of(s2.y - lvref);
             const float back = ex2(-lv), c = lv - m;
-            float sum = 0.f;
+            const float2 f2 = make_float2(fg, fg), c2 = make_float2(c, c);
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              float y[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int tok = tok0 + 32 * q + 16 * g + e + k;
-                if (MODS) y[k] = score(r[16 * g + e + k], fg, tok) + c;
-                else y[k] = fmaf(__uint_as_float(r[16 * g + e + k]), fg, c);
-                if (edge && tok > limit) y[k] = -INFINITY;
-                y[k] = ex2(y[k]);
-              }
-              sum += y[0] + y[1];
-              pk[8 * g + e / 2] = narrow2<false>(y[0], y[1]);
+              float2 y = fma2(make_float2(__uint_as_float(r[16 * g + e]),
+                                          __uint_as_float(r[16 * g + e + 1])), f2, c2);
+              y.x = ex2(y.x);
+              y.y = ex2(y.y);
+              sum = add2(sum, y);
+              pk[8 * g + e / 2] = narrow2<false>(y.x, y.y);
             }
-            l = fmaf(sum, back, l);
+            l = fmaf(sum.x + sum.y, back, l);
           }
           tmem_store16(tm + s_col + 16 * q, pk);
+        }
+        };
+        // Inner tiles of a plain softmax take one pass with the references as they are: P and the
+        // sums are formed while the columns arrive, and only if some exponent turns out above 8
+        // (or a value scale above its reference) is the tile done again in two passes.
+        bool done = false;
+        if (!MODS && !edge) {
+          float lvtop = sc[0].y;
+#pragma unroll
+          for (int g = 1; g < kGranules; ++g) lvtop = fmaxf(lvtop, sc[g].y);
+          if (lvtop <= lvref) {
+            uint32_t r[2][16], pk[4][16];
+            float high = -INFINITY, more = 0.f;
+            tmem_ld16(tm + s_col, r[0]);
+#pragma unroll
+            for (int g = 0; g < kGranules; ++g) {
+              tmem_wait_ld(r[g & 1]);
+              if (g + 1 < kGranules) tmem_ld16(tm + s_col + 16 * (g + 1), r[(g + 1) & 1]);
+              const float2 s2 = sc[g];
+              const float fg = fac * s2.x, lv = low_of(s2.y - lvref);
+              const float back = ex2(-lv), c = lv - m;
+              const float2 f2 = make_float2(fg, fg), c2 = make_float2(c, c);
+              float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                const uint32_t* x = &r[g & 1][e];
+                float2 y = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), f2, c2);
+                high = max3(high, y.x, y.y);
+                y.x = ex2(y.x);
+                y.y = ex2(y.y);
+                sum = add2(sum, y);
+                pk[g / 2][8 * (g & 1) + e / 2] = narrow2<false>(y.x, y.y);
+              }
+              more = fmaf(sum.x + sum.y, back, more);
+            }
+            if (!__any_sync(0xffffffffu, high > 8.f)) {
+              l += more;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) tmem_store16(tm + s_col + 16 * q, pk[q]);
+              done = true;
+            }
+          }
+        }
+        if (!done) {
+          if (MODS || edge) tile(std::true_type{});
+          else tile(std::false_type{});
         }
         tmem_wait_st();
         tc_fence_before_sync();
@@ -412,7 +512,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       // ---- the output row ----
       if (ok && wait(&bars->ofull[t], 0, PS_OFULL)) {
         tc_fence_after_sync();
-        const float inv = l == 0.f ? 0.f : vref / l;
+        const float inv = l == 0.f ? 0.f : ex2(lvref) / l;
         const int tq_out = valid ? tq : 0;
         uint16_t* dst = p.out + ((u.s.row + static_cast<int64_t>(tq_out)) * p.q_heads + head) * D;
         const bool nans = bars->nan_any != 0u;
@@ -441,45 +541,62 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       }
     }
   } else if (warp < 12) {
-    // ================= producers =================
-    const int tid = threadIdx.x - 256;
+    fewer_registers<kProducerRegs>();
+    // ================= keys, and the scales of both pools =================
     PromptProducer<D> prod;
-    constexpr int kEach = PromptProducer<D>::kEach;
-    uint4 raw_k[kEach], raw_v[kEach];
-    prod.locate(p, u, 0, tid);
-    prod.fetch(p.c.k, raw_k);
-    prod.fetch(p.c.v, raw_v);
+    prod.tid = threadIdx.x - 256;
+    uint4 raw[PromptProducer<D>::kEach];
+    // thread g < kGranules: the scales of granule g, its page number read a tile ahead
+    const int32_t* pages = p.c.page_table + static_cast<int64_t>(u.b) * p.c.max_pages;
+    const int granule = static_cast<int>(prod.tid) * kGranule;
+    auto scale_page = [&](int tile) -> int {
+      const int at = tile * kPromptKeys + granule;
+      return prod.tid < kGranules && at < u.kv_end ? __ldg(pages + (at >> p.c.page_shift)) : -1;
+    };
+    auto scales_of = [&](int tile, int id) -> float2 {
+      if (prod.tid >= kGranules || tile * kPromptKeys + granule >= u.kv_end) return make_float2(0.f, 0.f);
+      if (id < 0 || id >= p.c.pages) {
+        index_error(p.c.err, DK_PROMPT, DEC_ERR_PAGE, static_cast<uint32_t>(u.b));
+        return make_float2(__uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u));
+      }
+      const int64_t at = static_cast<int64_t>(id) * p.c.heads + u.h;
+      return make_float2(__ldg(p.c.k_scale + at), __ldg(p.c.v_scale + at));
+    };
+    prod.locate(p, u, 0);
+    prod.fetch(p, u, 0, p.c.k, raw);
+    float2 s2 = scales_of(0, scale_page(0));
+    prod.locate(p, u, 1);
+    int next_id = scale_page(1);
     bool ok = true;
     for (int i = 0; i < u.tiles && ok; ++i) {
       const int slot = i & 1;
-      // ---- K, and the tile's scales ----
       if (i >= 2) ok = wait(&bars->kempty[slot], ((i >> 1) - 1) & 1, PS_KEMPTY);
       if (!ok) break;
-      PromptProducer<D>::store(raw_k, base + L::kK + slot * L::kTile, tid);
-      if (tid < kGranules) {
-        const int at = i * kPromptKeys + tid * kGranule;
-        float2 s2 = make_float2(0.f, 0.f);
-        if (at < u.kv_end) {
-          const int id = __ldg(p.c.page_table + static_cast<int64_t>(u.b) * p.c.max_pages +
-                               (at >> p.c.page_shift));
-          if (id < 0 || id >= p.c.pages) {
-            index_error(p.c.err, DK_PROMPT, DEC_ERR_PAGE, static_cast<uint32_t>(u.b));
-            s2.x = s2.y = __uint_as_float(0x7FC00000u);
-          } else {
-            const int64_t sa = static_cast<int64_t>(id) * p.c.heads + u.h;
-            s2 = make_float2(__ldg(p.c.k_scale + sa), __ldg(p.c.v_scale + sa));
-          }
-        }
-        scales[(i & 3) * kGranules + tid] = s2;
-      }
+      prod.store(raw, base + L::kK + slot * L::kTile);
+      if (prod.tid < kGranules) scales[(i & 3) * kGranules + prod.tid] = make_float2(s2.x, log2f(s2.y));
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->kfull[slot]));
       if (i + 1 < u.tiles) {
-        prod.locate(p, u, i + 1, tid);
-        prod.fetch(p.c.k, raw_k);
+        prod.fetch(p, u, i + 1, p.c.k, raw);
+        s2 = scales_of(i + 1, next_id);
+        prod.locate(p, u, i + 2);
+        next_id = scale_page(i + 2);
       }
-      // ---- V ----
+    }
+  } else if (warp < 16) {
+    fewer_registers<kProducerRegs>();
+    // ================= values =================
+    PromptProducer<D> prod;
+    prod.tid = threadIdx.x - 384;
+    constexpr int kEach = PromptProducer<D>::kEach;
+    uint4 raw[kEach];
+    prod.locate(p, u, 0);
+    prod.fetch(p, u, 0, p.c.v, raw);
+    prod.locate(p, u, 1);
+    bool ok = true;
+    for (int i = 0; i < u.tiles && ok; ++i) {
+      const int slot = i & 1;
       if (i >= 2) ok = wait(&bars->vempty[slot], ((i >> 1) - 1) & 1, PS_VEMPTY);
       if (!ok) break;
       if (i * kPromptKeys >= edge0) {
@@ -487,12 +604,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
         // that do see it
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
-          uint32_t w[4] = {raw_v[j].x, raw_v[j].y, raw_v[j].z, raw_v[j].w};
+          uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
           uint32_t any = 0u;
 #pragma unroll
           for (int e = 0; e < 4; ++e) any |= ((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
           if (any != 0u) {
-            const int run = j * 128 + tid, token = run / (D / 16), piece = run % (D / 16);
             uint32_t bits = 0u;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
@@ -500,22 +616,34 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
                 bits |= 1u << e;
                 w[e / 4] &= ~(0xFFu << (8 * (e % 4)));
               }
-            raw_v[j] = make_uint4(w[0], w[1], w[2], w[3]);
-            const int at = i * kPromptKeys + token - edge0;
-            if (at < kEdgeTokens)
-              atomicOr(&nan_bits[at * (D / 32) + piece / 2], bits << (16 * (piece & 1)));
-            bars->nan_any = 1u;
+            raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            const int at = i * kPromptKeys + prod.token(j);
+            // what lies past every row's reach is dropped with it
+            if (at < u.kv_end && at - edge0 < kEdgeTokens) {
+              atomicOr(&nan_bits[(at - edge0) * (D / 32) + prod.piece() / 2],
+                       bits << (16 * (prod.piece() & 1)));
+              bars->nan_any = 1u;
+            }
           }
         }
       }
-      PromptProducer<D>::store(raw_v, base + L::kV + slot * L::kTile, tid);
+      prod.store(raw, base + L::kV + slot * L::kTile);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->vfull[slot]));
-      if (i + 1 < u.tiles) prod.fetch(p.c.v, raw_v);
+      if (i + 1 < u.tiles) {
+        prod.fetch(p, u, i + 1, p.c.v, raw);
+        prod.locate(p, u, i + 2);
+      }
     }
   } else {
+    fewer_registers<kIssueRegs>();
+  }
+  if (warp == 16) {
     // ================= MMA =================
+    // One issuer for both row tiles: P V and the next Q K^T of a tile stay together in the tensor
+    // core's queue, which keeps the two tiles' softmaxes out of step (two issuers mix the tiles'
+    // products, and both tiles then wait for both).
     const uint32_t lead = elect_one();
     const uint32_t idesc_s = idesc_f16_f32(0u, 0u, 128, kPromptKeys);
     const uint32_t idesc_o = idesc_f16_f32(0u, 1u, 128, D);
@@ -544,9 +672,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       const int slot = i & 1, next = slot ^ 1;
       const bool more = i + 1 < u.tiles;
       ok = wait(&bars->vfull[slot], (i >> 1) & 1, PS_VFULL);
+      if (ok && more) ok = wait(&bars->kfull[next], ((i + 1) >> 1) & 1, PS_KFULL);
       for (int t = 0; t < u.row_tiles && ok; ++t) {
         ok = wait(&bars->pready[t], i & 1, PS_PREADY);
-        if (ok && t == 0 && more) ok = wait(&bars->kfull[next], ((i + 1) >> 1) & 1, PS_KFULL);
         if (!ok) break;
         tc_fence_after_sync();
 #pragma unroll
@@ -568,7 +696,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
