@@ -151,18 +151,15 @@ struct PromptUnit {
   int b, h, row0, rows, start, kv_end, tiles, row_tiles;
 };
 
-template <int D>
-__device__ __forceinline__ bool prompt_unit(const AttendParams& p, int units_per_head,
+// Row tile rt of sequence b, for kv head h; false where the sequence has no such rows.
+__device__ __forceinline__ bool prompt_unit(const AttendParams& p, int b, int h, int rt,
                                             PromptUnit& u) {
-  // the last row tiles see the most keys: they start first
-  int x = static_cast<int>(blockIdx.x);
-  const int rt = units_per_head - 1 - x / (p.c.heads * p.c.B);
-  x %= p.c.heads * p.c.B;
-  u.h = x % p.c.heads;
-  u.b = x / p.c.heads;
-  u.s = load_sequence(p.c, u.b, DK_PROMPT);
+  u.h = h;
+  u.b = b;
+  u.s = load_sequence(p.c, b, DK_PROMPT);
   u.row0 = rt * kPromptRows;
   u.rows = u.s.n * p.group;
+  u.tiles = 0;
   if (u.row0 >= u.rows) return false;
   const int last = u.row0 + kPromptRows < u.rows ? u.row0 + kPromptRows - 1 : u.rows - 1;
   u.start = u.s.len - u.s.n;
@@ -170,6 +167,20 @@ __device__ __forceinline__ bool prompt_unit(const AttendParams& p, int units_per
   u.tiles = (u.kv_end + kPromptKeys - 1) / kPromptKeys;
   u.row_tiles = u.rows - u.row0 > 128 ? 2 : 1;
   return true;
+}
+
+// The (sequence, row tile) pair that a CTA works on.  CTAs start in the order of their numbers, and
+// the most key tiles should start first.  Within a sequence that is the last row tile; over ragged
+// sequences, while there are few pairs (with many, the last ones to finish weigh little), a small
+// kernel ahead ranks the pairs by their key tiles.  (It is a kernel of its own because a pair read
+// from global memory is known to be the same for the whole CTA; ranked inside, every size of the
+// unit took a register per thread, and the spills cost more than the order gained.)
+constexpr int kRankedPairs = 256;
+
+__device__ __forceinline__ void plain_pair(const AttendParams& p, int row_tiles, int order, int& b,
+                                           int& rt) {
+  b = order % p.c.B;
+  rt = row_tiles - 1 - order / p.c.B;
 }
 
 // ------------------------------------------------------------------------------------
@@ -240,7 +251,7 @@ struct PromptProducer {
 
 template <int D, bool MODS>
 __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendParams p,
-                                                                   int units_per_head) {
+                                                                   int row_tiles) {
   using L = PromptSmem<D>;
   extern __shared__ uint8_t raw_smem[];
   const uint32_t base = (smem_u32(raw_smem) + 1023u) & ~1023u;
@@ -251,7 +262,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   PromptUnit u;
-  if (!prompt_unit<D>(p, units_per_head, u)) return;       // the whole CTA
+  {
+    int b, rt;
+    int order = static_cast<int>(blockIdx.x) / p.c.heads;
+    if (p.meta != nullptr) {
+      grid_dependency_wait();
+      order = __ldg(reinterpret_cast<const int*>(p.meta) + order);
+    }
+    plain_pair(p, row_tiles, order, b, rt);
+    if (!prompt_unit(p, b, static_cast<int>(blockIdx.x) % p.c.heads, rt, u)) return;   // the whole CTA
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -703,7 +723,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
 }
 
 template <int D>
-cudaError_t launch_prompt_d(const AttendParams& p, cudaStream_t s) {
+cudaError_t launch_prompt_d(const AttendParams& p, int row_tiles, cudaStream_t s) {
   constexpr int smem = PromptSmem<D>::kAlloc;
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
   const bool mods = p.softcap > 0.f || p.slopes != nullptr;
@@ -717,12 +737,17 @@ cudaError_t launch_prompt_d(const AttendParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     set_on[mods] = dev;
   }
-  const int64_t rows = static_cast<int64_t>(p.c.max_new) * p.group;
-  const int64_t units = (rows + kPromptRows - 1) / kPromptRows;
-  const int64_t blocks = units * p.c.heads * p.c.B;
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  fn<<<static_cast<unsigned>(blocks), kPromptThreads, smem, s>>>(p, static_cast<int>(units));
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(row_tiles * p.c.heads * p.c.B));
+  cfg.blockDim = dim3(kPromptThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.meta != nullptr ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, fn, p, row_tiles);
 }
 
 }  // namespace b2b

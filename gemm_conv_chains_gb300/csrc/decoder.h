@@ -85,6 +85,8 @@ cudaError_t launch_attend_192(int nt, const AttendParams& p, cudaStream_t s);
 cudaError_t launch_attend_256(int nt, const AttendParams& p, cudaStream_t s);
 // The tcgen05 kernel for prompts (head sizes 64, 96, 128).
 cudaError_t launch_prompt(const AttendParams& p, cudaStream_t s);
+// Bytes of workspace that it takes for `rows` query rows per sequence and kv head (p.meta).
+int64_t prompt_workspace(int64_t rows, int32_t B);
 cudaError_t launch_attend_combine(const AttendParams& p, int nt, int threads, cudaStream_t s);
 
 }  // namespace b2b

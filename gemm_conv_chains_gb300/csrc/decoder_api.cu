@@ -132,7 +132,8 @@ SplitChoice split_of(const b2b_cache* c, int32_t q_heads, int num_sms) {
   const int64_t most = static_cast<int64_t>(c->max_pages) * c->page_size;
   s.whole = most <= kMinTiles * 64 ? 1 : 0;
   s.prompt = c->head_dim <= 128 && rows >= kPromptFrom ? 1 : 0;
-  s.bytes = s.whole || s.prompt ? 0
+  s.bytes = s.prompt  ? prompt_workspace(rows, c->batch)
+            : s.whole ? 0
                     : 16 * ((static_cast<int64_t>(c->batch) + 2) / 2) +
                           static_cast<int64_t>(s.grid) * 2 * s.nt * 8 * (c->head_dim + 1) * 4;
   return s;
@@ -306,8 +307,8 @@ b2b_status b2b_cache_attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, 
   p.grid = sc.grid;
   p.min_tiles = kMinTiles;
   p.whole = sc.whole;
-  p.meta = sc.whole ? nullptr : static_cast<int64_t*>(workspace);
-  p.part = sc.whole ? nullptr
+  p.meta = sc.bytes == 0 ? nullptr : static_cast<int64_t*>(workspace);
+  p.part = sc.bytes == 0 || sc.prompt ? nullptr
                     : reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                                16 * ((static_cast<int64_t>(cache->batch) + 2) / 2));
   p.wait_limit_ns = kDecoderWaitNs;
