@@ -52,7 +52,7 @@ __device__ __forceinline__ float rcp_fast(float x) {
 
 __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                              uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -60,7 +60,7 @@ __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], const uint32_t (&a)[
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 
@@ -79,16 +79,16 @@ __device__ __forceinline__ void copy_wait() {
 }
 
 template <int BYTES>
-__device__ __forceinline__ void load_words(uint32_t addr, uint32_t* w) {
-  if constexpr (BYTES == 16)
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(addr)
-                 : "memory");
-  else if constexpr (BYTES == 8)
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
-  else
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+__device__ __forceinline__ void load_words(const uint8_t* src, uint32_t* w) {
+  if constexpr (BYTES == 16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(src);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (BYTES == 8) {
+    const uint2 v = *reinterpret_cast<const uint2*>(src);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(src);
+  }
 }
 
 // A query row's fp16 form: bf16 rows are divided by the power of two of their largest
@@ -102,7 +102,7 @@ __device__ __forceinline__ float row_unit_of(float amax, bool bf16, float& inv) 
   return __uint_as_float(e << 23);
 }
 
-template <int D_>
+template <int D_, int NT>
 struct CacheDims {
   static constexpr int D = D_;
   static constexpr int kKBytes = D / 4;                                   // per lane and token
@@ -110,23 +110,25 @@ struct CacheDims {
   static constexpr int kKRun = kKBytes % 16 == 0 ? 16 : 8;                // bytes per copy
   static constexpr int kVRun = kVBytes % 16 == 0 ? 16 : kVBytes % 8 == 0 ? 8 : 4;
   static constexpr int kStage = kStrip * 2 * D;                           // bytes per warp
-  // about 96 KB per CTA, two CTAs per SM: ~160 KB in flight, several times what the HBM
-  // latency asks for
-  static constexpr int kStages = D <= 64 ? 8 : D <= 96 ? 7 : D <= 128 ? 6 : D <= 192 ? 4 : 3;
+  // what fits the CTAs per SM (64 or 96 KB of ring each): ~150 KB in flight per SM, several times
+  // what the HBM latency asks for
+  static constexpr int kCtas = attend_ctas_per_sm(D, NT);
+  static constexpr int kStages =
+      kCtas == 3 ? (D <= 64 ? 8 : D <= 96 ? 5 : 4) : (D <= 64 ? 8 : D <= 96 ? 7 : D <= 128 ? 6 : D <= 192 ? 4 : 3);
   static constexpr int kRing = kStages * kStage;
 };
 
 template <int D, int NT>
 constexpr int attend_smem() {
-  constexpr int ring = kAttendWarps * CacheDims<D>::kRing;
+  constexpr int ring = kAttendWarps * CacheDims<D, NT>::kRing;
   constexpr int join = kAttendWarps * NT * 8 * (D + 2) * 4;
-  return (ring > join ? ring : join) + kAttendWarps * CacheDims<D>::kStages * 8 +
+  return (ring > join ? ring : join) + kAttendWarps * CacheDims<D, NT>::kStages * 8 +
          (NT > 1 ? D / 16 * NT * 256 : 0) + NT * 8 * 4;
 }
 
 template <int D, int NT, bool MODS>
-__global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_kernel(const AttendParams p) {
-  using C = CacheDims<D>;
+__global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) attend_kernel(const AttendParams p) {
+  using C = CacheDims<D, NT>;
   constexpr int RT = NT * 8;
   constexpr int KS = D / 16;           // k steps of S^T, m tiles of O^T
   extern __shared__ __align__(16) uint8_t smem[];
@@ -244,6 +246,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_kernel(const Atte
       sc = make_float2(__ldg(c.k_scale + at_scale), __ldg(c.v_scale + at_scale));
     };
     int issue_strip = strip, issue_n = 0;            // next strip to copy, and its count
+    int issue_stage = 0;
     int ids = fetch_page(strip), next_ids;
     float2 scs, next_scs = make_float2(0.f, 0.f);
     fetch_scales(ids, scs);
@@ -256,7 +259,8 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_kernel(const Atte
         const int id = __shfl_sync(0xffffffffu, ids, k);
         const float ks = __shfl_sync(0xffffffffu, scs.x, k);
         const float vs = __shfl_sync(0xffffffffu, scs.y, k);
-        const int stage = issue_n % C::kStages;
+        const int stage = issue_stage;
+        issue_stage = issue_stage + 1 == C::kStages ? 0 : issue_stage + 1;
         if (lane == 0) stage_scales[stage] = make_float2(ks, vs);
         const int slot0 = (issue_strip << 4) & ((1 << c.page_shift) - 1);
         const int64_t off = (static_cast<int64_t>(id) * c.heads + h) * head_bytes + slot0 * D;
@@ -378,17 +382,17 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_kernel(const Atte
     float vref = 0.f, vref_inv = 0.f;
 
     // ---- the strips ----
-    for (int n = 0; strip < strip_end; ++n, strip += kAttendWarps) {
+    for (int stage = 0; strip < strip_end; strip += kAttendWarps) {
       copy_wait<C::kStages - 2>();
       __syncwarp();
-      const int stage = n % C::kStages;
       const float2 sc = stage_scales[stage];
-      uint32_t src = ring_at + stage * C::kStage;
-      float x[NT][4];
+      const uint8_t* src = ring + stage * C::kStage;
+      stage = stage + 1 == C::kStages ? 0 : stage + 1;
+      float x[NT][4], x2[NT][4];           // even and odd k steps: two shorter chains of MMAs
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[nt][e] = 0.f;
+        for (int e = 0; e < 4; ++e) x[nt][e] = x2[nt][e] = 0.f;
       {
         uint32_t kw[2][C::kKBytes / 4];
 #pragma unroll
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_kernel(const Atte
             uint2 q;
             if constexpr (NT == 1) q = make_uint2(qf[u][0], qf[u][1]);
             else q = q_frags[(u * NT + nt) * 32 + lane];
-            mma_m16n8k16(x[nt], a, q.x, q.y);
+            mma_m16n8k16(u & 1 ? x2[nt] : x[nt], a, q.x, q.y);
           }
         }
       }
@@ -419,7 +423,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_kernel(const Atte
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float z = x[nt][e] * (qfactor[nt][e & 1] * sc.x);
+          float z = (x[nt][e] + x2[nt][e]) * (qfactor[nt][e & 1] * sc.x);
           if (MODS) {
             if (p.softcap > 0.f)                     // cap tanh(z / cap); tanh y = 1 - 2 / (e^2y + 1)
               z = p.softcap - 2.f * p.softcap *
@@ -637,7 +641,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_kernel(const Atte
 template <int D, int NT, bool MODS>
 cudaError_t launch_attend_one(const AttendParams& p, cudaStream_t s) {
   constexpr int smem = attend_smem<D, NT>();
-  static_assert(smem <= 113 * 1024, "two CTAs per SM");
+  static_assert(smem * attend_ctas_per_sm(D, NT) <= 226 * 1024, "CTAs per SM");
   auto* fn = attend_kernel<D, NT, MODS>;
   // per device: a process that moves between devices sets it again, which is harmless
   static thread_local int set_on = -1;

@@ -77,6 +77,11 @@ cudaError_t launch_rotary_table(float2* table, int64_t n, int32_t half, const do
                                 cudaStream_t s);
 cudaError_t launch_append(bool bf16, const AppendParams& p, cudaStream_t s);
 
+// CTAs of the split kernel that an SM holds at once: its registers decide (one row tile of 8 at
+// head sizes up to 128: 168 per thread).  More warps hide more of each strip's latencies.
+__host__ __device__ constexpr int attend_ctas_per_sm(int D, int nt) {
+  return nt == 1 && D <= 128 ? 3 : 2;
+}
 // The split kernel with row tiles of 8 nt query rows, per head size.
 cudaError_t launch_attend_64(int nt, const AttendParams& p, cudaStream_t s);
 cudaError_t launch_attend_96(int nt, const AttendParams& p, cudaStream_t s);

@@ -128,7 +128,7 @@ SplitChoice split_of(const b2b_cache* c, int32_t q_heads, int num_sms) {
   SplitChoice s;
   const int64_t rows = static_cast<int64_t>(c->max_new) * (q_heads / c->heads);
   s.nt = rows <= 8 ? 1 : rows <= 16 || c->head_dim > 128 ? 2 : 4;
-  s.grid = 2 * num_sms;
+  s.grid = attend_ctas_per_sm(c->head_dim, s.nt) * num_sms;
   const int64_t most = static_cast<int64_t>(c->max_pages) * c->page_size;
   s.whole = most <= kMinTiles * 64 ? 1 : 0;
   s.prompt = c->head_dim <= 128 && rows >= kPromptFrom ? 1 : 0;
