@@ -10,12 +10,14 @@
 //
 // The tokens are the M side of both products (S^T = K Q^T, O^T = V^T P^T) and the query rows
 // the N side, in tiles of 8, so that up to 8 rows (a usual group of query heads) waste nothing.
-// The order of the summed index is free as long as both operands share it, which removes every
-// transposition of 8-bit data: a lane loads 16-byte runs of the channels of its own fragment
-// rows (keys: tokens g and g + 8, channel run t; values: tokens 2t, 2t + 1, 2t + 8, 2t + 9,
-// channel run g; lane = 4 g + t), and only P^T crosses lanes (movmatrix).  So each lane reads
-// back exactly what it copied itself: the shared-memory ring needs no barrier, only the
-// lane's own cp.async groups.
+// The order of the summed index is free as long as both operands share it, and so are the orders
+// of tokens and channels, which removes every transposition of 8-bit data: a lane reads runs of
+// channels of its own fragment rows (lane = 4 g + t; keys: two tokens by g, channel run t;
+// values: four tokens by t, channel run by g), and only P^T crosses lanes (movmatrix).  A strip
+// is copied as it lies (whole 128-byte lines, each written to shared memory at once: lines
+// scattered to the lanes that want them took 20 shared-memory cycles per instruction instead of
+// 4, and bounded the kernel), its 16-byte units xor-ed so that the reads meet no bank twice.  A
+// warp's ring is its own: no block barrier, only cp.async groups and a warp barrier.
 //
 // Work is cut evenly: the tiles of 64 tokens of all (sequence, kv head, row tile) are numbered
 // in a row and each CTA takes an equal run of them, found from the lengths on the device; runs
@@ -64,13 +66,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
-template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
-                 : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -109,6 +106,27 @@ struct CacheDims {
   static constexpr int kVBytes = D / 8;
   static constexpr int kKRun = kKBytes % 16 == 0 ? 16 : 8;                // bytes per copy
   static constexpr int kVRun = kVBytes % 16 == 0 ? 16 : kVBytes % 8 == 0 ? 8 : 4;
+  // Fragment row r (0..7) holds token r, or with kSpread token (r & 1) * 4 + (r >> 1): then the four
+  // tokens that a lane's values come from are neighbours (t, t + 4, t + 8, t + 12).
+  static constexpr bool kSpread = D == 64 || D == 128 || D == 256;
+  static __device__ __forceinline__ int token_of_row(int r) {
+    return kSpread ? (r & 1) * 4 + (r >> 1) : r;
+  }
+  static __device__ __forceinline__ int value_token(int t, int i) {
+    return kSpread ? t + 4 * i : 2 * t + (i & 1) + 8 * (i >> 1);
+  }
+  // Run of channels that lane row g takes of a value row (the first of its runs).
+  static __device__ __forceinline__ int value_run(int g) {
+    return D == 128 || D == 256 ? (g & 1) * 4 + (g >> 1) : g;
+  }
+  // Byte offset of byte b of token `tok` in a strip: the 16-byte units of a 128-byte line change
+  // places by the token.
+  static __device__ __forceinline__ uint32_t at(int tok, int b) {
+    uint32_t o = tok * D + b;
+    if constexpr (D == 128 || D == 256) o ^= (tok & 7) << 4;
+    else if constexpr (D == 64) o ^= (((tok >> 2) & 1) << 6) ^ (((tok >> 1) & 1) << 5);
+    return o;
+  }
   static constexpr int kStage = kStrip * 2 * D;                           // bytes per warp
   // what fits the CTAs per SM (64 or 96 KB of ring each): ~150 KB in flight per SM, several times
   // what the HBM latency asks for
@@ -263,25 +281,16 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
         issue_stage = issue_stage + 1 == C::kStages ? 0 : issue_stage + 1;
         if (lane == 0) stage_scales[stage] = make_float2(ks, vs);
         const int slot0 = (issue_strip << 4) & ((1 << c.page_shift) - 1);
-        const int64_t off = (static_cast<int64_t>(id) * c.heads + h) * head_bytes + slot0 * D;
-        const uint8_t* kp = c.k + off;
-        const uint8_t* vp = c.v + off;
-        uint32_t dst = ring_at + stage * C::kStage;
+        const int64_t off =
+            (static_cast<int64_t>(id) * c.heads + h) * head_bytes + slot0 * D + 16 * lane;
+        const uint32_t dst = ring_at + stage * C::kStage;
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int j = 0; j < C::kKBytes / C::kKRun; ++j) {
-            copy_async<C::kKRun>(dst + lane * C::kKRun, kp + (g + 8 * half) * D + C::kKRun * (t + 4 * j));
-            dst += 32 * C::kKRun;
-          }
-#pragma unroll
-        for (int tok = 0; tok < 4; ++tok)
-#pragma unroll
-          for (int j = 0; j < C::kVBytes / C::kVRun; ++j) {
-            copy_async<C::kVRun>(dst + lane * C::kVRun,
-                                 vp + (2 * t + (tok & 1) + 8 * (tok >> 1)) * D + C::kVRun * (g + 8 * j));
-            dst += 32 * C::kVRun;
-          }
+        for (int i = 0; i < D / 32; ++i) {
+          const int unit = 32 * i + lane;
+          const uint32_t to = dst + C::at(unit / (D / 16), 16 * (unit % (D / 16)));
+          copy_async(to, c.k + off + 512 * i);
+          copy_async(to + kStrip * D, c.v + off + 512 * i);
+        }
         ++issue_n;
         issue_strip += kAttendWarps;
         if ((issue_n & 31) == 0) {                   // the prefetched 32 take over
@@ -398,10 +407,9 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int j = 0; j < C::kKBytes / C::kKRun; ++j) {
-            load_words<C::kKRun>(src + lane * C::kKRun, kw[half] + j * (C::kKRun / 4));
-            src += 32 * C::kKRun;
-          }
+          for (int j = 0; j < C::kKBytes / C::kKRun; ++j)
+            load_words<C::kKRun>(src + C::at(C::token_of_row(g) + 8 * half, C::kKRun * (t + 4 * j)),
+                                 kw[half] + j * (C::kKRun / 4));
 #pragma unroll
         for (int u = 0; u < KS; ++u) {
           uint32_t a[4];
@@ -416,7 +424,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
           }
         }
       }
-      const int tok0 = strip * kStrip + g;           // of x[.][0], x[.][1]; + 8: x[.][2], x[.][3]
+      const int tok0 = strip * kStrip + C::token_of_row(g);   // of x[.][0], x[.][1]; + 8: of x[.][2], x[.][3]
       const bool edge = strip * kStrip + kStrip - 1 > low_limit;
       // scores in the log2 domain
 #pragma unroll
@@ -491,10 +499,10 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
 #pragma unroll
       for (int tok = 0; tok < 4; ++tok)
 #pragma unroll
-        for (int j = 0; j < C::kVBytes / C::kVRun; ++j) {
-          load_words<C::kVRun>(src + lane * C::kVRun, vw[tok] + j * (C::kVRun / 4));
-          src += 32 * C::kVRun;
-        }
+        for (int j = 0; j < C::kVBytes / C::kVRun; ++j)
+          load_words<C::kVRun>(src + kStrip * D + C::at(C::value_token(t, tok),
+                                                        C::kVRun * (C::value_run(g) + 8 * j)),
+                               vw[tok] + j * (C::kVRun / 4));
       auto value_tile = [&](int i, uint32_t (&a)[4]) {
         const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
         e4m3x4_to_f16(__byte_perm(vw[0][i / 2], vw[1][i / 2], sel), a[0], a[1]);
@@ -507,7 +515,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
         uint32_t nan = 0;
 #pragma unroll
         for (int tok = 0; tok < 4; ++tok) {
-          const int at_tok = strip * kStrip + 2 * t + (tok & 1) + 8 * (tok >> 1);
+          const int at_tok = strip * kStrip + C::value_token(t, tok);
 #pragma unroll
           for (int w = 0; w < C::kVBytes / 4; ++w) {
             if (at_tok > high_limit) vw[tok][w] = 0u;
@@ -578,7 +586,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
       const int w = i / 2;
-      const int d = C::kVRun * (g + 8 * (4 * w / C::kVRun)) + (4 * w) % C::kVRun + 2 * (i & 1);
+      const int d = C::kVRun * (C::value_run(g) + 8 * (4 * w / C::kVRun)) + (4 * w) % C::kVRun + 2 * (i & 1);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int r = 8 * nt + 2 * t;
