@@ -251,12 +251,11 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
       if (st >= strip_end) return -2;
       return __ldg(pages_of + (st >> page_strips_shift));
     };
-    auto fetch_scales = [&](int& id, float2& sc) {
+    auto fetch_scales = [&](int id, float2& sc) {
       sc = make_float2(0.f, 0.f);
       if (id == -2) return;
       if (id < 0 || id >= c.pages) {
         index_error(c.err, DK_ATTEND, DEC_ERR_PAGE, static_cast<uint32_t>(b));
-        id = 0;                          // in bounds; its NaN scale shows in the output
         sc = make_float2(__uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u));
         return;
       }
@@ -265,25 +264,19 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
     };
     int issue_strip = strip, issue_n = 0;            // next strip to copy, and its count
     int issue_stage = 0;
-    int ids = fetch_page(strip), next_ids;
-    float2 scs, next_scs = make_float2(0.f, 0.f);
-    fetch_scales(ids, scs);
-    next_ids = fetch_page(strip + 32 * kAttendWarps);
+    int ids = fetch_page(strip), next_ids = fetch_page(strip + 32 * kAttendWarps);
+    float2 scs = make_float2(0.f, 0.f), next_scs = scs;
 
     const int64_t head_bytes = static_cast<int64_t>(D) << c.page_shift;
-    auto issue = [&]() {
+    // The next strip's bytes, then (they are needed later, and come from another load) its scales.
+    auto issue_copy = [&]() {
       if (issue_strip < strip_end) {
-        const int k = issue_n & 31;
-        const int id = __shfl_sync(0xffffffffu, ids, k);
-        const float ks = __shfl_sync(0xffffffffu, scs.x, k);
-        const float vs = __shfl_sync(0xffffffffu, scs.y, k);
-        const int stage = issue_stage;
-        issue_stage = issue_stage + 1 == C::kStages ? 0 : issue_stage + 1;
-        if (lane == 0) stage_scales[stage] = make_float2(ks, vs);
+        int id = __shfl_sync(0xffffffffu, ids, issue_n & 31);
+        if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(c.pages)) id = 0;   // its scales are NaN
         const int slot0 = (issue_strip << 4) & ((1 << c.page_shift) - 1);
         const int64_t off =
             (static_cast<int64_t>(id) * c.heads + h) * head_bytes + slot0 * D + 16 * lane;
-        const uint32_t dst = ring_at + stage * C::kStage;
+        const uint32_t dst = ring_at + issue_stage * C::kStage;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           const int unit = 32 * i + lane;
@@ -291,18 +284,49 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
           copy_async(to, c.k + off + 512 * i);
           copy_async(to + kStrip * D, c.v + off + 512 * i);
         }
-        ++issue_n;
-        issue_strip += kAttendWarps;
-        if ((issue_n & 31) == 0) {                   // the prefetched 32 take over
-          ids = next_ids;
-          fetch_scales(ids, scs);
-          next_ids = fetch_page(issue_strip + 32 * kAttendWarps);
-        }
       }
       copy_commit();
     };
+    auto issue_scales = [&]() {
+      if (issue_strip < strip_end) {
+        const int k = issue_n & 31;
+        const float ks = __shfl_sync(0xffffffffu, scs.x, k);
+        const float vs = __shfl_sync(0xffffffffu, scs.y, k);
+        if (lane == 0) stage_scales[issue_stage] = make_float2(ks, vs);
+      }
+    };
+    auto advance = [&]() {
+      if (issue_strip >= strip_end) return;
+      issue_stage = issue_stage + 1 == C::kStages ? 0 : issue_stage + 1;
+      issue_strip += kAttendWarps;
+      ++issue_n;
+      if ((issue_n & 31) == 16) {
+        fetch_scales(next_ids, next_scs);
+      } else if ((issue_n & 31) == 0) {              // the prefetched 32 take over
+        ids = next_ids;
+        scs = next_scs;
+        next_ids = fetch_page(issue_strip + 32 * kAttendWarps);
+      }
+    };
+    static_assert(C::kStages <= 16, "the first fill stays within the first 32 strips' half");
+    {
+      const int strip0 = issue_strip;
 #pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) issue();
+      for (int i = 0; i < C::kStages - 1; ++i) {
+        issue_copy();
+        issue_stage = i + 1;
+        issue_strip += kAttendWarps;
+        ++issue_n;
+      }
+      fetch_scales(ids, scs);
+      issue_strip = strip0;
+      issue_n = issue_stage = 0;
+#pragma unroll
+      for (int i = 0; i < C::kStages - 1; ++i) {
+        issue_scales();
+        advance();
+      }
+    }
 
     // ---- the query rows as fp16 fragments ----
     // k step u, lane (g, t): row 8 nt + g, channels kKRun * (t + 4 j) + 4 * (u mod run) + 0..3
@@ -566,7 +590,9 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_m16n8k16(o[i][nt], a, pf[nt][0], pf[nt][1]);
       }
-      issue();
+      issue_copy();
+      issue_scales();
+      advance();
     }
     copy_wait<0>();
 

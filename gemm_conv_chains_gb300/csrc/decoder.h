@@ -92,6 +92,7 @@ cudaError_t launch_attend_256(int nt, const AttendParams& p, cudaStream_t s);
 cudaError_t launch_prompt(const AttendParams& p, cudaStream_t s);
 // Bytes of workspace that it takes for `rows` query rows per sequence and kv head (p.meta).
 int64_t prompt_workspace(int64_t rows, int32_t B);
-cudaError_t launch_attend_combine(const AttendParams& p, int nt, int threads, cudaStream_t s);
+// Joins what the split kernel left in parts.
+cudaError_t launch_attend_combine(const AttendParams& p, int nt, int num_sms, cudaStream_t s);
 
 }  // namespace b2b

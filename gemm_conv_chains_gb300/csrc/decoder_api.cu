@@ -324,9 +324,7 @@ b2b_status b2b_cache_attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, 
     default: break;
   }
   if (e != cudaSuccess || sc.whole) return launched(e);
-  // a few rows in many parts: more threads per row
-  const int64_t rows = static_cast<int64_t>(cache->batch) * cache->max_new * q_heads;
-  return launched(launch_attend_combine(p, sc.nt, rows <= 4 * d->num_sms ? 512 : 128, s));
+  return launched(launch_attend_combine(p, sc.nt, d->num_sms, s));
 }
 
 b2b_status b2b_get_cache_error(uint32_t info[4]) {

@@ -1,18 +1,22 @@
 // kernels_attend_join.cu -- joins the partial results of the row tiles that the split cache
-// attention cut between CTAs, and chooses its row tiles.
+// attention cut between CTAs.
 #include "cache_attention.cuh"
 
 namespace b2b {
 
-// One block per query row.  A row tile of `tiles` numbered tiles from number a on lies in the
-// runs a / per .. (a + tiles - 1) / per; one run: the row is already written.  The weights
-// 2^(lse_i - max) are computed once per row in shared memory, so that the sums over the parts
-// are independent loads; groups of D / 4 threads take every so-many-th part.
-__global__ void attend_join_kernel(const AttendParams p, int RT) {
+// One block per query row and share of its channels.  A row tile of `tiles` numbered tiles from
+// number a on lies in the runs a / per .. (a + tiles - 1) / per; one run: the row is already
+// written.  A part is RT rows of D normalised sums and RT log2 sums of weights.  Groups of `lanes`
+// threads (four channels each) take every so-many-th part with a running maximum of their own, four
+// loads in flight, and are joined in shared memory: latency bound, a few KB per block.
+__global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, int RT, int lanes,
+                                                          int shares) {
   extern __shared__ float sh[];
   const CacheView& c = p.c;
   const int D = c.D;
-  const int64_t x = blockIdx.x;
+  int64_t x = blockIdx.x;
+  const int share = static_cast<int>(x % shares);
+  x /= shares;
   const int head = static_cast<int>(x % p.q_heads);
   const int tq = static_cast<int>(x / p.q_heads % c.max_new);
   const int b = static_cast<int>(x / p.q_heads / c.max_new);
@@ -32,78 +36,96 @@ __global__ void attend_join_kernel(const AttendParams p, int RT) {
   const float* first = p.part + (2 * c0 + (c0 * per < a ? 1 : 0)) * part_floats;
   const float* rest = p.part + 2 * (c0 + 1) * part_floats;   // slot 0 of the later runs
   const int rr = r % RT;
-  auto part_of = [&](int i) { return i == 0 ? first : rest + 2 * (i - 1) * part_floats; };
 
-  float* weight = sh;
-  float* scratch = sh + p.grid;
-  float top = kNoMax;
-  for (int i = threadIdx.x; i < parts; i += blockDim.x) {
-    const float v = __ldg(part_of(i) + RT * D + rr);
-    weight[i] = v;
-    top = fmaxf(top, v);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = top;
-  __syncthreads();
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) top = fmaxf(top, scratch[w]);
-  __syncthreads();
-
-  const int lanes = D / 4, groups = blockDim.x / lanes;
-  const int grp = threadIdx.x / lanes, d = 4 * (threadIdx.x % lanes);
+  const int groups = blockDim.x / lanes;
+  const int grp = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+  const int d = 4 * (share * lanes + lane);
+  constexpr int kFlight = 4;
+  float m = kNoMax, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-  if (grp < groups) {
-#pragma unroll 4
-    for (int i = grp; i < parts; i += groups) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(part_of(i) + rr * D + d));
-      const float f = weight[i] <= kNoMax ? 0.f : exp2_fast(weight[i] - top);
-      sum += f;
-      acc.x += f * v.x;
-      acc.y += f * v.y;
-      acc.z += f * v.z;
-      acc.w += f * v.w;
+  for (int i = grp; i < parts; i += kFlight * groups) {
+    float lse[kFlight];
+    float4 v[kFlight];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const int at = i + k * groups;
+      lse[k] = kNoMax;
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (at < parts) {
+        const float* part = at == 0 ? first : rest + 2 * (at - 1) * part_floats;
+        lse[k] = __ldg(part + RT * D + rr);
+        v[k] = __ldg(reinterpret_cast<const float4*>(part + rr * D + d));
+      }
     }
-    float4* put = reinterpret_cast<float4*>(scratch);
-    put[grp * lanes + d / 4] = acc;
-    if (d == 0) weight[p.grid + 4 * groups * lanes + grp] = sum;
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) top = fmaxf(top, lse[k]);
+    const float f = exp2_fast(m - top);
+    m = top;
+    l *= f;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const float w = lse[k] <= kNoMax ? 0.f : exp2_fast(lse[k] - top);   // a NaN stays one
+      l += w;
+      acc.x += w * v[k].x;
+      acc.y += w * v[k].y;
+      acc.z += w * v[k].z;
+      acc.w += w * v[k].w;
+    }
+  }
+  float* stat = sh;                                  // [groups][2], then [groups][lanes] float4
+  float4* put = reinterpret_cast<float4*>(sh + ((2 * groups + 3) & ~3));
+  if (grp < groups) {
+    put[grp * lanes + lane] = acc;
+    if (lane == 0) {
+      stat[2 * grp] = m;
+      stat[2 * grp + 1] = l;
+    }
   }
   __syncthreads();
-  if (threadIdx.x < lanes) {
-    const float4* get = reinterpret_cast<const float4*>(scratch);
-    for (int k = 1; k < groups; ++k) {
-      const float4 v = get[k * lanes + threadIdx.x];
-      acc.x += v.x;
-      acc.y += v.y;
-      acc.z += v.z;
-      acc.w += v.w;
-      sum += weight[p.grid + 4 * groups * lanes + k];
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint16_t* dst = p.out + ((s.row + static_cast<int64_t>(tq)) * p.q_heads + head) * D + d;
-    *reinterpret_cast<uint2*>(dst) =
-        p.is_bf16
-            ? make_uint2(narrow2<true>(acc.x * inv, acc.y * inv), narrow2<true>(acc.z * inv, acc.w * inv))
-            : make_uint2(narrow2<false>(acc.x * inv, acc.y * inv),
-                         narrow2<false>(acc.z * inv, acc.w * inv));
+  if (threadIdx.x >= lanes) return;
+  float top = kNoMax;
+  for (int k = 0; k < groups; ++k) top = fmaxf(top, stat[2 * k]);
+  float sum = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < groups; ++k) {
+    const float w = exp2_fast(stat[2 * k] - top);
+    const float4 v = put[k * lanes + lane];
+    sum += w * stat[2 * k + 1];
+    acc.x += w * v.x;
+    acc.y += w * v.y;
+    acc.z += w * v.z;
+    acc.w += w * v.w;
   }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint16_t* dst = p.out + ((s.row + static_cast<int64_t>(tq)) * p.q_heads + head) * D + d;
+  *reinterpret_cast<uint2*>(dst) =
+      p.is_bf16 ? make_uint2(narrow2<true>(acc.x * inv, acc.y * inv), narrow2<true>(acc.z * inv, acc.w * inv))
+                : make_uint2(narrow2<false>(acc.x * inv, acc.y * inv),
+                             narrow2<false>(acc.z * inv, acc.w * inv));
 }
 
-cudaError_t launch_attend_combine(const AttendParams& p, int nt, int threads, cudaStream_t s) {
-  const int64_t blocks = static_cast<int64_t>(p.c.B) * p.c.max_new * p.q_heads;
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  const int lanes = p.c.D / 4, groups = threads / lanes;
+cudaError_t launch_attend_combine(const AttendParams& p, int nt, int num_sms, cudaStream_t s) {
+  const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.max_new * p.q_heads;
+  // few rows may have many parts each (a long context): more blocks and more groups per row
+  int shares = 1;
+  while (rows * shares < num_sms && p.c.D / 4 / (2 * shares) >= 4 && p.c.D / 4 % (2 * shares) == 0)
+    shares *= 2;
+  const int lanes = p.c.D / 4 / shares, threads = rows < 4 * num_sms ? 256 : 128;
+  const int groups = threads / lanes;
+  if (rows * shares > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * shares));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = sizeof(float) * (p.grid + 4 * groups * lanes + groups + 32);
+  cfg.dynamicSmemBytes = sizeof(float) * (((2 * groups + 3) & ~3) + 4 * groups * lanes);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_join_kernel, p, nt * 8);
+  return cudaLaunchKernelEx(&cfg, attend_join_kernel, p, nt * 8, lanes, shares);
 }
 
 }  // namespace b2b
