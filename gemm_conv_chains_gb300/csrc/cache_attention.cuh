@@ -164,46 +164,57 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
                                               (NT > 1 ? KS * NT * 256 : 0));
 
   // ---- this CTA's run of tiles ----
-  auto work_of = [&](const Sequence& s) -> int64_t {
-    if (s.n <= 0) return 0;
-    const int64_t row_tiles = (static_cast<int64_t>(s.n) * p.group + RT - 1) / RT;
-    const int64_t tiles = p.whole ? 1 : (s.len + kTileTokens - 1) / kTileTokens;
+  // (Counts of tiles fit 32 bits: the host refuses more.  The plan is latency, in a kernel whose
+  // instructions are not in the cache yet: one pass of loads, 32-bit arithmetic, short code.)
+  auto work_of = [&](const Sequence& s) -> uint32_t {
+    if (s.n <= 0) return 0u;
+    const uint32_t row_tiles = (static_cast<uint32_t>(s.n) * p.group + RT - 1) / RT;
+    const uint32_t tiles = p.whole ? 1u : (s.len + kTileTokens - 1) / kTileTokens;
     return row_tiles * c.heads * tiles;
   };
-  int64_t total = 0;
-  for (int b = lane; b < c.B; b += 32) total += work_of(load_sequence(c, b, DK_ATTEND));
+  // lane's share of the first kHeld x 32 sequences stays in registers for the search
+  constexpr int kHeld = 4;
+  uint32_t held[kHeld], total = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  if (!p.whole && per < p.min_tiles) per = p.min_tiles;
-  int64_t at = blockIdx.x * per;
-  const int64_t run_end = at + per < total ? at + per : total;
+  for (int i = 0; i < kHeld; ++i) {
+    held[i] = 0u;
+    if (32 * i + lane < c.B) held[i] = work_of(load_sequence(c, 32 * i + lane, DK_ATTEND));
+    total += held[i];
+  }
+  for (int b = 32 * kHeld + lane; b < c.B; b += 32) total += work_of(load_sequence(c, b, DK_ATTEND));
+  total = __reduce_add_sync(0xffffffffu, total);
+  uint32_t per = (total + gridDim.x - 1) / gridDim.x;
+  if (!p.whole && per < static_cast<uint32_t>(p.min_tiles)) per = p.min_tiles;
+  uint32_t at = blockIdx.x * per;
+  const uint32_t run_begin = at, run_end = at + per < total ? at + per : total;
   const bool scribe = p.meta != nullptr && blockIdx.x == 0 && warp == 0;
   if (scribe && lane == 0) p.meta[0] = per;            // for the kernel that joins the runs
   grid_launch_dependents();
   if (at >= run_end && !scribe) return;
 
-  // the sequence that holds tile `at`
+  // the sequence that holds tile `at`, and the number of its first tile
   int b = 0;
-  int64_t base = 0;                    // number of sequence b's first tile
+  uint32_t base = 0;
   {
-    int64_t before = 0;
+    uint32_t before = 0;
     bool found = false;
-    for (int b0 = 0; b0 < c.B; b0 += 32) {
-      int64_t w = 0;
-      if (b0 + lane < c.B) w = work_of(load_sequence(c, b0 + lane, DK_ATTEND));
-      int64_t upto = w;
+#pragma unroll 1
+    for (int i = 0; 32 * i < c.B; ++i) {
+      uint32_t w = 0u;
+      if (i < kHeld) w = i == 0 ? held[0] : i == 1 ? held[1] : i == 2 ? held[2] : held[3];
+      else if (32 * i + lane < c.B) w = work_of(load_sequence(c, 32 * i + lane, DK_ATTEND));
+      uint32_t upto = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += v;
       }
       upto += before;
-      if (scribe && b0 + lane < c.B) p.meta[1 + b0 + lane] = upto - w;
+      if (scribe && 32 * i + lane < c.B) p.meta[1 + 32 * i + lane] = upto - w;
       const uint32_t hit = __ballot_sync(0xffffffffu, upto > at);
       if (hit != 0u && !found) {
         const int src = __ffs(hit) - 1;
-        b = b0 + src;
+        b = 32 * i + src;
         base = __shfl_sync(0xffffffffu, upto - w, src);
         found = true;
         if (!scribe) break;
@@ -215,22 +226,23 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
   Sequence s = at < run_end ? load_sequence(c, b, DK_ATTEND) : Sequence{0, 0, 0};
   while (at < run_end) {
     // ---- the next piece: (sequence b, kv head h, row tile rt), tiles [t0, t1) of it ----
-    int64_t work = work_of(s);
+    uint32_t work = work_of(s);
     while (at >= base + work) {
       base += work;
       s = load_sequence(c, ++b, DK_ATTEND);
       work = work_of(s);
     }
     const int rows = s.n * p.group;
-    const int row_tiles = (rows + RT - 1) / RT;
-    const int64_t tiles = p.whole ? 1 : (s.len + kTileTokens - 1) / kTileTokens;
-    const int64_t piece = (at - base) / tiles;
-    const int h = static_cast<int>(piece / row_tiles), rt = static_cast<int>(piece % row_tiles);
-    const int64_t t0 = at - base - piece * tiles;
-    int64_t t1 = t0 + (run_end - at);
+    const uint32_t row_tiles = static_cast<uint32_t>(rows + RT - 1) / RT;
+    const uint32_t tiles = p.whole ? 1u : static_cast<uint32_t>(s.len + kTileTokens - 1) / kTileTokens;
+    const uint32_t piece = (at - base) / tiles;
+    const int h = row_tiles == 1 ? piece : piece / row_tiles;
+    const int rt = static_cast<int>(piece - h * row_tiles);
+    const uint32_t t0 = at - base - piece * tiles;
+    uint32_t t1 = t0 + (run_end - at);
     if (t1 > tiles) t1 = tiles;
     const bool partial = t0 != 0 || t1 != tiles;
-    const int slot = (t0 == 0 && at != blockIdx.x * per) ? 1 : 0;
+    const int slot = (t0 == 0 && at != run_begin) ? 1 : 0;
     at += t1 - t0;
 
     const int row0 = rt * RT;
@@ -240,8 +252,8 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
     const int high_limit = start + last_row / p.group;    // and of its last
     int strip = static_cast<int>(p.whole ? 0 : t0 * (kTileTokens / kStrip)) + warp;
     const int strips_all = high_limit / kStrip + 1;
-    const int64_t strips_run = p.whole ? strips_all : t1 * (kTileTokens / kStrip);
-    const int strip_end = static_cast<int>(strips_run < strips_all ? strips_run : strips_all);
+    const int strips_run = p.whole ? strips_all : static_cast<int>(t1 * (kTileTokens / kStrip));
+    const int strip_end = strips_run < strips_all ? strips_run : strips_all;
 
     // ---- page numbers and scales of this warp's next 32 strips, one per lane ----
     const int32_t* pages_of = c.page_table + static_cast<int64_t>(b) * c.max_pages;
@@ -309,9 +321,31 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
       }
     };
     static_assert(C::kStages <= 16, "the first fill stays within the first 32 strips' half");
+    // ---- the query rows as fp16 fragments ----
+    // k step u, lane (g, t): row 8 nt + g, channels kKRun * (t + 4 j) + 4 * (u mod run) + 0..3.
+    // One row tile of 8: every warp holds it; more: warp nt turns tile nt, through shared memory.
+    // The loads go out here, behind the page numbers and ahead of what waits for those.
+    constexpr int kPerRun = C::kKRun / 4;            // k steps per run of channels
+    const int q_nt = NT == 1 ? 0 : warp;
+    const int q_row = row0 + 8 * q_nt + g;
+    const bool q_valid = q_nt < NT && q_row < rows;
+    uint32_t raw[KS][2];
+    {
+      const int tq = q_valid ? q_row / p.group : 0;
+      const uint16_t* src = p.q + (s.row + static_cast<int64_t>(tq)) * p.ldq +
+                            static_cast<int64_t>(h * p.group + (q_valid ? q_row - tq * p.group : 0)) * D;
+#pragma unroll
+      for (int u = 0; u < KS; ++u) {
+        const int d = C::kKRun * (t + 4 * (u / kPerRun)) + 4 * (u % kPerRun);
+        uint2 w = make_uint2(0u, 0u);
+        if (q_valid) w = __ldg(reinterpret_cast<const uint2*>(src + d));
+        raw[u][0] = w.x;
+        raw[u][1] = w.y;
+      }
+    }
     {
       const int strip0 = issue_strip;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < C::kStages - 1; ++i) {
         issue_copy();
         issue_stage = i + 1;
@@ -321,69 +355,49 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
       fetch_scales(ids, scs);
       issue_strip = strip0;
       issue_n = issue_stage = 0;
-#pragma unroll
-      for (int i = 0; i < C::kStages - 1; ++i) {
-        issue_scales();
-        advance();
-      }
     }
-
-    // ---- the query rows as fp16 fragments ----
-    // k step u, lane (g, t): row 8 nt + g, channels kKRun * (t + 4 j) + 4 * (u mod run) + 0..3
     uint32_t qf[NT == 1 ? KS : 1][2];
     float qfactor[NT][2];                            // of rows 8 nt + 2 t, + 1
     int limit[NT][2];                                // last key each of them sees
     float slope[NT][2];
     {
-      __syncthreads();                               // q_frags, row_units: the last piece is done
-      constexpr int kPerRun = C::kKRun / 4;          // k steps per run of channels
+      float amax = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (NT > 1 && nt % kAttendWarps != warp && NT >= kAttendWarps) continue;
-        if (NT > 1 && NT < kAttendWarps && nt != warp) continue;
-        const int r = row0 + 8 * nt + g;
-        uint32_t raw[KS][2];
-        float amax = 0.f;
-        const bool valid = r < rows;
-        const int tq = valid ? r / p.group : 0;
-        const uint16_t* src = p.q + (s.row + static_cast<int64_t>(tq)) * p.ldq +
-                              static_cast<int64_t>(h * p.group + (valid ? r - tq * p.group : 0)) * D;
+      for (int u = 0; u < KS; ++u) {
+        const float2 a = p.is_bf16 ? widen2<true>(raw[u][0]) : widen2<false>(raw[u][0]);
+        const float2 z = p.is_bf16 ? widen2<true>(raw[u][1]) : widen2<false>(raw[u][1]);
+        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(z.x), fabsf(z.y))));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      float inv;
+      const float unit = row_unit_of(amax, p.is_bf16 != 0, inv);
+      // (q_frags and row_units are free: the last piece ended in a block barrier)
+      if (t == 0 && (NT == 1 ? warp == 0 : warp < NT)) row_units[8 * q_nt + g] = unit;
 #pragma unroll
-        for (int u = 0; u < KS; ++u) {
-          const int d = C::kKRun * (t + 4 * (u / kPerRun)) + 4 * (u % kPerRun);
-          uint2 w = make_uint2(0u, 0u);
-          if (valid) w = __ldg(reinterpret_cast<const uint2*>(src + d));
-          raw[u][0] = w.x;
-          raw[u][1] = w.y;
-          const float2 a = p.is_bf16 ? widen2<true>(w.x) : widen2<false>(w.x);
-          const float2 z = p.is_bf16 ? widen2<true>(w.y) : widen2<false>(w.y);
-          amax = fmaxf(amax, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(z.x), fabsf(z.y))));
+      for (int u = 0; u < KS; ++u) {
+        uint32_t w[2] = {raw[u][0], raw[u][1]};
+        if (p.is_bf16) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 a = widen2<true>(w[i]);
+            w[i] = narrow2<false>(a.x * inv, a.y * inv);
+          }
         }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        float inv;
-        const float unit = row_unit_of(amax, p.is_bf16 != 0, inv);
-        if (NT == 1 ? warp == 0 : true)
-          if (t == 0) row_units[8 * nt + g] = unit;
-#pragma unroll
-        for (int u = 0; u < KS; ++u) {
-          uint32_t w[2] = {raw[u][0], raw[u][1]};
-          if (p.is_bf16) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float2 a = widen2<true>(w[i]);
-              w[i] = narrow2<false>(a.x * inv, a.y * inv);
-            }
-          }
-          if constexpr (NT == 1) {
-            qf[u][0] = w[0];
-            qf[u][1] = w[1];
-          } else {
-            q_frags[(u * NT + nt) * 32 + lane] = make_uint2(w[0], w[1]);
-          }
+        if constexpr (NT == 1) {
+          qf[u][0] = w[0];
+          qf[u][1] = w[1];
+        } else {
+          if (warp < NT) q_frags[(u * NT + warp) * 32 + lane] = make_uint2(w[0], w[1]);
         }
       }
       __syncthreads();
+    }
+    // the scales of the first strips, asked for with their bytes
+#pragma unroll 1
+    for (int i = 0; i < C::kStages - 1; ++i) {
+      issue_scales();
+      advance();
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)

@@ -68,7 +68,7 @@ struct AttendParams {
   float scale, softcap;       // softcap 0: none
   int32_t grid, min_tiles, whole;
   float* part;                // split workspace: see cache_attention.cuh
-  int64_t* meta;
+  uint32_t* meta;             // [0]: tiles per run, [1 + b]: sequence b's first tile
   uint64_t wait_limit_ns;
 };
 

@@ -134,7 +134,7 @@ SplitChoice split_of(const b2b_cache* c, int32_t q_heads, int num_sms) {
   s.prompt = c->head_dim <= 128 && rows >= kPromptFrom ? 1 : 0;
   s.bytes = s.prompt  ? prompt_workspace(rows, c->batch)
             : s.whole ? 0
-                    : 16 * ((static_cast<int64_t>(c->batch) + 2) / 2) +
+                    : 16 * ((static_cast<int64_t>(c->batch) + 4) / 4) +
                           static_cast<int64_t>(s.grid) * 2 * s.nt * 8 * (c->head_dim + 1) * 4;
   return s;
 }
@@ -147,6 +147,10 @@ b2b_status check_attention(const b2b_cache* c, int64_t T, int32_t q_heads, float
   const int64_t rows = static_cast<int64_t>(c->max_new) * q_heads;
   if (q_heads > 65536 || rows > kMostRows || rows * (c->batch > 0 ? c->batch : 1) > 0x7FFFFFFF)
     return B2B_ERR_UNSUPPORTED;
+  // the split kernel numbers its work, (8 query rows, 64 tokens) at the finest, in 32 bits
+  const double tiles = std::ceil(static_cast<double>(c->max_pages) * c->page_size / 64) *
+                       std::ceil(static_cast<double>(rows) / c->heads / 8) * c->heads * c->batch;
+  if (tiles > 2.0e9) return B2B_ERR_UNSUPPORTED;
   return B2B_OK;
 }
 
@@ -307,10 +311,10 @@ b2b_status b2b_cache_attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, 
   p.grid = sc.grid;
   p.min_tiles = kMinTiles;
   p.whole = sc.whole;
-  p.meta = sc.bytes == 0 ? nullptr : static_cast<int64_t*>(workspace);
+  p.meta = sc.bytes == 0 ? nullptr : static_cast<uint32_t*>(workspace);
   p.part = sc.bytes == 0 || sc.prompt ? nullptr
                     : reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                               16 * ((static_cast<int64_t>(cache->batch) + 2) / 2));
+                                               16 * ((static_cast<int64_t>(cache->batch) + 4) / 4));
   p.wait_limit_ns = kDecoderWaitNs;
   auto s = static_cast<cudaStream_t>(stream);
   if (sc.prompt) return launched(launch_prompt(p, s));

@@ -26,15 +26,15 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, 
   const int h = head / p.group;
   const int r = tq * p.group + head % p.group;
   const int row_tiles = (s.n * p.group + RT - 1) / RT;
-  const int64_t tiles = (s.len + kTileTokens - 1) / kTileTokens;
-  const int64_t per = p.meta[0];
-  const int64_t a = p.meta[1 + b] + (static_cast<int64_t>(h) * row_tiles + r / RT) * tiles;
-  const int64_t c0 = a / per, c1 = (a + tiles - 1) / per;
+  const uint32_t tiles = (s.len + kTileTokens - 1) / kTileTokens;
+  const uint32_t per = p.meta[0];
+  const uint32_t a = p.meta[1 + b] + (static_cast<uint32_t>(h) * row_tiles + r / RT) * tiles;
+  const uint32_t c0 = a / per, c1 = (a + tiles - 1) / per;
   if (c0 == c1) return;
   const int parts = static_cast<int>(c1 - c0) + 1;
   const int64_t part_floats = static_cast<int64_t>(RT) * (D + 1);
-  const float* first = p.part + (2 * c0 + (c0 * per < a ? 1 : 0)) * part_floats;
-  const float* rest = p.part + 2 * (c0 + 1) * part_floats;   // slot 0 of the later runs
+  const float* first = p.part + (2 * static_cast<int64_t>(c0) + (c0 * per < a ? 1 : 0)) * part_floats;
+  const float* rest = p.part + 2 * (static_cast<int64_t>(c0) + 1) * part_floats;   // slot 0 of the later runs
   const int rr = r % RT;
 
   const int groups = blockDim.x / lanes;
