@@ -1,4 +1,5 @@
-"""Python binding of libb2b.so (include/b2b.h): argument marshalling only.
+"""Python binding of libb2b.so (include/b2b.h): argument marshalling only (by ctypes; for the
+decoder-block operators, which run once per token, by the extension of csrc/binding.cpp).
 
 Every function takes CUDA tensors, checks dtypes, shapes and contiguity (the C ABI sees
 only pointers and sizes), allocates the output with torch when none is given, and calls
@@ -9,9 +10,8 @@ raises instead of falling back.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib
 import os
-import struct
 import threading
 from typing import Optional
 
@@ -25,20 +25,7 @@ STATUS = {0: "B2B_OK", 1: "B2B_ERR_NULL", 2: "B2B_ERR_SHAPE", 3: "B2B_ERR_ALIGN"
 
 _lock = threading.Lock()
 _lib = None
-
-
-class _Cache(ctypes.Structure):
-    """b2b_cache (include/b2b.h)."""
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int32),
-                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
-                ("batch", ctypes.c_int32), ("page_table", ctypes.c_void_p),
-                ("max_pages", ctypes.c_int32), ("max_new", ctypes.c_int32),
-                ("lens", ctypes.c_void_p), ("starts", ctypes.c_void_p)]
-
-
-# A b2b_cache as bytes in one step: the binding of a single-token call is a good part of it.
-_pack_cache = struct.Struct("@PPPPqiiiiPiiPP").pack
+_native = None
 
 
 class B2BError(RuntimeError):
@@ -116,19 +103,22 @@ def lib() -> ctypes.CDLL:
         L.b2b_get_tune_record.argtypes = [i32, p64, i32, ctypes.POINTER(i32), i32,
                                           ctypes.POINTER(i32)]
         L.b2b_get_tune_record.restype = ci
-        vpi, f32, f64 = ctypes.c_char_p, ctypes.c_float, ctypes.c_double
+        f64 = ctypes.c_double
         L.b2b_rotary_table.argtypes = [i64, i32, f64, ci, f64, i64, f64, f64, f64, vp, vp]
-        L.b2b_rotary.argtypes = [ci, i64, i32, i32, i32, ci, i32, vp, i64, vp, i64, vp, vp, i64, vp]
-        L.b2b_cache_append.argtypes = [ci, vpi, i64, vp, i64, vp, i64, vp, i64, i32, ci, vp, i64,
-                                       i32, vp, i64, vp]
-        L.b2b_cache_attention_workspace.argtypes = [vpi, i64, i32, ctypes.POINTER(i64)]
-        L.b2b_cache_attention.argtypes = [ci, vpi, i64, vp, i64, i32, f32, f32, vp, vp, vp, i64, vp]
+        L.b2b_rotary_table.restype = ci
         L.b2b_get_cache_error.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
-        for name in ("b2b_rotary_table", "b2b_rotary", "b2b_cache_append",
-                     "b2b_cache_attention_workspace", "b2b_cache_attention", "b2b_get_cache_error"):
-            getattr(L, name).restype = ci
+        L.b2b_get_cache_error.restype = ci
         _lib = L
         return L
+
+
+def _binding():
+    """The extension of csrc/binding.cpp (built with libb2b.so)."""
+    global _native
+    if _native is None:
+        lib()
+        _native = importlib.import_module("._binding", __package__)
+    return _native
 
 
 # ------------------------------------------------------------------------------------
@@ -430,87 +420,11 @@ LAYOUTS = {"half": 0, "interleaved": 1}
 SCALINGS = {"plain": 0, "linear": 1, "blend": 2}
 
 
-# These operators run once per token of a generation, where their checks and marshalling are a
-# good part of a call: each check first asks the few questions that all good operands answer
-# alike, and only then finds out what to refuse.
-
-def _dense(t, name, dt, shape, index) -> int:
-    """Checks a contiguous operand on CUDA device `index` and returns its address."""
-    if t.dtype is dt and t.shape == shape and t.is_contiguous() and t.get_device() == index:
-        return t.data_ptr()
-    _check_tensor(t, name, dt, shape)
-    raise ValueError(f"{name} is on {t.device}, the other operands on cuda:{index}: "
-                     "all operands and the output must be on one device")
-
-
-def _rows(t, name, dt, shape, index) -> int:
-    """Checks a [T, H, D] operand on CUDA device `index` whose heads and channels are dense and
-    returns its token stride in elements."""
-    T, H, D = shape
-    if t.dtype is not dt:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dt}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.get_device() != index or index < 0:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        raise ValueError(f"{name} is on {t.device}, the other operands on cuda:{index}: "
-                         "all operands and the output must be on one device")
-    ld, sh, sd = t.stride()
-    if sd != 1 or (H > 1 and sh != D):
-        raise ValueError(f"{name} must have dense heads and channels, got strides {t.stride()}")
-    return ld if T > 1 else H * D
-
-
-def _table_of(table, index):
-    """Checks a rotary table [positions, rot / 2, 2] and returns its address and rot."""
-    shape = table.shape
-    if len(shape) != 3 or shape[2] != 2:
-        raise ValueError(f"table has shape {tuple(shape)}, expected [positions, rot / 2, 2]")
-    return _dense(table, "table", torch.float32, shape, index), 2 * shape[1]
-
-
 def _layout(layout) -> int:
     try:
         return LAYOUTS[layout]
     except KeyError:
         raise ValueError(f"unknown layout {layout!r}; expected one of {list(LAYOUTS)}") from None
-
-
-def _empty(shape, dtype, device, stream):
-    """A new tensor for work on `stream` (None: the current one), from that stream's memory."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-# torch.cuda.current_stream without the Stream object around the handle, where torch has it.
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream_on(stream, dev):
-    """_stream for a device index."""
-    if stream is None and _current_raw_stream is not None:
-        return _current_raw_stream(dev)
-    return _stream(stream, dev)
-
-
-class _on_device:
-    """torch.cuda.device(dev) for an index, without its cost where it is already current."""
-
-    def __init__(self, dev):
-        self.inner = None if torch.cuda.current_device() == dev else torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.inner is not None:
-            self.inner.__enter__()
-
-    def __exit__(self, *exc):
-        if self.inner is not None:
-            self.inner.__exit__(*exc)
 
 
 def rotary_table(positions, rot, base=10000.0, scaling="plain", factor=1.0, original=0, low=1.0,
@@ -524,59 +438,26 @@ def rotary_table(positions, rot, base=10000.0, scaling="plain", factor=1.0, orig
     device = torch.device(device)
     if device.type != "cuda":
         raise ValueError(f"device must be a CUDA device, got {device}")
-    out = _empty((positions, rot // 2, 2), torch.float32, device, stream)
-    with _on_device(out.get_device()):
+    out = torch.empty((positions, rot // 2, 2), dtype=torch.float32, device=device)
+    with torch.cuda.device(out.device):
         _raise(lib().b2b_rotary_table(positions, rot, base, SCALINGS[scaling], factor, original,
-                                      low, high, gain, out.data_ptr(),
-                                      _stream(stream, out.device)), "b2b_rotary_table")
+                                      low, high, gain, _ptr(out), _stream(stream, out.device)),
+               "b2b_rotary_table")
     return out
 
+
+# What the calls below allocate (outputs, workspace) comes from the memory of the stream they run
+# on; the checks and their messages are in csrc/binding.cpp.
 
 def rotary(x, table, positions, layout="half", inverse=False, out=None, stream=None):
     """x [T, H, D] (token stride free) with the first rot channels of each head turned by the
     angles of positions [T] (int32), table [P, rot / 2, 2] (rotary_table); the inverse turns
     back, which is the gradient.  out may be x (b2b_rotary)."""
-    dt, shape, dev = x.dtype, x.shape, x.get_device()
-    code = _dtype_code(x)
-    ldx = _rows(x, "x", dt, shape, dev)
-    T, H, D = shape
-    table_ptr, rot = _table_of(table, dev)
-    positions_ptr = _dense(positions, "positions", torch.int32, (T,), dev)
-    if out is None:
-        out = _empty(shape, dt, x.device, stream)
-        ldo = H * D
-    else:
-        ldo = _rows(out, "out", dt, shape, dev)
-    with _on_device(dev):
-        _raise((_lib or lib()).b2b_rotary(
-            code, T, H, D, rot, _layout(layout), 1 if inverse else 0, x.data_ptr(), ldx, table_ptr,
-            table.shape[0], positions_ptr, out.data_ptr(), ldo, _stream_on(stream, dev)), "b2b_rotary")
-    return out
-
-
-def _cache_of(T, dev, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts, max_new):
-    """Checks the cache's tensors and describes them: (b2b_cache as bytes, kv heads, head size,
-    sequences, pages per sequence, page size, max_new)."""
-    shape = k_cache.shape
-    if len(shape) != 4:
-        raise ValueError(f"k_cache has shape {tuple(shape)}, expected "
-                         "[pages, heads, page size, head size]")
-    pages, heads, page, D = shape
-    f8, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [sequences, pages]")
-    B, max_pages = page_table.shape
-    if max_new is None:
-        max_new = T if starts is not None else T // max(B, 1)
-    scales = (pages, heads)
-    c = _pack_cache(_dense(k_cache, "k_cache", f8, shape, dev),
-                    _dense(v_cache, "v_cache", f8, shape, dev),
-                    _dense(k_scale, "k_scale", f32, scales, dev),
-                    _dense(v_scale, "v_scale", f32, scales, dev), pages, heads, page, D, B,
-                    _dense(page_table, "page_table", i32, (B, max_pages), dev), max_pages, max_new,
-                    _dense(lens, "lens", i32, (B,), dev),
-                    0 if starts is None else _dense(starts, "starts", i32, (B + 1,), dev))
-    return c, heads, D, B, max_pages, page, max_new
+    got = (_native or _binding()).rotary(x, table, positions, _layout(layout), 1 if inverse else 0,
+                                         out, stream)
+    if type(got) is int:
+        raise B2BError(got, "b2b_rotary")
+    return got
 
 
 def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts=None,
@@ -589,48 +470,12 @@ def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, sta
     page_table [B, pages per sequence], lens [B] (the new tokens included) and starts [B + 1]
     (rows of each sequence among the T; None: T / B each) are int32; max_new is the most new
     tokens of a sequence (default: T, or T / B without starts)."""
-    dt, dev = k.dtype, k.get_device()
-    code = _dtype_code(k)
-    T = k.shape[0]
-    c, heads, D, *_ = _cache_of(T, dev, k_cache, v_cache, k_scale, v_scale, page_table, lens,
-                                starts, max_new)
-    ldk = _rows(k, "k", dt, (T, heads, D), dev)
-    ldv = _rows(v, "v", dt, (T, heads, D), dev)
-    table_ptr, rot = (None, 0) if table is None else _table_of(table, dev)
-    q_ptr, q_out_ptr, ldq, ldqo, q_heads = None, None, 0, 0, 0
-    if q is not None:
-        if table is None:
-            raise ValueError("q is given to be rotated: it needs a table")
-        q_heads = q.shape[1]
-        shape = (T, q_heads, D)
-        ldq = _rows(q, "q", dt, shape, dev)
-        if q_out is None:
-            q_out = _empty(shape, dt, k.device, stream)
-            ldqo = q_heads * D
-        else:
-            ldqo = _rows(q_out, "q_out", dt, shape, dev)
-        q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out is given without q")
-    with _on_device(dev):
-        _raise((_lib or lib()).b2b_cache_append(
-            code, c, T, k.data_ptr(), ldk, v.data_ptr(), ldv, table_ptr,
-            0 if table is None else table.shape[0], rot, _layout(layout), q_ptr, ldq, q_heads,
-            q_out_ptr, ldqo, _stream_on(stream, dev)), "b2b_cache_append")
-    return q_out
-
-
-@functools.lru_cache(maxsize=1024)
-def _workspace_bytes(dev, T, q_heads, pages, heads, D, B, max_pages, page, max_new, starts) -> int:
-    """b2b_cache_attention_workspace: a function of the sizes (and the device's SMs) alone.  The
-    addresses only have to be there."""
-    any_ptr = 1 << 12
-    c = _pack_cache(any_ptr, any_ptr, any_ptr, any_ptr, pages, heads, page, D, B, any_ptr, max_pages,
-                    max_new, any_ptr, any_ptr if starts else 0)
-    need = ctypes.c_int64(0)
-    _raise(lib().b2b_cache_attention_workspace(c, T, q_heads, ctypes.byref(need)),
-           "b2b_cache_attention_workspace")
-    return need.value
+    got = (_native or _binding()).cache_append(
+        k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts, max_new, table,
+        _layout(layout), q, q_out, stream)
+    if type(got) is int:
+        raise B2BError(got, "b2b_cache_append")
+    return got
 
 
 def cache_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts=None,
@@ -641,45 +486,22 @@ def cache_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, sta
     The cache and its sequences as in cache_append; scale defaults to D^-1/2; softcap caps the
     scores by a tanh, slopes [q heads] (float32) add slope * (key position - query position).
     workspace (uint8, at least cache_attention_workspace's bytes): allocated when not given."""
-    dt, shape, dev = q.dtype, q.shape, q.get_device()
-    code = _dtype_code(q)
-    ldq = _rows(q, "q", dt, shape, dev)
-    T, q_heads, D = shape
-    c, heads, cache_D, B, max_pages, page, most = _cache_of(
-        T, dev, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts, max_new)
-    if D != cache_D:
-        raise ValueError(f"q has head size {D}, the cache {cache_D}")
-    slopes_ptr = None if slopes is None else _dense(slopes, "slopes", torch.float32, (q_heads,), dev)
-    if out is None:
-        out = _empty(shape, dt, q.device, stream)
-        out_ptr = out.data_ptr()
-    else:
-        out_ptr = _dense(out, "out", dt, shape, dev)
-    with _on_device(dev):
-        if workspace is None:
-            size = _workspace_bytes(dev, T, q_heads, k_cache.shape[0], heads, D, B, max_pages, page,
-                                    most, starts is not None)
-            if size > 0:
-                workspace = _empty(size, torch.uint8, q.device, stream)
-            work_ptr = workspace.data_ptr() if size > 0 else None
-        else:
-            size = workspace.numel()
-            work_ptr = _dense(workspace, "workspace", torch.uint8, (size,), dev)
-        _raise((_lib or lib()).b2b_cache_attention(
-            code, c, T, q.data_ptr(), ldq, q_heads, D ** -0.5 if scale is None else scale, softcap,
-            slopes_ptr, out_ptr, work_ptr, size, _stream_on(stream, dev)), "b2b_cache_attention")
-    return out
+    got = (_native or _binding()).cache_attention(
+        q, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts, max_new, scale, softcap,
+        slopes, out, workspace, stream)
+    if type(got) is int:
+        raise B2BError(got, "b2b_cache_attention")
+    return got
 
 
 def cache_attention_workspace(T, q_heads, k_cache, v_cache, k_scale, v_scale, page_table, lens,
                               starts=None, max_new=None) -> int:
     """Bytes of workspace that cache_attention takes for these arguments (0: none)."""
-    dev = k_cache.get_device()
-    _, heads, D, B, max_pages, page, most = _cache_of(
-        T, dev, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts, max_new)
-    with _on_device(dev):
-        return _workspace_bytes(dev, T, q_heads, k_cache.shape[0], heads, D, B, max_pages, page,
-                                most, starts is not None)
+    got = (_native or _binding()).cache_attention_workspace(
+        T, q_heads, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts, max_new)
+    if got < 0:
+        raise B2BError(-got, "b2b_cache_attention_workspace")
+    return got
 
 
 def get_cache_error():

@@ -11,19 +11,35 @@ OK, NULL, SHAPE, ALIGN, UNSUP, CUDA = 0, 1, 2, 3, 4, 5
 FAKE, MIS = 0x10000, 0x10008
 
 
+i32, i64, vp, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
+
+
+class Cache(ctypes.Structure):
+    """b2b_cache (include/b2b.h)."""
+    _fields_ = [("k", vp), ("v", vp), ("k_scale", vp), ("v_scale", vp), ("pages", i64),
+                ("heads", i32), ("page_size", i32), ("head_dim", i32), ("batch", i32),
+                ("page_table", vp), ("max_pages", i32), ("max_new", i32), ("lens", vp),
+                ("starts", vp)]
+
+
 @pytest.fixture(scope="module")
 def L():
-    return ops.lib()
+    L = ctypes.CDLL(ops.lib()._name)
+    cp = ctypes.POINTER(Cache)
+    L.b2b_rotary_table.argtypes = ops.lib().b2b_rotary_table.argtypes
+    L.b2b_rotary.argtypes = [i32, i64, i32, i32, i32, i32, i32, vp, i64, vp, i64, vp, vp, i64, vp]
+    L.b2b_cache_append.argtypes = [i32, cp, i64, vp, i64, vp, i64, vp, i64, i32, i32, vp, i64, i32,
+                                   vp, i64, vp]
+    L.b2b_cache_attention_workspace.argtypes = [cp, i64, i32, ctypes.POINTER(i64)]
+    L.b2b_cache_attention.argtypes = [i32, cp, i64, vp, i64, i32, f32, f32, vp, vp, vp, i64, vp]
+    return L
 
 
 def cache(**kw):
     a = dict(k=FAKE, v=FAKE, k_scale=FAKE, v_scale=FAKE, pages=10, heads=2, page_size=16,
              head_dim=64, batch=2, page_table=FAKE, max_pages=4, max_new=1, lens=FAKE, starts=None)
     a.update(kw)
-    values = [a[n] for n, _ in ops._Cache._fields_]
-    packed = ops._pack_cache(*[0 if x is None else x for x in values])
-    assert packed == bytes(ops._Cache(*values))              # the two forms of the struct agree
-    return packed
+    return Cache(*[a[n] for n, _ in Cache._fields_])
 
 
 def attend(L, c=None, dt=0, T=2, q=FAKE, ldq=256, q_heads=4, scale=0.1, cap=0.0, slopes=None,
@@ -126,22 +142,29 @@ def test_valid_calls_without_a_device_report_a_cuda_error(L):
 
 def test_binding_refusals():
     x = torch.zeros(2, 2, 64, dtype=torch.float16)
-    with pytest.raises(ValueError, match="CUDA"):
-        ops.rotary(x, torch.zeros(4, 32, 2), torch.zeros(2, dtype=torch.int32))
-    with pytest.raises(TypeError):
-        ops.rotary(x.float(), torch.zeros(4, 32, 2), torch.zeros(2, dtype=torch.int32))
-    with pytest.raises(ValueError, match="CUDA"):
-        ops._rows(x, "x", x.dtype, (2, 2, 64), -1)
-    with pytest.raises(ValueError, match="shape"):
-        ops._rows(x, "x", x.dtype, (2, 3, 64), 0)
+    table, pos = torch.zeros(4, 32, 2), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="x must be a CUDA tensor"):
+        ops.rotary(x, table, pos)
+    with pytest.raises(TypeError, match="expected float16 or bfloat16, got torch.float32"):
+        ops.rotary(x.float(), table, pos)
+    with pytest.raises(TypeError, match="must be a torch.Tensor"):
+        ops.rotary(None, table, pos)
+    with pytest.raises(ValueError, match="three dimensions"):
+        ops.rotary(x[0], table, pos)
     with pytest.raises(ValueError, match="layout"):
-        ops._layout("pairs")
+        ops.rotary(x, table, pos, layout="pairs")
     with pytest.raises(ValueError, match="scaling"):
         ops.rotary_table(4, 32, scaling="other")
     with pytest.raises(ValueError, match="CUDA"):
         ops.rotary_table(4, 32, device="cpu")
     k = torch.zeros(3, 2, 16, 64).to(torch.float8_e4m3fn)
     s = torch.zeros(3, 2)
+    pages, lens = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
-        ops._cache_of(2, 0, k, k, s, s, torch.zeros(2, 4, dtype=torch.int32),
-                      torch.zeros(2, dtype=torch.int32), None, None)
+        ops.cache_append(x, x, k, k, s, s, pages, lens)
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.cache_attention(x, k, k, s, s, pages, lens)
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.cache_attention_workspace(2, 2, k, k, s, s, pages, lens)
+    with pytest.raises(TypeError):
+        ops.cache_attention(x)

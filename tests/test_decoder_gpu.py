@@ -433,3 +433,71 @@ def test_no_rows_is_no_launch():
     assert torch.equal(before.view(torch.uint8), args[0].view(torch.uint8))
     table = ops.rotary_table(4, 64)
     assert ops.rotary(q, table, torch.empty(0, dtype=torch.int32).cuda()).shape == (0, 2, 64)
+
+
+# ------------------------------------------------------------------------------------
+# refusals of the binding that need CUDA tensors
+# ------------------------------------------------------------------------------------
+
+def test_binding_refuses_wrong_operands():
+    c = ref.Cache([5, 7], [1, 1], 2, 64, 16)
+    args = c.args(starts=False)
+    q = torch.zeros(2, 4, 64, dtype=torch.float16, device="cuda")
+    k = torch.zeros(2, 2, 64, dtype=torch.float16, device="cuda")
+
+    def other(i, t):
+        return args[:i] + [t] + args[i + 1:]
+
+    for i, t, error in [(0, args[0].view(torch.uint8), TypeError), (1, args[1][:1], ValueError),
+                        (0, args[0].transpose(1, 2), ValueError), (2, args[2].double(), TypeError),
+                        (2, args[2].cpu(), ValueError), (3, args[3][:, :1], ValueError),
+                        (4, args[4].long(), TypeError), (4, args[4][0], ValueError),
+                        (5, args[5][:1], ValueError), (5, args[5].cpu(), ValueError)]:
+        with pytest.raises(error):
+            ops.cache_attention(q, *other(i, t))
+        with pytest.raises(error):
+            ops.cache_append(k, k, *other(i, t))
+    with pytest.raises(ValueError, match="starts has shape"):
+        ops.cache_attention(q, *args, starts=args[5])
+    with pytest.raises(ValueError, match="head size"):
+        ops.cache_attention(torch.zeros(2, 4, 128, dtype=torch.float16, device="cuda"), *args)
+    with pytest.raises(ValueError, match="dense heads"):
+        ops.cache_attention(q.transpose(0, 1).contiguous().transpose(0, 1), *args)
+    with pytest.raises(TypeError, match="out has dtype"):
+        ops.cache_attention(q, *args, out=q.float())
+    with pytest.raises(TypeError, match="slopes has dtype"):
+        ops.cache_attention(q, *args, slopes=torch.zeros(4, dtype=torch.float16, device="cuda"))
+    with pytest.raises(ops.B2BError):                        # 3 query heads over 2 kv heads
+        ops.cache_attention(q[:, :3], *args)
+    with pytest.raises(ops.B2BError):
+        ops.cache_attention(q, *args, softcap=-1.0)
+    with pytest.raises(ValueError, match="needs a table"):
+        ops.cache_append(k, k, *args, q=q)
+    with pytest.raises(ValueError, match="without q"):
+        ops.cache_append(k, k, *args, q_out=q)
+    with pytest.raises(TypeError, match="v has dtype"):
+        ops.cache_append(k, k.bfloat16(), *args)
+    table = ops.rotary_table(20, 64)
+    with pytest.raises(ValueError, match="table has shape"):
+        ops.rotary(q, table[..., 0], args[5])
+    with pytest.raises(TypeError, match="positions has dtype"):
+        ops.rotary(q, table, args[5].long())
+    with pytest.raises(ops.B2BError):                        # rot above the head's channels
+        ops.rotary(q, ops.rotary_table(20, 128), args[5])
+    long = ref.Cache([4000], [1], 1, 64, 16)
+    with pytest.raises(ops.B2BError):
+        ops.cache_attention(q[:1], *long.args(starts=False),
+                            workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+def test_streams_by_object_and_handle():
+    x = _randn(1, 9, 3, 64).half().cuda()
+    table = ops.rotary_table(50, 64)
+    pos = torch.arange(9, dtype=torch.int32).cuda()
+    want = ops.rotary(x, table, pos)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    by_object = ops.rotary(x, table, pos, stream=side)
+    by_handle = ops.rotary(x, table, pos, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(by_object, want) and torch.equal(by_handle, want)
