@@ -192,7 +192,7 @@ b2b_status b2b_rotary(b2b_dtype dt, int64_t T, int32_t H, int32_t D, int32_t rot
   if (T < 0 || H <= 0 || D <= 0 || positions_in_table < 0) return B2B_ERR_SHAPE;
   if (D % 8 != 0) return B2B_ERR_ALIGN;
   if (b2b_status st = check_rot(D, rot, layout); st != B2B_OK) return st;
-  if (T > kMostRows || D > 65536 || static_cast<int64_t>(H) * D > (int64_t{1} << 27))
+  if (T > kMostRows || D > 2048 || static_cast<int64_t>(H) * D > (int64_t{1} << 27))
     return B2B_ERR_UNSUPPORTED;
   if (b2b_status st = check_ld(ldx, static_cast<int64_t>(H) * D); st != B2B_OK) return st;
   if (b2b_status st = check_ld(ldo, static_cast<int64_t>(H) * D); st != B2B_OK) return st;

@@ -86,12 +86,11 @@ __device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
                     narrow2<BF16>(f[4], f[5]), narrow2<BF16>(f[6], f[7]));
 }
 
-// (a, b) turned by (cos, sin): a c - b s, b c + a s, each product and sum rounded to fp32
-// on its own (no fused multiply-add), so that a rotated key has one value whichever
-// kernel turns it.
+// (a, b) turned by (cos, sin): a c - b s, b c + a s; one function, so that a key has one value
+// whichever kernel turns it.
 __device__ __forceinline__ void turn(float& a, float& b, float2 cs) {
-  const float x = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
-  const float y = __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
+  const float x = fmaf(a, cs.x, -(b * cs.y));
+  const float y = fmaf(b, cs.x, a * cs.y);
   a = x;
   b = y;
 }
@@ -104,45 +103,102 @@ __device__ __forceinline__ int row_units(int D, int rot, int interleaved) {
   return interleaved ? D / 8 : rot / 16 + (D - rot) / 8;
 }
 
-// The fp32 values of unit u after the rotation: lo (and hi in a half-layout pair unit).
-// cs: the position's table row.  Returns the channel of lo, or of both through `pair`.
-template <bool BF16>
-__device__ __forceinline__ int load_unit(const uint16_t* row, const float2* cs, int u, int rot,
-                                         int interleaved, bool inverse, float (&lo)[8],
-                                         float (&hi)[8], bool& pair) {
-  const float sign = inverse ? -1.f : 1.f;
-  pair = false;
+// Where a thread's unit u lies in every row that it takes: channel d, and (a pair unit of the half
+// layout) its partners at d + rot / 2.
+struct UnitAt {
+  int d;
+  bool pair, turned;
+};
+__device__ __forceinline__ UnitAt unit_at(int u, int rot, int interleaved) {
+  UnitAt a;
   if (interleaved) {
-    const int d = 8 * u;
-    widen8<BF16>(__ldg(reinterpret_cast<const uint4*>(row + d)), lo);
-    if (d < rot) {
-      const float4* t = reinterpret_cast<const float4*>(cs + d / 2);
-      const float4 c0 = __ldg(t), c1 = __ldg(t + 1);
-      turn(lo[0], lo[1], make_float2(c0.x, sign * c0.y));
-      turn(lo[2], lo[3], make_float2(c0.z, sign * c0.w));
-      turn(lo[4], lo[5], make_float2(c1.x, sign * c1.y));
-      turn(lo[6], lo[7], make_float2(c1.z, sign * c1.w));
+    a.d = 8 * u;
+    a.pair = false;
+    a.turned = a.d < rot;
+  } else {
+    const int pairs = rot / 16;
+    a.pair = a.turned = u < pairs;
+    a.d = a.pair ? 8 * u : rot + 8 * (u - pairs);
+  }
+  return a;
+}
+
+// A unit's raw vectors, to be asked for ahead of what their use waits for.
+struct RawUnit {
+  uint4 lo, hi;
+};
+__device__ __forceinline__ RawUnit load_raw(const uint16_t* row, const UnitAt& a, int rot) {
+  RawUnit r;
+  r.lo = __ldg(reinterpret_cast<const uint4*>(row + a.d));
+  r.hi = r.lo;
+  if (a.pair) r.hi = __ldg(reinterpret_cast<const uint4*>(row + a.d + rot / 2));
+  return r;
+}
+
+// The (cos, sin) of a unit's pairs: kept in registers by a thread that turns several units with
+// them, or read from a table row as they are used.
+struct Angles {
+  float4 v[4];
+  __device__ __forceinline__ float4 operator[](int i) const { return v[i]; }
+};
+struct AngleRow {
+  const float4* t;
+  __device__ __forceinline__ float4 operator[](int i) const { return __ldg(t + i); }
+};
+__device__ __forceinline__ AngleRow angle_row(const float2* row, const UnitAt& a, int interleaved) {
+  return AngleRow{reinterpret_cast<const float4*>(row + (interleaved ? a.d / 2 : a.d))};
+}
+__device__ __forceinline__ Angles load_angles(const float2* row, const UnitAt& a, int interleaved) {
+  const AngleRow t = angle_row(row, a, interleaved);
+  Angles g;
+  if (a.turned) {
+    g.v[0] = t[0];
+    g.v[1] = t[1];
+    if (!interleaved) {
+      g.v[2] = t[2];
+      g.v[3] = t[3];
     }
-    return d;
   }
-  const int pairs = rot / 16;
-  if (u >= pairs) {
-    const int d = rot + 8 * (u - pairs);
-    widen8<BF16>(__ldg(reinterpret_cast<const uint4*>(row + d)), lo);
-    return d;
-  }
-  pair = true;
-  const int d = 8 * u;
-  widen8<BF16>(__ldg(reinterpret_cast<const uint4*>(row + d)), lo);
-  widen8<BF16>(__ldg(reinterpret_cast<const uint4*>(row + d + rot / 2)), hi);
-  const float4* t = reinterpret_cast<const float4*>(cs + d);
+  return g;
+}
+
+// The fp32 values of a unit after the rotation: lo, and hi of a pair unit.
+template <bool BF16, class A>
+__device__ __forceinline__ void turn_unit(const RawUnit& r, const UnitAt& a, const A& g,
+                                          int interleaved, float sign, float (&lo)[8], float (&hi)[8]) {
+  widen8<BF16>(r.lo, lo);
+  if (!a.turned) return;
+  if (interleaved) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 c = __ldg(t + i);
-    turn(lo[2 * i], hi[2 * i], make_float2(c.x, sign * c.y));
-    turn(lo[2 * i + 1], hi[2 * i + 1], make_float2(c.z, sign * c.w));
+    for (int i = 0; i < 2; ++i) {
+      const float4 c = g[i];
+      turn(lo[4 * i], lo[4 * i + 1], make_float2(c.x, sign * c.y));
+      turn(lo[4 * i + 2], lo[4 * i + 3], make_float2(c.z, sign * c.w));
+    }
+  } else {
+    widen8<BF16>(r.hi, hi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 c = g[i];
+      turn(lo[2 * i], hi[2 * i], make_float2(c.x, sign * c.y));
+      turn(lo[2 * i + 1], hi[2 * i + 1], make_float2(c.z, sign * c.w));
+    }
   }
-  return d;
+}
+
+// The unit stored in its rows' type; what is not turned is copied bit by bit.
+template <bool BF16, class A>
+__device__ __forceinline__ void store_turned(uint16_t* row, const RawUnit& r, const UnitAt& a,
+                                             const A& g, int rot, int interleaved, float sign) {
+  uint4* dst = reinterpret_cast<uint4*>(row + a.d);
+  if (!a.turned) {
+    *dst = r.lo;
+    return;
+  }
+  float lo[8], hi[8];
+  turn_unit<BF16>(r, a, g, interleaved, sign, lo, hi);
+  *dst = narrow8<BF16>(lo);
+  if (a.pair) *reinterpret_cast<uint4*>(row + a.d + rot / 2) = narrow8<BF16>(hi);
 }
 
 // Two fp32 values to e4m3, nearest even, saturating; a NaN stays one.

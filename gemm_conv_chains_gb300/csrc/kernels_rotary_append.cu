@@ -5,51 +5,183 @@
 namespace b2b {
 
 // ------------------------------------------------------------------------------------
-// rotary positions
+// rows of heads turned: rotary positions, and the queries of an append
 // ------------------------------------------------------------------------------------
 // y_a = x_a c - x_b s, y_b = x_b c + x_a s for each channel pair (a, b) of a head's first
 // `rot` channels, (c, s) the table's row of the token's position; the inverse takes -s and
 // is also the gradient, the rotation being orthogonal.  Every element is read and written
-// once and takes three operations: HBM bound.  A thread owns one 16-byte vector (its
-// partner vector too in the half layout), so that both layouts load and store whole
-// sectors, and a block owns whole tokens, so that the heads of a token share its table
-// row in L1.
+// once and takes two operations: HBM bound, if enough of it is in flight.  A thread keeps one
+// unit of a row (16 bytes, or two times 16 that are partners in the half layout; whole sectors
+// either way) for all the heads and tokens that it walks, its angles in registers, and copies
+// what it will turn into a ring of its own in shared memory, kAhead units ahead (cp.async, no
+// barrier: it reads back what it copied itself).  Without the ring the same walk ran 79 us on
+// 16384 tokens of 40 heads (4.2 TB/s), whether a thread asked for one, two or four units at a
+// time in registers: more registers per thread cost as many threads.
+constexpr int kTurnThreads = 256;
+constexpr int kAhead = 8;
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+struct TurnRows {
+  const uint16_t* x;
+  uint16_t* out;
+  const float2* table;
+  int64_t ldx, ldo, table_len;
+  int H, D, rot, interleaved;
+  float sign;
+};
+
+// One unit per thread and step, straight from global to global memory: few registers, so that
+// many threads hide the latency of short calls.
 template <bool BF16>
-__global__ void __launch_bounds__(256) rotary_kernel(const RotaryParams p, int units,
-                                                     int tokens_per_block) {
-  const int row_units_total = p.H * units;
-  const bool in_place = p.x == p.out && p.ldx == p.ldo;
-  for (int j = threadIdx.x; j < row_units_total * tokens_per_block; j += blockDim.x) {
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * tokens_per_block + j / row_units_total;
-    if (t >= p.T) break;
-    const int r = j % row_units_total;
-    const int h = r / units, u = r % units;
-    const int pos = __ldg(p.positions + t);
-    if (pos < 0 || pos >= p.table_len) {
-      index_error(p.err, DK_ROTARY, DEC_ERR_POSITION, static_cast<uint32_t>(t));
-      continue;
+__device__ __forceinline__ void turn_one(const TurnRows& r, int64_t t, int h, int u, int pos) {
+  const UnitAt at = unit_at(u, r.rot, r.interleaved);
+  if (!at.turned && r.x == r.out && r.ldx == r.ldo) return;      // in place: nothing to copy
+  const RawUnit raw = load_raw(r.x + t * r.ldx + static_cast<int64_t>(h) * r.D, at, r.rot);
+  const AngleRow g = angle_row(r.table + static_cast<int64_t>(pos) * (r.rot / 2), at, r.interleaved);
+  store_turned<BF16>(r.out + t * r.ldo + static_cast<int64_t>(h) * r.D, raw, at, g, r.rot,
+                     r.interleaved, r.sign);
+}
+
+// Turns rows [t0, t1); position(t) gives a row's position, or -1 for a row to leave out.  Threads:
+// (units, groups of heads, rows side by side where they are short) in x, idle beyond.
+template <bool BF16, class Position>
+__device__ __forceinline__ void turn_rows(const TurnRows& r, int64_t t0, int64_t t1, int units,
+                                          Position position) {
+  extern __shared__ __align__(16) uint4 ring[];
+  const int groups = static_cast<int>(blockDim.x) / units;
+  const int G = groups < r.H ? groups : r.H, Z = groups / G;     // heads and rows side by side
+  const int group = static_cast<int>(threadIdx.x) / units;
+  const int z = group / G, first = group - z * G;
+  const UnitAt at = unit_at(threadIdx.x - group * units, r.rot, r.interleaved);
+  const bool in_place = r.x == r.out && r.ldx == r.ldo;
+  if (z >= Z || (in_place && !at.turned)) return;
+  t0 += z;
+  const int mine = (r.H - first + G - 1) / G;                    // heads of this thread per row
+  const int64_t step = static_cast<int64_t>(G) * r.D;
+  const uint32_t ring_at = smem_u32(ring) + threadIdx.x * 16;
+  const uint32_t part = blockDim.x * 16;
+
+  int64_t row = t0;                                              // of the next unit to copy
+  int k = 0, slot = 0;
+  const uint16_t* src = r.x + t0 * r.ldx + static_cast<int64_t>(first) * r.D + at.d;
+  auto copy = [&]() {
+    if (row < t1) {
+      const uint32_t dst = ring_at + slot * 2 * part;
+      copy16(dst, src);
+      if (at.pair) copy16(dst + part, src + r.rot / 2);
+      src += step;
+      if (++k == mine) {
+        k = 0;
+        src += Z * r.ldx - mine * step;
+        row += Z;
+      }
     }
-    const uint16_t* row = p.x + t * p.ldx + static_cast<int64_t>(h) * p.D;
-    uint16_t* dst = p.out + t * p.ldo + static_cast<int64_t>(h) * p.D;
-    if (in_place && (p.interleaved ? 8 * u >= p.rot : u >= p.rot / 16)) continue;
-    float lo[8], hi[8];
-    bool pair;
-    const int d = load_unit<BF16>(row, p.table + static_cast<int64_t>(pos) * (p.rot / 2), u, p.rot,
-                                  p.interleaved, p.inverse != 0, lo, hi, pair);
-    *reinterpret_cast<uint4*>(dst + d) = narrow8<BF16>(lo);
-    if (pair) *reinterpret_cast<uint4*>(dst + d + p.rot / 2) = narrow8<BF16>(hi);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    slot = slot + 1 == kAhead ? 0 : slot + 1;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kAhead - 1; ++i) copy();
+
+  int pos = t0 < t1 ? position(t0) : -1;
+  int read = 0;
+  for (int64_t t = t0; t < t1; t += Z) {
+    Angles g;
+    if (pos >= 0) g = load_angles(r.table + static_cast<int64_t>(pos) * (r.rot / 2), at, r.interleaved);
+    const int next = t + Z < t1 ? position(t + Z) : -1;
+    uint16_t* dst = r.out + t * r.ldo + static_cast<int64_t>(first) * r.D;
+    for (int j = 0; j < mine; ++j, dst += step) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+      RawUnit raw;
+      raw.lo = ring[threadIdx.x + read * 2 * blockDim.x];
+      raw.hi = at.pair ? ring[threadIdx.x + (read * 2 + 1) * blockDim.x] : raw.lo;
+      read = read + 1 == kAhead ? 0 : read + 1;
+      if (pos >= 0) store_turned<BF16>(dst, raw, at, g, r.rot, r.interleaved, r.sign);
+      copy();
+    }
+    pos = next;
   }
 }
 
-cudaError_t launch_rotary(bool bf16, const RotaryParams& p, cudaStream_t s) {
-  const int units = p.interleaved ? p.D / 8 : p.rot / 16 + (p.D - p.rot) / 8;
+// Threads and shared memory of a block that turns rows of H heads.
+int turn_units(int D, int rot, int interleaved) {
+  return interleaved ? D / 8 : rot / 16 + (D - rot) / 8;
+}
+constexpr int kTurnSmem = kAhead * 2 * kTurnThreads * 16;
+
+// Rows per block of the walk: about 16 units per thread, or 0 where that leaves too few blocks to
+// fill the SMs twice over, and one unit per thread is faster (8193 rows of 12 heads of 64: 5.3 us
+// against 7.5; 16384 rows of 40 heads of 128: 79 us against 68).
+int64_t turn_rows_per_block(int64_t T, int H, int units) {
+  const int64_t per_row = static_cast<int64_t>(H) * units;
+  const int64_t rows = (16 * kTurnThreads + per_row - 1) / per_row;
+  return T / rows >= 1024 ? rows : 0;
+}
+
+// position(t) of rotary: the given one, if the table has it.
+__device__ __forceinline__ int rotary_position(const RotaryParams& p, int64_t t) {
+  const int pos = __ldg(p.positions + t);
+  if (pos >= 0 && pos < p.table_len) return pos;
+  index_error(p.err, DK_ROTARY, DEC_ERR_POSITION, static_cast<uint32_t>(t));
+  return -1;
+}
+
+__device__ __forceinline__ TurnRows rows_of(const RotaryParams& p) {
+  return TurnRows{p.x, p.out, p.table, p.ldx, p.ldo, p.table_len, p.H, p.D, p.rot, p.interleaved,
+                  p.inverse ? -1.f : 1.f};
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kTurnThreads, 3) rotary_walk_kernel(const RotaryParams p, int units,
+                                                                      int64_t rows) {
+  const int64_t t0 = blockIdx.x * rows, t1 = t0 + rows < p.T ? t0 + rows : p.T;
+  turn_rows<BF16>(rows_of(p), t0, t1, units, [&](int64_t t) { return rotary_position(p, t); });
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kTurnThreads) rotary_kernel(const RotaryParams p, int units,
+                                                              int tokens_per_block) {
   const int per_token = p.H * units;
-  const int tpb = per_token >= 256 ? 1 : 256 / per_token;
-  const int64_t blocks = (p.T + tpb - 1) / tpb;
+  for (int j = threadIdx.x; j < per_token * tokens_per_block; j += blockDim.x) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * tokens_per_block + j / per_token;
+    if (t >= p.T) break;
+    const int q = j % per_token;
+    const int pos = rotary_position(p, t);
+    if (pos >= 0) turn_one<BF16>(rows_of(p), t, q / units, q % units, pos);
+  }
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device.
+cudaError_t allow_smem(const void* fn, int bytes, int& set_on) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || set_on == dev) return e;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) set_on = dev;
+  return e;
+}
+
+cudaError_t launch_rotary(bool bf16, const RotaryParams& p, cudaStream_t s) {
+  const int units = turn_units(p.D, p.rot, p.interleaved);
+  if (units > kTurnThreads) return cudaErrorInvalidConfiguration;
+  if (const int64_t rows = turn_rows_per_block(p.T, p.H, units); rows > 0) {
+    static thread_local int set_on[2] = {-1, -1};
+    auto* fn = bf16 ? rotary_walk_kernel<true> : rotary_walk_kernel<false>;
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), kTurnSmem, set_on[bf16]);
+        e != cudaSuccess)
+      return e;
+    fn<<<static_cast<unsigned>((p.T + rows - 1) / rows), kTurnThreads, kTurnSmem, s>>>(p, units, rows);
+    return cudaGetLastError();
+  }
+  const int per_token = p.H * units;
+  const int tpb = per_token >= kTurnThreads ? 1 : kTurnThreads / per_token;
+  const unsigned blocks = static_cast<unsigned>((p.T + tpb - 1) / tpb);
   if (bf16)
-    rotary_kernel<true><<<static_cast<unsigned>(blocks), 256, 0, s>>>(p, units, tpb);
+    rotary_kernel<true><<<blocks, kTurnThreads, 0, s>>>(p, units, tpb);
   else
-    rotary_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, s>>>(p, units, tpb);
+    rotary_kernel<false><<<blocks, kTurnThreads, 0, s>>>(p, units, tpb);
   return cudaGetLastError();
 }
 
@@ -99,99 +231,146 @@ cudaError_t launch_rotary_table(float2* table, int64_t n, int32_t half, const do
 // append to the paged e4m3 cache
 // ------------------------------------------------------------------------------------
 // One block per page that a sequence's new tokens touch, kv head, and pool (keys or
-// values); further blocks rotate the queries.  With A the largest finite magnitude of the
-// block's new values (keys after the rotation) and s the page's scale if it already holds
-// older tokens of the sequence, else 0:
-//   s' = max(s, A / 448, 2^-64);  new codes e4m3(y / s'), saturating;
+// values).  With A the largest finite magnitude of the block's new values (keys after the
+// rotation) and s the page's scale if it already holds older tokens of the sequence, else 0:
+//   s' = max(s, A / 448, 2^-64);  new codes e4m3(y (1 / s')), saturating;
 //   older codes e4m3(code * (s / s')) if s' > s, else untouched.
-// The new tokens are read twice (the maximum first), the second time from L1 or L2: a page
-// of new tokens is at most 128 KB.  The rest is one pass; with one new token per sequence
-// a call is bound by its latency (three dependent loads before the first store).
+// A thread keeps one unit of a row, asks for its first tokens' along with the page number and holds
+// them between the maximum and the codes; what a page has beyond that is read twice, the second
+// time from L1 or L2.  One new token per sequence is bound by the latency of its dependent loads
+// (sequence, page number and tokens, scale); prompts by the instructions per element, 0.6 of the
+// issue slots (ragged prompts, 18 k tokens, 8 heads of 128, pages of 32: 72 us with an index
+// division per unit and an exact division per element, 36 us so).
+// The queries of few tokens are turned by further blocks of the same launch; those of many by a
+// launch of the walk above.
 constexpr int kAppendThreads = 128;
 
-template <bool BF16>
-__device__ __forceinline__ void append_page(const AppendParams& p, int b, int j, int h, bool value,
-                                            float* shared) {
+// The largest magnitude (a NaN is none), or only of the finite ones.
+template <bool FINITE>
+__device__ __forceinline__ void most_of(const float (&v)[8], float& most) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float a = fabsf(v[e]);
+    if (!FINITE || a <= 3.402823466e38f) most = fmaxf(most, a);
+  }
+}
+
+// Eight values as codes, the scale's reciprocal given.
+__device__ __forceinline__ void store_codes(uint8_t* dst, const float (&v)[8], float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = e4m3x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// The block's maximum of a value per thread.
+__device__ __forceinline__ float block_max(float v) {
+  __shared__ float shared[kAppendThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kAppendThreads / 32; ++w) v = fmaxf(v, shared[w]);
+  return v;
+}
+
+// ROTATION: 0 none (values, or keys as they are), 1 interleaved, 2 half.  Each is compiled by
+// itself: the pairs of the half layout alone hold twice the registers.
+template <bool BF16, int ROTATION>
+__device__ __forceinline__ void append_page(const AppendParams& p, int b, int j, int h, bool value) {
   const CacheView& c = p.c;
   const Sequence s = load_sequence(c, b, DK_APPEND);
   if (s.n == 0) return;
   const int page = 1 << c.page_shift;
   const int start = s.len - s.n;
-  const int64_t pi = (start >> c.page_shift) + static_cast<int64_t>(j);
-  const int64_t first_slot = pi << c.page_shift;
-  if (first_slot >= s.len) return;
-  const int64_t lo_tok = first_slot > start ? first_slot : start;
-  const int64_t hi_tok = first_slot + page < s.len ? first_slot + page : s.len;
-  const int held = first_slot < start ? static_cast<int>(start - first_slot) : 0;
-  const int count = static_cast<int>(hi_tok - lo_tok);
+  const int first_page = start >> c.page_shift;
+  if (j > ((s.len - 1) >> c.page_shift) - first_page) return;
+  const int pi = first_page + j;
+  const int first_slot = pi << c.page_shift;
+  const int lo_tok = first_slot > start ? first_slot : start;
+  const int hi_tok = s.len - first_slot > page ? first_slot + page : s.len;
+  const int held = first_slot < start ? start - first_slot : 0;
   const int id = __ldg(c.page_table + static_cast<int64_t>(b) * c.max_pages + pi);
+  const int rot = ROTATION != 0 ? p.rot : 0;
+  constexpr int inter = ROTATION != 2;                // without a rotation: plain vectors
+  const int units = row_units(c.D, rot, inter);
+  const int64_t ld = value ? p.ldv : p.ldk;
+  const uint16_t* src = (value ? p.v : p.k) + (s.row + (lo_tok - start)) * ld +
+                        static_cast<int64_t>(h) * c.D;
+  const float2* cs = p.table + static_cast<int64_t>(lo_tok) * (rot / 2);
+  // this thread's unit of every row, and its tokens first, first + G, ...
+  const int G = kAppendThreads / units, first = static_cast<int>(threadIdx.x) / units;
+  UnitAt at = unit_at(threadIdx.x - first * units, rot, inter);
+  if (ROTATION == 0) at.turned = false;
+  if (ROTATION != 2) at.pair = false;
+  const int count = first < G ? hi_tok - lo_tok : 0;
+  // the first of them are asked for together with the page number
+  constexpr int kHeld = ROTATION == 2 ? 2 : 4;        // a pair unit is two vectors
+  RawUnit held_raw[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (first + k * G < count) held_raw[k] = load_raw(src + (first + k * G) * ld, at, rot);
   if (id < 0 || id >= c.pages) {
     if (threadIdx.x == 0) index_error(c.err, DK_APPEND, DEC_ERR_PAGE, static_cast<uint32_t>(b));
     return;
   }
-  const bool rotate = !value && p.table != nullptr;
-  if (rotate && hi_tok > p.table_len) {
+  if (ROTATION != 0 && hi_tok > p.table_len) {
     if (threadIdx.x == 0) index_error(c.err, DK_APPEND, DEC_ERR_POSITION, static_cast<uint32_t>(b));
     return;
   }
-  const int64_t at = static_cast<int64_t>(id) * c.heads + h;
-  float* scale_at = (value ? c.v_scale : c.k_scale) + at;
-  uint8_t* codes = (value ? c.v : c.k) + (at << c.page_shift) * c.D;
+  const int64_t page_at = static_cast<int64_t>(id) * c.heads + h;
+  float* scale_at = (value ? c.v_scale : c.k_scale) + page_at;
+  uint8_t* codes = (value ? c.v : c.k) + (page_at << c.page_shift) * c.D;
   const float before = held > 0 ? *scale_at : 0.f;
 
-  const int rot = rotate ? p.rot : 0;
-  const int inter = rotate ? p.interleaved : 1;       // without a rotation: plain vectors
-  const int units = row_units(c.D, rot, inter);
-  const int64_t ld = value ? p.ldv : p.ldk;
-  const uint16_t* src = (value ? p.v : p.k) +
-                        (s.row + (lo_tok - start)) * ld + static_cast<int64_t>(h) * c.D;
-  float lo[8], hi[8];
-  bool pair = false;
+  // this thread's units, turned: f(token, lo, hi)
+  auto each = [&](auto f) {
+    float lo[8], hi[8];
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      const int tok = first + k * G;
+      if (tok >= count) break;
+      turn_unit<BF16>(held_raw[k], at, angle_row(cs + tok * (rot / 2), at, inter), inter, 1.f, lo, hi);
+      f(tok, lo, hi);
+    }
+#pragma unroll 1
+    for (int tok = first + kHeld * G; tok < count; tok += G) {
+      turn_unit<BF16>(load_raw(src + tok * ld, at, rot), at, angle_row(cs + tok * (rot / 2), at, inter),
+                      inter, 1.f, lo, hi);
+      f(tok, lo, hi);
+    }
+  };
   float most = 0.f;
-  const int total = count * units;
-  for (int i = threadIdx.x; i < total; i += kAppendThreads) {
-    const int tok = i / units, u = i - tok * units;
-    load_unit<BF16>(src + tok * ld, p.table + (lo_tok + tok) * (rot / 2), u, rot, inter, false, lo,
-                    hi, pair);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float a = fabsf(lo[e]), z = pair ? fabsf(hi[e]) : 0.f;
-      if (a <= 3.402823466e38f) most = fmaxf(most, a);
-      if (z <= 3.402823466e38f) most = fmaxf(most, z);
-    }
+  each([&](int, const float (&lo)[8], const float (&hi)[8]) {
+    most_of<false>(lo, most);
+    if (at.pair) most_of<false>(hi, most);
+  });
+  most = block_max(most);
+  if (most > 3.402823466e38f) {                      // an infinity among them: without those, then
+    most = 0.f;
+    each([&](int, const float (&lo)[8], const float (&hi)[8]) {
+      most_of<true>(lo, most);
+      if (at.pair) most_of<true>(hi, most);
+    });
+    most = block_max(most);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = most;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kAppendThreads / 32; ++w) most = fmaxf(most, shared[w]);
   const float after = fmaxf(fmaxf(before, __fdiv_rn(most, kE4m3Max)), kScaleMin);
+  const float inv = __fdiv_rn(1.f, after);
 
-  for (int i = threadIdx.x; i < total; i += kAppendThreads) {
-    const int tok = i / units, u = i - tok * units;
-    const int d = load_unit<BF16>(src + tok * ld, p.table + (lo_tok + tok) * (rot / 2), u, rot,
-                                  inter, false, lo, hi, pair);
-    uint8_t* dst = codes + static_cast<int64_t>(lo_tok - first_slot + tok) * c.D + d;
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = e4m3x2(__fdiv_rn(lo[2 * e], after), __fdiv_rn(lo[2 * e + 1], after));
-    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-    if (pair) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = e4m3x2(__fdiv_rn(hi[2 * e], after), __fdiv_rn(hi[2 * e + 1], after));
-      *reinterpret_cast<uint2*>(dst + rot / 2) =
-          make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-    }
-  }
+  uint8_t* dst = codes + (lo_tok - first_slot) * c.D + at.d;
+  each([&](int tok, const float (&lo)[8], const float (&hi)[8]) {
+    store_codes(dst + tok * c.D, lo, inv);
+    if (at.pair) store_codes(dst + tok * c.D + rot / 2, hi, inv);
+  });
   if (held > 0 && after > before) {
     const float ratio = __fdiv_rn(before, after);
     uint2* old = reinterpret_cast<uint2*>(codes);
     for (int i = threadIdx.x; i < held * c.D / 8; i += kAppendThreads) {
-      uint2 w = old[i];
-      uint32_t in[2] = {w.x, w.y}, out[2];
+      const uint2 w = old[i];
+      const uint32_t in[2] = {w.x, w.y};
+      uint32_t out[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         uint32_t a, z;
@@ -206,60 +385,75 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int b, int j,
   if (threadIdx.x == 0 && after != before) *scale_at = after;
 }
 
-// The sequence that row t of the new tokens belongs to: the last b with starts[b] <= t.
+// The sequence that row t of the new tokens belongs to: the last b with starts[b] <= t.  Whole
+// warp; the loads of a step are independent.
 __device__ __forceinline__ int sequence_of(const CacheView& c, int64_t t) {
   if (c.starts == nullptr) return static_cast<int>(t / (c.T / c.B));
-  int lo = 0, hi = c.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(c.starts + mid) <= t) lo = mid;
-    else hi = mid;
+  const int lane = threadIdx.x & 31;
+  int count = 0;
+  for (int b0 = 0; b0 < c.B; b0 += 32) {
+    const bool in = b0 + lane < c.B && __ldg(c.starts + b0 + lane) <= t;
+    const uint32_t vote = __ballot_sync(0xffffffffu, in);
+    count += __popc(vote);
+    if (vote != 0xffffffffu) break;
   }
-  return lo;
+  return count > 0 ? count - 1 : 0;
+}
+
+// Walks the sequences along ascending rows: the position of row t, or -1.
+struct QueryPosition {
+  const AppendParams& p;                             // the kernel's own argument
+  int b;
+  Sequence s;
+  __device__ __forceinline__ QueryPosition(const AppendParams& p_, int64_t t0)
+      : p(p_), b(sequence_of(p_.c, t0)), s(load_sequence(p_.c, b, DK_APPEND)) {}
+  __device__ __forceinline__ int operator()(int64_t t) {
+    while (t >= static_cast<int64_t>(s.row) + s.n && b + 1 < p.c.B)
+      s = load_sequence(p.c, ++b, DK_APPEND);
+    const int64_t i = t - s.row;
+    if (i < 0 || i >= s.n) return -1;
+    const int pos = static_cast<int>(s.len - s.n + i);
+    if (pos < p.table_len) return pos;
+    index_error(p.c.err, DK_APPEND, DEC_ERR_POSITION, static_cast<uint32_t>(b));
+    return -1;
+  }
+};
+
+__device__ __forceinline__ TurnRows rows_of(const AppendParams& p) {
+  return TurnRows{p.q, p.q_out, p.table, p.ldq, p.ldqo, p.table_len, p.q_heads, p.c.D, p.rot,
+                  p.interleaved, 1.f};
 }
 
 template <bool BF16>
-__device__ __forceinline__ void rotate_queries(const AppendParams& p, int64_t t) {
-  const CacheView& c = p.c;
-  const int b = sequence_of(c, t);
-  const Sequence s = load_sequence(c, b, DK_APPEND);
-  const int64_t i = t - s.row;
-  if (i < 0 || i >= s.n) return;
-  const int64_t pos = s.len - s.n + i;
-  if (pos >= p.table_len) {
-    if (threadIdx.x == 0) index_error(c.err, DK_APPEND, DEC_ERR_POSITION, static_cast<uint32_t>(b));
-    return;
-  }
-  const int units = row_units(c.D, p.rot, p.interleaved);
-  const float2* cs = p.table + pos * (p.rot / 2);
-  for (int j = threadIdx.x; j < p.q_heads * units; j += kAppendThreads) {
-    const int h = j / units, u = j - h * units;
-    float lo[8], hi[8];
-    bool pair;
-    const int d = load_unit<BF16>(p.q + t * p.ldq + static_cast<int64_t>(h) * c.D, cs, u, p.rot,
-                                  p.interleaved, false, lo, hi, pair);
-    uint16_t* dst = p.q_out + t * p.ldqo + static_cast<int64_t>(h) * c.D + d;
-    *reinterpret_cast<uint4*>(dst) = narrow8<BF16>(lo);
-    if (pair) *reinterpret_cast<uint4*>(dst + p.rot / 2) = narrow8<BF16>(hi);
-  }
+__global__ void __launch_bounds__(kTurnThreads, 3) query_walk_kernel(const AppendParams p, int units,
+                                                                     int64_t rows) {
+  const int64_t t0 = blockIdx.x * rows, t1 = t0 + rows < p.c.T ? t0 + rows : p.c.T;
+  QueryPosition position(p, t0);
+  turn_rows<BF16>(rows_of(p), t0, t1, units, [&](int64_t t) { return position(t); });
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p,
+template <bool BF16, int ROTATION>
+__global__ void __launch_bounds__(kAppendThreads, 8) append_kernel(const AppendParams p,
                                                                 int64_t page_blocks,
                                                                 int pages_per_seq) {
-  __shared__ float shared[kAppendThreads / 32];
   const int64_t x = blockIdx.x;
-  if (x >= page_blocks) {
-    rotate_queries<BF16>(p, x - page_blocks);
+  if (ROTATION != 0 && x >= page_blocks) {           // one token's queries
+    const int64_t t = x - page_blocks;
+    const int units = row_units(p.c.D, p.rot, p.interleaved);
+    QueryPosition position(p, t);
+    const int pos = position(t);
+    if (pos < 0) return;
+    for (int j = threadIdx.x; j < p.q_heads * units; j += kAppendThreads)
+      turn_one<BF16>(rows_of(p), t, j / units, j % units, pos);
     return;
   }
   const int value = static_cast<int>(x & 1);
-  int64_t r = x >> 1;
+  uint32_t r = static_cast<uint32_t>(x >> 1);
   const int h = static_cast<int>(r % p.c.heads);
   r /= p.c.heads;
-  append_page<BF16>(p, static_cast<int>(r / pages_per_seq), static_cast<int>(r % pages_per_seq), h,
-                    value != 0, shared);
+  const int b = static_cast<int>(r / pages_per_seq), j = static_cast<int>(r % pages_per_seq);
+  if (value) append_page<BF16, 0>(p, b, j, h, true);
+  else append_page<BF16, ROTATION>(p, b, j, h, false);
 }
 
 cudaError_t launch_append(bool bf16, const AppendParams& p, cudaStream_t s) {
@@ -267,14 +461,21 @@ cudaError_t launch_append(bool bf16, const AppendParams& p, cudaStream_t s) {
   // max_new tokens from any slot on touch at most this many pages
   const int per_seq = (p.c.max_new - 1 + page - 1) / page + 1;
   const int64_t page_blocks = static_cast<int64_t>(p.c.B) * per_seq * p.c.heads * 2;
-  const int64_t blocks = page_blocks + (p.q != nullptr ? p.c.T : 0);
+  const int units = turn_units(p.c.D, p.rot, p.interleaved);
+  const int64_t rows = p.q != nullptr ? turn_rows_per_block(p.c.T, p.q_heads, units) : 0;
+  const int64_t blocks = page_blocks + (p.q != nullptr && rows == 0 ? p.c.T : 0);
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  if (bf16)
-    append_kernel<true><<<static_cast<unsigned>(blocks), kAppendThreads, 0, s>>>(p, page_blocks,
-                                                                                 per_seq);
-  else
-    append_kernel<false><<<static_cast<unsigned>(blocks), kAppendThreads, 0, s>>>(p, page_blocks,
-                                                                                  per_seq);
+  auto* append = p.table == nullptr ? (bf16 ? append_kernel<true, 0> : append_kernel<false, 0>)
+                 : p.interleaved    ? (bf16 ? append_kernel<true, 1> : append_kernel<false, 1>)
+                                    : (bf16 ? append_kernel<true, 2> : append_kernel<false, 2>);
+  append<<<static_cast<unsigned>(blocks), kAppendThreads, 0, s>>>(p, page_blocks, per_seq);
+  if (cudaError_t e = cudaGetLastError(); e != cudaSuccess || rows == 0) return e;
+  static thread_local int set_on[2] = {-1, -1};
+  auto* fn = bf16 ? query_walk_kernel<true> : query_walk_kernel<false>;
+  if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), kTurnSmem, set_on[bf16]);
+      e != cudaSuccess)
+    return e;
+  fn<<<static_cast<unsigned>((p.c.T + rows - 1) / rows), kTurnThreads, kTurnSmem, s>>>(p, units, rows);
   return cudaGetLastError();
 }
 

@@ -240,7 +240,7 @@ b2b_status b2b_rotary_table(int64_t positions, int32_t rot, double base, b2b_rot
  * gradient: dx = inverse rotation of dy (exactly so for gain 1; with another gain both carry
  * it).  x, out: T rows of H x D, strides ldx, ldo; out may be x (same stride) for an in-place
  * rotation, and must not overlap it otherwise.  positions: device int32 [T].
- * D a multiple of 8, rot a multiple of 16, rot <= D. */
+ * D a multiple of 8 up to 2048, rot a multiple of 16, rot <= D. */
 b2b_status b2b_rotary(b2b_dtype dt, int64_t T, int32_t H, int32_t D, int32_t rot,
                       b2b_rotary_layout layout, int32_t inverse, const void* x, int64_t ldx,
                       const float* table, int64_t positions_in_table, const int32_t* positions,
@@ -273,7 +273,7 @@ typedef struct b2b_cache {
  * the queries q -> q_out when q is given (q_out may be q).  For each page touched and kv head,
  * A the largest finite magnitude of its new values and s its scale if it already holds older
  * tokens of the sequence (else 0):
- *   s' = max(s, A / 448, 2^-64),   new codes = e4m3(y / s'),
+ *   s' = max(s, A / 448, 2^-64),   new codes = e4m3(y * (1 / s')),
  *   and where s' > s the page's older codes become e4m3(code * (s / s'))
  * in fp32, to nearest even, saturating (an infinity becomes +-448 s'; a NaN stays one).  Calling
  * again with the same arguments changes nothing.  Pages that are written belong to one
