@@ -139,7 +139,7 @@ struct CacheDims {
 template <int D, int NT>
 constexpr int attend_smem() {
   constexpr int ring = kAttendWarps * CacheDims<D, NT>::kRing;
-  constexpr int join = kAttendWarps * NT * 8 * (D + 2) * 4;
+  constexpr int join = kAttendWarps * NT * 8 * (D + 6) * 4;
   return (ring > join ? ring : join) + kAttendWarps * CacheDims<D, NT>::kStages * 8 +
          (NT > 1 ? D / 16 * NT * 256 : 0) + NT * 8 * 4;
 }
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
   const int g = lane >> 2, t = lane & 3;
   const CacheView& c = p.c;
 
-  constexpr int kJoin = kAttendWarps * RT * (D + 2) * 4;
+  constexpr int kJoin = kAttendWarps * RT * (D + 6) * 4;
   constexpr int kBody = kAttendWarps * C::kRing > kJoin ? kAttendWarps * C::kRing : kJoin;
   uint8_t* ring = smem + warp * C::kRing;
   const uint32_t ring_at = smem_u32(ring);
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
     uint32_t qf[NT == 1 ? KS : 1][2];
     float qfactor[NT][2];                            // of rows 8 nt + 2 t, + 1
     int limit[NT][2];                                // last key each of them sees
-    float slope[NT][2];
+    float slope[NT][2], behind[NT][2];               // behind: of the tile's last row, tokens
     {
       float amax = 0.f;
 #pragma unroll
@@ -409,6 +409,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
         qfactor[nt][i] = row_units[8 * nt + 2 * t + i] * p.scale * (MODS ? 1.f : kLog2e);
         limit[nt][i] = valid ? start + tq : 0x7FFFFFFF;
         slope[nt][i] = 0.f;
+        behind[nt][i] = static_cast<float>(valid ? high_limit - limit[nt][i] : 0);
         if (MODS && p.slopes != nullptr && valid)
           slope[nt][i] = __ldg(p.slopes + h * p.group + (r - tq * p.group));
       }
@@ -465,6 +466,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
       const int tok0 = strip * kStrip + C::token_of_row(g);   // of x[.][0], x[.][1]; + 8: of x[.][2], x[.][3]
       const bool edge = strip * kStrip + kStrip - 1 > low_limit;
       // scores in the log2 domain
+      const float away = MODS ? static_cast<float>(tok0 - high_limit) : 0.f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -474,8 +476,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
             if (p.softcap > 0.f)                     // cap tanh(z / cap); tanh y = 1 - 2 / (e^2y + 1)
               z = p.softcap - 2.f * p.softcap *
                       rcp_fast(exp2_fast(z * (2.f * kLog2e / p.softcap)) + 1.f);
-            z += slope[nt][e & 1] * static_cast<float>(tok0 + 8 * (e >> 1) - limit[nt][e & 1]);
-            z *= kLog2e;
+            z = fmaf(slope[nt][e & 1], away + static_cast<float>(8 * (e >> 1)) + behind[nt][e & 1], z) * kLog2e;
           }
           if (edge && tok0 + 8 * (e >> 1) > limit[nt][e & 1]) z = -INFINITY;
           x[nt][e] = z;
@@ -621,18 +622,23 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
       }
     __syncthreads();                                 // every ring is drained
     float* join = reinterpret_cast<float*>(smem);
-    float* mine = join + warp * RT * D;
-    float2* stats = reinterpret_cast<float2*>(join + kAttendWarps * RT * D);
+    // rows of D + 4 floats; the pairs of a 16-channel block change places by the block, so that the
+    // lanes of a store, whose channels are 16 apart, meet few banks twice
+    constexpr int kRow = D + 4;
+    auto place = [](int d) { return (d & ~15) | ((d & 15) ^ (((d >> 4) & 7) << 1)); };
+    float* mine = join + warp * RT * kRow;
+    float2* stats = reinterpret_cast<float2*>(join + kAttendWarps * RT * kRow);
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
       const int w = i / 2;
-      const int d = C::kVRun * (C::value_run(g) + 8 * (4 * w / C::kVRun)) + (4 * w) % C::kVRun + 2 * (i & 1);
+      const int d =
+          place(C::kVRun * (C::value_run(g) + 8 * (4 * w / C::kVRun)) + (4 * w) % C::kVRun + 2 * (i & 1));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int r = 8 * nt + 2 * t;
-        *reinterpret_cast<float2*>(mine + r * D + d) =
+        *reinterpret_cast<float2*>(mine + r * kRow + d) =
             make_float2(o[i][nt][0] * vref, o[i][nt][2] * vref);
-        *reinterpret_cast<float2*>(mine + (r + 1) * D + d) =
+        *reinterpret_cast<float2*>(mine + (r + 1) * kRow + d) =
             make_float2(o[i][nt][1] * vref, o[i][nt][3] * vref);
       }
     }
@@ -662,12 +668,13 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
       for (int w = 0; w < kAttendWarps; ++w) {
         const float f = exp2_fast(st[w].x - top);
         sum += f * st[w].y;
-        const float4 v = *reinterpret_cast<const float4*>(join + (w * RT + r) * D + d);
+        const float4 v = *reinterpret_cast<const float4*>(join + (w * RT + r) * kRow + (place(d) & ~3));
         acc.x += f * v.x;
         acc.y += f * v.y;
         acc.z += f * v.z;
         acc.w += f * v.w;
       }
+      if ((d >> 4) & 1) acc = make_float4(acc.z, acc.w, acc.x, acc.y);   // an odd block: pairs swapped
       const float inv = sum == 0.f ? 0.f : 1.f / sum;     // a row that sees no key is zero
       acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       if (partial) {
