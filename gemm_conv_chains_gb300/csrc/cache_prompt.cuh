@@ -32,9 +32,9 @@ namespace b2b {
 constexpr int kPromptRows = 256;       // query rows of a CTA: two M = 128 tiles
 constexpr int kPromptKeys = 128;       // keys per tile
 constexpr int kPromptThreads = 640;
-// Registers per thread of the softmax, producer and MMA warpgroups: 2 x 152 + 2 x 72 + 32 <= 5 x 96,
+// Registers per thread of the softmax, producer and MMA warpgroups: 2 x 136 + 2 x 72 + 64 <= 5 x 96,
 // what 640 threads are launched with.
-constexpr int kSoftmaxRegs = 152, kProducerRegs = 72, kIssueRegs = 32;
+constexpr int kSoftmaxRegs = 136, kProducerRegs = 72, kIssueRegs = 64;
 constexpr int kGranule = 16;           // tokens that surely share a page
 constexpr int kGranules = kPromptKeys / kGranule;
 // The region in which some rows of a CTA see a token and others do not: at most 256 tokens,
