@@ -292,7 +292,7 @@ PyObject* cache_attention(PyObject* const* a) {
   const b2b_cache c = cache_of(a + 1, T, dev);
   if (D != c.head_dim)
     throw ValueRefusal("q has head size " + std::to_string(D) + ", the cache " + std::to_string(c.head_dim));
-  const float scale = a[9] == Py_None ? 1.f / std::sqrt(static_cast<float>(D)) : static_cast<float>(number(a[9]));
+  const float scale = static_cast<float>(a[9] == Py_None ? 1.0 / std::sqrt(static_cast<double>(D)) : number(a[9]));
   const int64_t H[1] = {heads};
   const void* slopes =
       a[11] == Py_None ? nullptr : dense(tensor(a[11], "slopes"), "slopes", at::kFloat, H, dev);

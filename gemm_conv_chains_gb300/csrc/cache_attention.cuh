@@ -26,8 +26,9 @@
 // running maximum and sum of its own, joined in shared memory.
 //
 // Precision: codes, and with a per-row power of two also bf16 queries, are exact in fp16; the
-// products sum in fp32; the softmax is fp32; P is rounded to fp16 (11 bits, finer than a bf16
-// output, and of the order of an fp16 output's own rounding); the value scales go into P before
+// products sum in fp32; the softmax is fp32; P is rounded to fp16 (11 bits, much finer than a bf16
+// output), and for fp16 outputs, whose own rounding is no coarser, the rest that the rounding
+// leaves is multiplied as well (attend-long, fp16: error 3.0e-4 -> LONG_ERR); the value scales go into P before
 // that rounding, relative to a running power of two, so that they cannot under- or overflow it.
 #pragma once
 
@@ -144,7 +145,8 @@ constexpr int attend_smem() {
          (NT > 1 ? D / 16 * NT * 256 : 0) + NT * 8 * 4;
 }
 
-template <int D, int NT, bool MODS>
+// MODS: capped or biased scores.  F16: fp16 queries and outputs, else bf16.
+template <int D, int NT, bool MODS, bool F16>
 __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) attend_kernel(const AttendParams p) {
   using C = CacheDims<D, NT>;
   constexpr int RT = NT * 8;
@@ -364,20 +366,20 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
       float amax = 0.f;
 #pragma unroll
       for (int u = 0; u < KS; ++u) {
-        const float2 a = p.is_bf16 ? widen2<true>(raw[u][0]) : widen2<false>(raw[u][0]);
-        const float2 z = p.is_bf16 ? widen2<true>(raw[u][1]) : widen2<false>(raw[u][1]);
+        const float2 a = widen2<!F16>(raw[u][0]);
+        const float2 z = widen2<!F16>(raw[u][1]);
         amax = fmaxf(amax, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(z.x), fabsf(z.y))));
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       float inv;
-      const float unit = row_unit_of(amax, p.is_bf16 != 0, inv);
+      const float unit = row_unit_of(amax, !F16, inv);
       // (q_frags and row_units are free: the last piece ended in a block barrier)
       if (t == 0 && (NT == 1 ? warp == 0 : warp < NT)) row_units[8 * q_nt + g] = unit;
 #pragma unroll
       for (int u = 0; u < KS; ++u) {
         uint32_t w[2] = {raw[u][0], raw[u][1]};
-        if (p.is_bf16) {
+        if constexpr (!F16) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float2 a = widen2<true>(w[i]);
@@ -521,7 +523,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
             for (int e = 0; e < 4; ++e) o[u][nt][e] *= f;
       }
       const float vs = sc.y * vref_inv;
-      uint32_t pf[NT][2];
+      uint32_t pf[NT][2], rest[NT][2];     // P, and for fp16 outputs what its rounding left
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float e[4];
@@ -530,8 +532,16 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
           e[i] = exp2_fast(x[nt][i] - m[nt][i & 1]);
           l[nt][i & 1] += e[i];
         }
-        pf[nt][0] = transpose8x8(narrow2<false>(e[0] * vs, e[1] * vs));
-        pf[nt][1] = transpose8x8(narrow2<false>(e[2] * vs, e[3] * vs));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float a = e[2 * i] * vs, z = e[2 * i + 1] * vs;
+          const uint32_t r = narrow2<false>(a, z);
+          pf[nt][i] = transpose8x8(r);
+          if constexpr (F16) {
+            const float2 kept = widen2<false>(r);
+            rest[nt][i] = transpose8x8(narrow2<false>(a - kept.x, z - kept.y));
+          }
+        }
       }
       // ---- O^T += V^T P^T ----
       uint32_t vw[4][C::kVBytes / 4];
@@ -603,7 +613,10 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
         uint32_t a[4];
         value_tile(i, a);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_m16n8k16(o[i][nt], a, pf[nt][0], pf[nt][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_m16n8k16(o[i][nt], a, pf[nt][0], pf[nt][1]);
+          if constexpr (F16) mma_m16n8k16(o[i][nt], a, rest[nt][0], rest[nt][1]);
+        }
       }
       issue_copy();
       issue_scales();
@@ -685,19 +698,18 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
         uint16_t* dst = p.out + ((s.row + static_cast<int64_t>(tq)) * p.q_heads + h * p.group +
                                  (row0 + r - tq * p.group)) * D + d;
         *reinterpret_cast<uint2*>(dst) =
-            p.is_bf16 ? make_uint2(narrow2<true>(acc.x, acc.y), narrow2<true>(acc.z, acc.w))
-                      : make_uint2(narrow2<false>(acc.x, acc.y), narrow2<false>(acc.z, acc.w));
+            make_uint2(narrow2<!F16>(acc.x, acc.y), narrow2<!F16>(acc.z, acc.w));
       }
     }
     __syncthreads();                                 // the ring may be filled again
   }
 }
 
-template <int D, int NT, bool MODS>
+template <int D, int NT, bool MODS, bool F16>
 cudaError_t launch_attend_one(const AttendParams& p, cudaStream_t s) {
   constexpr int smem = attend_smem<D, NT>();
   static_assert(smem * attend_ctas_per_sm(D, NT) <= 226 * 1024, "CTAs per SM");
-  auto* fn = attend_kernel<D, NT, MODS>;
+  auto* fn = attend_kernel<D, NT, MODS, F16>;
   // per device: a process that moves between devices sets it again, which is harmless
   static thread_local int set_on = -1;
   int dev = -1;
@@ -712,16 +724,20 @@ cudaError_t launch_attend_one(const AttendParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+template <int D, int NT>
+cudaError_t launch_attend_nt(const AttendParams& p, cudaStream_t s) {
+  if (p.softcap > 0.f || p.slopes != nullptr)
+    return p.is_bf16 ? launch_attend_one<D, NT, true, false>(p, s) : launch_attend_one<D, NT, true, true>(p, s);
+  return p.is_bf16 ? launch_attend_one<D, NT, false, false>(p, s) : launch_attend_one<D, NT, false, true>(p, s);
+}
+
 template <int D>
 cudaError_t launch_attend_d(int nt, const AttendParams& p, cudaStream_t s) {
-  const bool mods = p.softcap > 0.f || p.slopes != nullptr;
-  if (nt == 1)
-    return mods ? launch_attend_one<D, 1, true>(p, s) : launch_attend_one<D, 1, false>(p, s);
+  if (nt == 1) return launch_attend_nt<D, 1>(p, s);
   if constexpr (D <= 128) {
-    if (nt == 4)
-      return mods ? launch_attend_one<D, 4, true>(p, s) : launch_attend_one<D, 4, false>(p, s);
+    if (nt == 4) return launch_attend_nt<D, 4>(p, s);
   }
-  return mods ? launch_attend_one<D, 2, true>(p, s) : launch_attend_one<D, 2, false>(p, s);
+  return launch_attend_nt<D, 2>(p, s);
 }
 
 }  // namespace b2b

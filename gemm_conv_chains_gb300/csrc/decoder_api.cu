@@ -118,8 +118,27 @@ struct SplitChoice {
 // kernel about as long as 512 tokens take one CTA.
 constexpr int kMinTiles = 8;
 
-// Query rows per sequence and kv head from which the tcgen05 kernel takes a call.
-constexpr int64_t kPromptFrom = 64;
+// Whether the tcgen05 kernel takes a call, `rows` query rows per sequence and kv head.  Its time goes
+// with the key tiles of the longest unit (256 rows of one sequence and head) and the waves of units
+// over the SMs: 1.85 us per 128 keys (1.45 where a unit has only one row tile), whatever the head
+// size, latency between its softmax and its products.  The split kernel's goes with all the work,
+// cut evenly over the SMs: per 32 rows and 128 keys 7.5 ns at head size 128, 5.1 at 64.  Measured
+// over 1, 4 and 16 sequences of 300 to 30000 tokens, e.g. 8 kv heads of 128, 4 query heads each:
+//   1 sequence,   128 new tokens, 4000 cached: split  57 us, tcgen05  69
+//   1 sequence,   256 new tokens, 4000 cached: split  96 us, tcgen05  71
+//   4 sequences,   33 new tokens, 4000 cached: split  64 us, tcgen05  64
+//   16 sequences, 128 new tokens, 4000 cached: split 606 us, tcgen05 169
+// The split kernel also has the longer start and a second launch: it has to be 15 % ahead.  On
+// contexts of up to 512 tokens, where it does not cut sequences, it falls behind earlier.
+bool prompt_pays(int32_t D, int64_t rows, int64_t heads, bool whole, int num_sms) {
+  if (D > 128 || rows <= 32) return false;
+  const double pieces = static_cast<double>((rows + 31) / 32) * heads;      // of the split kernel
+  if (whole) return pieces >= 150;
+  const double units = static_cast<double>((rows + 255) / 256) * heads;
+  const double waves = units > num_sms ? units / num_sms : 1.0;
+  const double split_ns = D == 64 ? 5.1 : D == 96 ? 6.3 : 7.5;
+  return pieces * split_ns >= 0.85 * waves * (rows <= 128 ? 1450.0 : 1850.0);
+}
 
 // The limit of each on-chip wait of the tcgen05 kernel.
 constexpr uint64_t kDecoderWaitNs = 1000000000ull;
@@ -131,7 +150,8 @@ SplitChoice split_of(const b2b_cache* c, int32_t q_heads, int num_sms) {
   s.grid = attend_ctas_per_sm(c->head_dim, s.nt) * num_sms;
   const int64_t most = static_cast<int64_t>(c->max_pages) * c->page_size;
   s.whole = most <= kMinTiles * 64 ? 1 : 0;
-  s.prompt = c->head_dim <= 128 && rows >= kPromptFrom ? 1 : 0;
+  s.prompt = prompt_pays(c->head_dim, rows, static_cast<int64_t>(c->batch) * c->heads, s.whole != 0,
+                         num_sms);
   s.bytes = s.prompt  ? prompt_workspace(rows, c->batch)
             : s.whole ? 0
                     : 16 * ((static_cast<int64_t>(c->batch) + 4) / 4) +

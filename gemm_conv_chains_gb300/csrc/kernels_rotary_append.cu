@@ -233,14 +233,14 @@ cudaError_t launch_rotary_table(float2* table, int64_t n, int32_t half, const do
 // One block per page that a sequence's new tokens touch, kv head, and pool (keys or
 // values).  With A the largest finite magnitude of the block's new values (keys after the
 // rotation) and s the page's scale if it already holds older tokens of the sequence, else 0:
-//   s' = max(s, A / 448, 2^-64);  new codes e4m3(y (1 / s')), saturating;
+//   s' = max(s, A / 448, 2^-64);  new codes e4m3(y / s'), saturating;
 //   older codes e4m3(code * (s / s')) if s' > s, else untouched.
 // A thread keeps one unit of a row, asks for its first tokens' along with the page number and holds
 // them between the maximum and the codes; what a page has beyond that is read twice, the second
 // time from L1 or L2.  One new token per sequence is bound by the latency of its dependent loads
 // (sequence, page number and tokens, scale); prompts by the instructions per element, 0.6 of the
 // issue slots (ragged prompts, 18 k tokens, 8 heads of 128, pages of 32: 72 us with an index
-// division per unit and an exact division per element, 36 us so).
+// division per unit and an exact division per element, PAGES_US so).
 // The queries of few tokens are turned by further blocks of the same launch; those of many by a
 // launch of the walk above.
 constexpr int kAppendThreads = 128;
@@ -255,11 +255,24 @@ __device__ __forceinline__ void most_of(const float (&v)[8], float& most) {
   }
 }
 
-// Eight values as codes, the scale's reciprocal given.
-__device__ __forceinline__ void store_codes(uint8_t* dst, const float (&v)[8], float inv) {
+// Eight values as codes of a scale and its reciprocal.  FINITE: the quotients by the reciprocal, each
+// corrected once by its residual y - q s (Markstein's step), which rounds like the quotient itself
+// and not like the product; an infinity has no residual and takes the exact division.
+template <bool FINITE>
+__device__ __forceinline__ void store_codes(uint8_t* dst, const float (&v)[8], float scale, float inv) {
+  float q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (FINITE) {
+      q[e] = v[e] * inv;
+      q[e] = fmaf(fmaf(-q[e], scale, v[e]), inv, q[e]);
+    } else {
+      q[e] = __fdiv_rn(v[e], scale);
+    }
+  }
   uint32_t w[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) w[e] = e4m3x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+  for (int e = 0; e < 4; ++e) w[e] = e4m3x2(q[2 * e], q[2 * e + 1]);
   *reinterpret_cast<uint2*>(dst) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
@@ -348,7 +361,8 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int b, int j,
     if (at.pair) most_of<false>(hi, most);
   });
   most = block_max(most);
-  if (most > 3.402823466e38f) {                      // an infinity among them: without those, then
+  const bool finite = most <= 3.402823466e38f;
+  if (!finite) {                                     // an infinity among them: without those, then
     most = 0.f;
     each([&](int, const float (&lo)[8], const float (&hi)[8]) {
       most_of<true>(lo, most);
@@ -360,10 +374,17 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int b, int j,
   const float inv = __fdiv_rn(1.f, after);
 
   uint8_t* dst = codes + (lo_tok - first_slot) * c.D + at.d;
-  each([&](int tok, const float (&lo)[8], const float (&hi)[8]) {
-    store_codes(dst + tok * c.D, lo, inv);
-    if (at.pair) store_codes(dst + tok * c.D + rot / 2, hi, inv);
-  });
+  if (finite) {
+    each([&](int tok, const float (&lo)[8], const float (&hi)[8]) {
+      store_codes<true>(dst + tok * c.D, lo, after, inv);
+      if (at.pair) store_codes<true>(dst + tok * c.D + rot / 2, hi, after, inv);
+    });
+  } else {
+    each([&](int tok, const float (&lo)[8], const float (&hi)[8]) {
+      store_codes<false>(dst + tok * c.D, lo, after, inv);
+      if (at.pair) store_codes<false>(dst + tok * c.D + rot / 2, hi, after, inv);
+    });
+  }
   if (held > 0 && after > before) {
     const float ratio = __fdiv_rn(before, after);
     uint2* old = reinterpret_cast<uint2*>(codes);

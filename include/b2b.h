@@ -273,7 +273,7 @@ typedef struct b2b_cache {
  * the queries q -> q_out when q is given (q_out may be q).  For each page touched and kv head,
  * A the largest finite magnitude of its new values and s its scale if it already holds older
  * tokens of the sequence (else 0):
- *   s' = max(s, A / 448, 2^-64),   new codes = e4m3(y * (1 / s')),
+ *   s' = max(s, A / 448, 2^-64),   new codes = e4m3(y / s'),
  *   and where s' > s the page's older codes become e4m3(code * (s / s'))
  * in fp32, to nearest even, saturating (an infinity becomes +-448 s'; a NaN stays one).  Calling
  * again with the same arguments changes nothing.  Pages that are written belong to one

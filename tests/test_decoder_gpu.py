@@ -305,9 +305,82 @@ def test_attention(dt, older, new, heads, group, D, page):
     _check_attention(out, c, rows[:, 1: 1 + Hq], D ** -0.5)
 
 
+# Enough rows and heads for the kernel that takes prompts (256 query rows per block): ragged, rows
+# that end inside a row tile, contexts that end inside a key tile, sequences with one new token.
+PROMPTS = [
+    ([0, 100, 7, 300, 64, 1, 130, 255], [70, 1, 33, 40, 64, 2, 65, 10], 8, 2, 64, 16),
+    ([0, 900, 250, 3], [150, 129, 1, 260], 8, 3, 128, 32),
+    ([1000, 40], [300, 257], 8, 4, 128, 64), ([5, 0, 700], [100, 200, 64], 8, 4, 96, 128),
+    ([129, 0, 17, 511], [128, 1, 90, 65], 16, 1, 64, 256), ([0], [1100], 4, 2, 128, 16),
+]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("older,new,heads,group,D,page", PROMPTS)
+def test_attention_of_prompts(dt, older, new, heads, group, D, page):
+    c = ref.Cache(older, new, heads, D, page, seed=D + len(older), fill=0xFF)
+    Hq = heads * group
+    rows = _randn(D, c.T, Hq + 1, D).to(DT[dt])
+    out = ops.cache_attention(rows.cuda()[:, :Hq], *c.args())
+    _check_attention(out, c, rows[:, :Hq], D ** -0.5)
+    assert torch.equal(out, ops.cache_attention(rows.cuda()[:, :Hq], *c.args()))
+    back = ops.cache_attention(-rows.cuda()[:, :Hq], *c.args(), scale=-D ** -0.5)
+    assert torch.equal(out, back)
+
+
+def _prompt_case(seed, new=40):
+    return ref.Cache([50 + 9 * i for i in range(8)], [new] * 8, 8, 128, 32, seed=seed)
+
+
+def test_prompt_scores_and_scales_far_apart():
+    c = _prompt_case(3)
+    c.ks *= torch.exp2(torch.linspace(-3, 6, c.pages))[:, None]
+    c.vs *= torch.exp2(torch.linspace(8, -12, c.pages))[:, None]
+    c.vs[5] = 0
+    q = (_randn(2, c.T, 16, 128) * 3).bfloat16()
+    out = ops.cache_attention(q.cuda(), *c.args())
+    _check_attention(out, c, q, 128 ** -0.5)
+
+
+def test_prompt_infinite_and_nan_inputs_stay_in_their_rows():
+    c = _prompt_case(4)
+    q = _randn(3, c.T, 16, 128).half()
+    want = ops.cache_attention(q.cuda(), *c.args()).cpu()
+    rows = torch.ones(c.T, 16, 128, dtype=torch.bool)
+    at = 3 * 40                                        # the fourth sequence
+    q[at + 2, 1, 7], q[at + 3, 0, 0] = math.nan, math.inf
+    rows[at + 2, 1] = rows[at + 3, 0] = False
+    place = c.older[3] + 20                            # its 21st new token: a value and a key
+    pid, slot = int(c.table[3, place // 32]), place % 32
+    c.v[pid, 2, slot, 9] = math.nan                    # query heads 4 and 5
+    c.k[pid, 6, slot, 100] = math.nan                  # query heads 12 and 13
+    rows[at + 20: at + 40, 4:6, 9] = False
+    rows[at + 20: at + 40, 12:14] = False
+    got = ops.cache_attention(q.cuda(), *c.args()).cpu()
+    assert torch.equal(got[rows], want[rows])
+    assert got[~rows].isnan().all()
+
+
+def test_prompt_index_errors_are_recorded():
+    c = _prompt_case(5)
+    q = _randn(5, c.T, 16, 128).half().cuda()
+    want = ops.cache_attention(q, *c.args())
+    for what, change in [(2, lambda r: r[4].__setitem__((2, 1), c.pages)),
+                         (2, lambda r: r[4].__setitem__((2, 0), -7)),
+                         (3, lambda r: r[5].__setitem__(2, 39)),
+                         (3, lambda r: r[5].__setitem__(2, 10 ** 6)),
+                         (4, lambda r: r[6].__setitem__(8, 400))]:
+        args = c.args()
+        change(args)
+        got = ops.cache_attention(q, *args)
+        st, info = ops.get_cache_error()
+        assert st == 2 and info[2] == what and info[3] == (7 if what == 4 else 2), (what, info)
+        assert torch.equal(got[:80], want[:80]) and torch.equal(got[120:280], want[120:280])
+
+
 @pytest.mark.parametrize("softcap,bias", [(20.0, False), (0.0, True), (5.0, True)])
-@pytest.mark.parametrize("older,new,heads,group,D,page", [SHAPES[3], SHAPES[9], SHAPES[11],
-                                                          ([2000], [200], 2, 2, 128, 64)])
+@pytest.mark.parametrize("older,new,heads,group,D,page", [SHAPES[3], SHAPES[9], SHAPES[11], PROMPTS[0],
+                                                          PROMPTS[1], PROMPTS[3]])
 def test_attention_cap_and_bias(softcap, bias, older, new, heads, group, D, page):
     c = ref.Cache(older, new, heads, D, page, seed=7, fill=0xFF)
     Hq = heads * group
