@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
   };
   // lane's share of the first kHeld x 32 sequences stays in registers for the search
   constexpr int kHeld = 4;
+  grid_dependency_wait();                              // launched early
   uint32_t held[kHeld], total = 0;
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
@@ -720,8 +721,7 @@ cudaError_t launch_attend_one(const AttendParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     set_on = dev;
   }
-  fn<<<p.grid, kAttendWarps * 32, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_early(fn, p.grid, kAttendWarps * 32, smem, s, p);
 }
 
 template <int D, int NT>

@@ -265,8 +265,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
   {
     int b, rt;
     int order = static_cast<int>(blockIdx.x) / p.c.heads;
+    grid_launch_dependents();
+    grid_dependency_wait();                                // launched early
     if (p.meta != nullptr) {
-      grid_dependency_wait();
       order = __ldg(reinterpret_cast<const int*>(p.meta) + order);
     }
     plain_pair(p, row_tiles, order, b, rt);
@@ -737,17 +738,8 @@ cudaError_t launch_prompt_d(const AttendParams& p, int row_tiles, cudaStream_t s
     if (e != cudaSuccess) return e;
     set_on[mods] = dev;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(row_tiles * p.c.heads * p.c.B));
-  cfg.blockDim = dim3(kPromptThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.meta != nullptr ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, fn, p, row_tiles);
+  return launch_early(fn, static_cast<int64_t>(row_tiles) * p.c.heads * p.c.B, kPromptThreads, smem, s,
+                      p, row_tiles);
 }
 
 }  // namespace b2b

@@ -72,6 +72,24 @@ struct AttendParams {
   uint64_t wait_limit_ns;
 };
 
+// Launches with programmatic stream serialisation, as the chain kernels: the kernel may be scheduled
+// while the one before it in the stream finishes, and waits for that (griddepcontrol.wait) before
+// it touches global memory.
+template <class... P, class... A>
+cudaError_t launch_early(void (*fn)(P...), int64_t grid, int block, int smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(block));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
+}
+
 cudaError_t launch_rotary(bool bf16, const RotaryParams& p, cudaStream_t s);
 cudaError_t launch_rotary_table(float2* table, int64_t n, int32_t half, const double* params,
                                 cudaStream_t s);

@@ -150,6 +150,10 @@ SplitChoice split_of(const b2b_cache* c, int32_t q_heads, int num_sms) {
   s.grid = attend_ctas_per_sm(c->head_dim, s.nt) * num_sms;
   const int64_t most = static_cast<int64_t>(c->max_pages) * c->page_size;
   s.whole = most <= kMinTiles * 64 ? 1 : 0;
+  // no more CTAs than there can be runs
+  const int64_t pieces = (rows + 8 * s.nt - 1) / (8 * s.nt) * c->heads * c->batch;
+  const int64_t runs = s.whole ? pieces : pieces * ((most / 64 + kMinTiles - 1) / kMinTiles);
+  if (runs < s.grid) s.grid = static_cast<int>(runs);
   s.prompt = prompt_pays(c->head_dim, rows, static_cast<int64_t>(c->batch) * c->heads, s.whole != 0,
                          num_sms);
   s.bytes = s.prompt  ? prompt_workspace(rows, c->batch)

@@ -20,8 +20,10 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, 
   const int head = static_cast<int>(x % p.q_heads);
   const int tq = static_cast<int>(x / p.q_heads % c.max_new);
   const int b = static_cast<int>(x / p.q_heads / c.max_new);
-  const Sequence s = load_sequence(c, b, DK_ATTEND);
+  grid_launch_dependents();
+  // (also for the lengths: the kernel before the split one may have written them)
   grid_dependency_wait();
+  const Sequence s = load_sequence(c, b, DK_ATTEND);
   if (tq >= s.n) return;
   const int h = head / p.group;
   const int r = tq * p.group + head % p.group;
@@ -115,17 +117,8 @@ cudaError_t launch_attend_combine(const AttendParams& p, int nt, int num_sms, cu
   const int lanes = p.c.D / 4 / shares, threads = rows < 4 * num_sms ? 256 : 128;
   const int groups = threads / lanes;
   if (rows * shares > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows * shares));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = sizeof(float) * (((2 * groups + 3) & ~3) + 4 * groups * lanes);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_join_kernel, p, nt * 8, lanes, shares);
+  const int smem = 4 * (((2 * groups + 3) & ~3) + 4 * groups * lanes);
+  return launch_early(attend_join_kernel, rows * shares, threads, smem, s, p, nt * 8, lanes, shares);
 }
 
 }  // namespace b2b

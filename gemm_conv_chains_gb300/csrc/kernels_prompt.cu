@@ -9,6 +9,7 @@ __global__ void __launch_bounds__(kRankedPairs) prompt_order_kernel(const Attend
                                                                     int* order) {
   __shared__ int key_tiles[kRankedPairs];
   grid_launch_dependents();
+  grid_dependency_wait();
   const int mine = threadIdx.x, pairs = row_tiles * p.c.B;
   if (mine < pairs) {
     PromptUnit u;
@@ -35,9 +36,10 @@ cudaError_t launch_prompt(const AttendParams& p, cudaStream_t s) {
   const int64_t row_tiles = (rows + kPromptRows - 1) / kPromptRows;
   if (row_tiles * p.c.heads * p.c.B > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   if (p.meta != nullptr) {
-    prompt_order_kernel<<<1, kRankedPairs, 0, s>>>(p, static_cast<int>(row_tiles),
-                                                   reinterpret_cast<int*>(p.meta));
-    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    if (cudaError_t e = launch_early(prompt_order_kernel, 1, kRankedPairs, 0, s, p,
+                                     static_cast<int>(row_tiles), reinterpret_cast<int*>(p.meta));
+        e != cudaSuccess)
+      return e;
   }
   switch (p.c.D) {
     case 64: return launch_prompt_d<64>(p, static_cast<int>(row_tiles), s);

@@ -4,6 +4,12 @@
 
 namespace b2b {
 
+// What a kernel launched early (launch_early) starts with.
+__device__ __forceinline__ void begin() {
+  grid_launch_dependents();
+  grid_dependency_wait();
+}
+
 // ------------------------------------------------------------------------------------
 // rows of heads turned: rotary positions, and the queries of an append
 // ------------------------------------------------------------------------------------
@@ -136,6 +142,7 @@ __device__ __forceinline__ TurnRows rows_of(const RotaryParams& p) {
 template <bool BF16>
 __global__ void __launch_bounds__(kTurnThreads, 3) rotary_walk_kernel(const RotaryParams p, int units,
                                                                       int64_t rows) {
+  begin();
   const int64_t t0 = blockIdx.x * rows, t1 = t0 + rows < p.T ? t0 + rows : p.T;
   turn_rows<BF16>(rows_of(p), t0, t1, units, [&](int64_t t) { return rotary_position(p, t); });
 }
@@ -143,6 +150,7 @@ __global__ void __launch_bounds__(kTurnThreads, 3) rotary_walk_kernel(const Rota
 template <bool BF16>
 __global__ void __launch_bounds__(kTurnThreads) rotary_kernel(const RotaryParams p, int units,
                                                               int tokens_per_block) {
+  begin();
   const int per_token = p.H * units;
   for (int j = threadIdx.x; j < per_token * tokens_per_block; j += blockDim.x) {
     const int64_t t = static_cast<int64_t>(blockIdx.x) * tokens_per_block + j / per_token;
@@ -172,17 +180,12 @@ cudaError_t launch_rotary(bool bf16, const RotaryParams& p, cudaStream_t s) {
     if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), kTurnSmem, set_on[bf16]);
         e != cudaSuccess)
       return e;
-    fn<<<static_cast<unsigned>((p.T + rows - 1) / rows), kTurnThreads, kTurnSmem, s>>>(p, units, rows);
-    return cudaGetLastError();
+    return launch_early(fn, (p.T + rows - 1) / rows, kTurnThreads, kTurnSmem, s, p, units, rows);
   }
   const int per_token = p.H * units;
   const int tpb = per_token >= kTurnThreads ? 1 : kTurnThreads / per_token;
-  const unsigned blocks = static_cast<unsigned>((p.T + tpb - 1) / tpb);
-  if (bf16)
-    rotary_kernel<true><<<blocks, kTurnThreads, 0, s>>>(p, units, tpb);
-  else
-    rotary_kernel<false><<<blocks, kTurnThreads, 0, s>>>(p, units, tpb);
-  return cudaGetLastError();
+  return launch_early(bf16 ? rotary_kernel<true> : rotary_kernel<false>, (p.T + tpb - 1) / tpb,
+                      kTurnThreads, 0, s, p, units, tpb);
 }
 
 // The table: (cos, sin) of position * frequency in fp64, rounded once to fp32.  params:
@@ -200,6 +203,7 @@ struct TableParams {
 
 __global__ void __launch_bounds__(256) rotary_table_kernel(float2* table, int64_t total, int half,
                                                            const TableParams p) {
+  begin();
   const int64_t idx = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (idx >= total) return;
   const int64_t pos = idx / half;
@@ -222,9 +226,7 @@ cudaError_t launch_rotary_table(float2* table, int64_t n, int32_t half, const do
                                 cudaStream_t s) {
   TableParams p{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
   const int64_t total = n * half;
-  rotary_table_kernel<<<static_cast<unsigned>((total + 255) / 256), 256, 0, s>>>(table, total, half,
-                                                                                p);
-  return cudaGetLastError();
+  return launch_early(rotary_table_kernel, (total + 255) / 256, 256, 0, s, table, total, half, p);
 }
 
 // ------------------------------------------------------------------------------------
@@ -448,6 +450,7 @@ __device__ __forceinline__ TurnRows rows_of(const AppendParams& p) {
 template <bool BF16>
 __global__ void __launch_bounds__(kTurnThreads, 3) query_walk_kernel(const AppendParams p, int units,
                                                                      int64_t rows) {
+  begin();
   const int64_t t0 = blockIdx.x * rows, t1 = t0 + rows < p.c.T ? t0 + rows : p.c.T;
   QueryPosition position(p, t0);
   turn_rows<BF16>(rows_of(p), t0, t1, units, [&](int64_t t) { return position(t); });
@@ -457,6 +460,7 @@ template <bool BF16, int ROTATION>
 __global__ void __launch_bounds__(kAppendThreads, 8) append_kernel(const AppendParams p,
                                                                 int64_t page_blocks,
                                                                 int pages_per_seq) {
+  begin();
   const int64_t x = blockIdx.x;
   if (ROTATION != 0 && x >= page_blocks) {           // one token's queries
     const int64_t t = x - page_blocks;
@@ -489,15 +493,15 @@ cudaError_t launch_append(bool bf16, const AppendParams& p, cudaStream_t s) {
   auto* append = p.table == nullptr ? (bf16 ? append_kernel<true, 0> : append_kernel<false, 0>)
                  : p.interleaved    ? (bf16 ? append_kernel<true, 1> : append_kernel<false, 1>)
                                     : (bf16 ? append_kernel<true, 2> : append_kernel<false, 2>);
-  append<<<static_cast<unsigned>(blocks), kAppendThreads, 0, s>>>(p, page_blocks, per_seq);
-  if (cudaError_t e = cudaGetLastError(); e != cudaSuccess || rows == 0) return e;
+  if (cudaError_t e = launch_early(append, blocks, kAppendThreads, 0, s, p, page_blocks, per_seq);
+      e != cudaSuccess || rows == 0)
+    return e;
   static thread_local int set_on[2] = {-1, -1};
   auto* fn = bf16 ? query_walk_kernel<true> : query_walk_kernel<false>;
   if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), kTurnSmem, set_on[bf16]);
       e != cudaSuccess)
     return e;
-  fn<<<static_cast<unsigned>((p.c.T + rows - 1) / rows), kTurnThreads, kTurnSmem, s>>>(p, units, rows);
-  return cudaGetLastError();
+  return launch_early(fn, (p.c.T + rows - 1) / rows, kTurnThreads, kTurnSmem, s, p, units, rows);
 }
 
 }  // namespace b2b
