@@ -192,39 +192,42 @@ struct PromptProducer {
   static constexpr int kLanes = kPieces > 4 ? 8 : 4;  // threads per token
   static constexpr int kTokens = 128 / kLanes;        // tokens of the warpgroup's one load
   static constexpr int kEach = kLanes;                // loads per thread and tile
-  int page[kEach];                                    // page numbers of the next tile's runs
   uint32_t tid;
+  int page;                                           // number of granule lane & 7's page, next tile
 
-  // The thread's run in load j: token j kTokens + tid / kLanes, of which the 16-token granule (and
-  // so the page) is the same for the whole load, or half of it.
+  // The thread's run in load j: token j kTokens + tid / kLanes.  A load's tokens lie in one 16-token
+  // granule (two with kTokens = 32, one per half of the warpgroup), and so in one page.
   __device__ __forceinline__ int token(int j) const { return j * kTokens + tid / kLanes; }
   __device__ __forceinline__ uint32_t piece() const { return tid % kLanes; }
+  __device__ __forceinline__ int granule(int j) const {
+    return kLanes == 8 ? j : 2 * j + static_cast<int>(tid >> 6);
+  }
 
   // Reads the page numbers of a tile (used a tile later, so that nothing waits for them).
   __device__ __forceinline__ void locate(const AttendParams& p, const PromptUnit& u, int tile) {
-    const CacheView& c = p.c;
-    const int32_t* pages = c.page_table + static_cast<int64_t>(u.b) * c.max_pages;
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      const int at = tile * kPromptKeys + token(j);
-      page[j] = at < u.kv_end ? __ldg(pages + (at >> c.page_shift)) : -1;
-    }
+    const int at = tile * kPromptKeys + static_cast<int>(tid & 7) * kGranule;
+    page = at < u.kv_end ? __ldg(p.c.page_table + static_cast<int64_t>(u.b) * p.c.max_pages +
+                                 (at >> p.c.page_shift))
+                         : 0;
   }
-  // Starts the loads of this thread's runs of the located tile.
+  // Starts the loads of this thread's runs of the located tile.  A number outside the pool is
+  // replaced (it is recorded with the scales, which become NaN); slots at or past kv_end are read
+  // as they are.
   __device__ __forceinline__ void fetch(const AttendParams& p, const PromptUnit& u, int tile,
                                         const uint8_t* pool, uint4 (&raw)[kEach]) const {
     const CacheView& c = p.c;
     const int mask = (1 << c.page_shift) - 1;
     const int64_t page_bytes = (static_cast<int64_t>(c.heads) << c.page_shift) * D;
-    const uint8_t* head = pool + ((static_cast<int64_t>(u.h) << c.page_shift) * D) + 16 * piece();
+    const uint32_t run = piece() < kPieces ? piece() : 0;
+    const uint8_t* head = pool + ((static_cast<int64_t>(u.h) << c.page_shift) * D) +
+                          static_cast<int>(tid / kLanes % kGranule) * D + 16 * run;
+    const int id = static_cast<uint32_t>(page) < static_cast<uint32_t>(c.pages) ? page : 0;
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
-      // a number outside the pool (-1: past the end) loads zeros; it is recorded with the scales,
-      // which become NaN
-      const int slot = (tile * kPromptKeys + token(j)) & mask;
-      raw[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (static_cast<uint32_t>(page[j]) < static_cast<uint32_t>(c.pages) && piece() < kPieces)
-        raw[j] = __ldg(reinterpret_cast<const uint4*>(head + page[j] * page_bytes + slot * D));
+      const int g = granule(j);
+      const int slot = (tile * kPromptKeys + g * kGranule) & mask;
+      raw[j] = __ldg(reinterpret_cast<const uint4*>(
+          head + __shfl_sync(0xffffffffu, id, g) * page_bytes + slot * D));
     }
   }
   // A run is two 16-byte units of a row.  Runs of the second 64 channels store theirs in the other
@@ -567,15 +570,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
     PromptProducer<D> prod;
     prod.tid = threadIdx.x - 256;
     uint4 raw[PromptProducer<D>::kEach];
-    // thread g < kGranules: the scales of granule g, its page number read a tile ahead
-    const int32_t* pages = p.c.page_table + static_cast<int64_t>(u.b) * p.c.max_pages;
-    const int granule = static_cast<int>(prod.tid) * kGranule;
-    auto scale_page = [&](int tile) -> int {
-      const int at = tile * kPromptKeys + granule;
-      return prod.tid < kGranules && at < u.kv_end ? __ldg(pages + (at >> p.c.page_shift)) : -1;
-    };
+    // thread g < kGranules: the scales of granule g, whose page number it has
     auto scales_of = [&](int tile, int id) -> float2 {
-      if (prod.tid >= kGranules || tile * kPromptKeys + granule >= u.kv_end) return make_float2(0.f, 0.f);
+      if (prod.tid >= kGranules ||
+          tile * kPromptKeys + static_cast<int>(prod.tid) * kGranule >= u.kv_end)
+        return make_float2(0.f, 0.f);
       if (id < 0 || id >= p.c.pages) {
         index_error(p.c.err, DK_PROMPT, DEC_ERR_PAGE, static_cast<uint32_t>(u.b));
         return make_float2(__uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u));
@@ -585,9 +584,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
     };
     prod.locate(p, u, 0);
     prod.fetch(p, u, 0, p.c.k, raw);
-    float2 s2 = scales_of(0, scale_page(0));
+    float2 s2 = scales_of(0, prod.page);
     prod.locate(p, u, 1);
-    int next_id = scale_page(1);
     bool ok = true;
     for (int i = 0; i < u.tiles && ok; ++i) {
       const int slot = i & 1;
@@ -600,9 +598,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       if (lane == 0) mbar_arrive(smem_u32(&bars->kfull[slot]));
       if (i + 1 < u.tiles) {
         prod.fetch(p, u, i + 1, p.c.k, raw);
-        s2 = scales_of(i + 1, next_id);
+        s2 = scales_of(i + 1, prod.page);
         prod.locate(p, u, i + 2);
-        next_id = scale_page(i + 2);
       }
     }
   } else if (warp < 16) {
@@ -621,10 +618,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       if (i >= 2) ok = wait(&bars->vempty[slot], ((i >> 1) - 1) & 1, PS_VEMPTY);
       if (!ok) break;
       if (i * kPromptKeys >= edge0) {
-        // a NaN that only some rows see: out of the product (0 * NaN is one), noted for the rows
-        // that do see it
+        // Slots past every row's reach may hold anything: taken as zeros.  A NaN that only some rows
+        // see comes out of the product too (0 * NaN is one) and is noted for the rows that see it.
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
+          if (i * kPromptKeys + prod.token(j) >= u.kv_end) raw[j] = make_uint4(0u, 0u, 0u, 0u);
           uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
           uint32_t any = 0u;
 #pragma unroll
@@ -639,8 +637,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
               }
             raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
             const int at = i * kPromptKeys + prod.token(j);
-            // what lies past every row's reach is dropped with it
-            if (at < u.kv_end && at - edge0 < kEdgeTokens) {
+            if (at - edge0 < kEdgeTokens && prod.piece() < PromptProducer<D>::kPieces) {
               atomicOr(&nan_bits[(at - edge0) * (D / 32) + prod.piece() / 2],
                        bits << (16 * (prod.piece() & 1)));
               bars->nan_any = 1u;
