@@ -3,7 +3,7 @@
 //
 // These run once per token of a generation, on kernels of 2 to 6 us.  Asking a dozen tensors for
 // their types, shapes and addresses from Python and handing them over by ctypes took 15 to 21 us a
-// call on the GB300's Arm host; here a call takes 5 to 6, most of it the launch.  The functions
+// call on the GB300's Arm host; here one of one launch takes 4.4 to 5.7.  The functions
 // take every argument by position (ops.py gives them names and defaults) and return the output, or
 // the status of include/b2b.h if the library refused.
 #define PY_SSIZE_T_CLEAN

@@ -21,6 +21,16 @@
 // (log2, relative to a running power of two) and are divided out of the row sum, so that a
 // probability costs one multiply-add, one exponential and one addition.  The row maximum only
 // moves when it is exceeded by 2^8, and O, in TMEM, is rescaled only then.
+//
+// Measured: prompts of 451 to 2048 tokens behind 1192 to 4096 cached ones (4 sequences, 32 query
+// heads on 8 of 128 channels): 236 us, 1.04 PFLOP/s, 0.54 of the library's dense bf16 rate.  The
+// split kernel took 1480 us on them.  The tensor pipe is busy for 42 % of the time: a key tile's
+// chain (S ready, 128 columns read, exponentials, P written, P V and the next Q K^T issued) takes
+// ~3800 clocks, of which the products are ~1100 and a softmax warp's work ~1600; the rest are
+// hand-offs.  64 channels take as long per key tile as 128, so the bound is this latency.  Slower:
+// one issuing warp per row tile (353 us: the softmaxes fall into step and the tensor core idles;
+// 264 when the two take turns), waits that spin (238), rolled MMA loops (246), the operand waits
+// hidden behind the other row tile's products (239 to 252).
 #pragma once
 
 #include <type_traits>
@@ -206,8 +216,8 @@ struct PromptProducer {
   // Reads the page numbers of a tile (used a tile later, so that nothing waits for them).
   __device__ __forceinline__ void locate(const AttendParams& p, const PromptUnit& u, int tile) {
     const int at = tile * kPromptKeys + static_cast<int>(tid & 7) * kGranule;
-    page = at < u.kv_end ? __ldg(p.c.page_table + static_cast<int64_t>(u.b) * p.c.max_pages +
-                                 (at >> p.c.page_shift))
+    page = at < u.kv_end ? p.c.page_table[static_cast<int64_t>(u.b) * p.c.max_pages +
+                                          (at >> p.c.page_shift)]
                          : 0;
   }
   // Starts the loads of this thread's runs of the located tile.  A number outside the pool is
@@ -226,8 +236,8 @@ struct PromptProducer {
     for (int j = 0; j < kEach; ++j) {
       const int g = granule(j);
       const int slot = (tile * kPromptKeys + g * kGranule) & mask;
-      raw[j] = __ldg(reinterpret_cast<const uint4*>(
-          head + __shfl_sync(0xffffffffu, id, g) * page_bytes + slot * D));
+      raw[j] = *reinterpret_cast<const uint4*>(
+          head + __shfl_sync(0xffffffffu, id, g) * page_bytes + slot * D);
     }
   }
   // A run is two 16-byte units of a row.  Runs of the second 64 channels store theirs in the other
@@ -271,7 +281,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
     grid_launch_dependents();
     grid_dependency_wait();                                // launched early
     if (p.meta != nullptr) {
-      order = __ldg(reinterpret_cast<const int*>(p.meta) + order);
+      order = static_cast<int>(p.meta[order]);
     }
     plain_pair(p, row_tiles, order, b, rt);
     if (!prompt_unit(p, b, static_cast<int>(blockIdx.x) % p.c.heads, rt, u)) return;   // the whole CTA
@@ -333,7 +343,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
 #pragma unroll 4
           for (int i = 0; i < D / 8; ++i) {
             uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (valid) w = __ldg(reinterpret_cast<const uint4*>(src) + i);
+            if (valid) w = reinterpret_cast<const uint4*>(src)[i];
             float f[8];
             widen8<true>(w, f);
 #pragma unroll
@@ -350,7 +360,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
 #pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
           uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (valid) w = __ldg(reinterpret_cast<const uint4*>(src) + i);
+          if (valid) w = reinterpret_cast<const uint4*>(src)[i];
           if (p.is_bf16) {
             float f[8];
             widen8<true>(w, f);
@@ -373,7 +383,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
 
       const int limit = valid ? u.start + tq : 0x7FFFFFFF;
       const int low_limit = u.start + (u.row0 + 128 * t) / p.group;
-      const float slope = MODS && p.slopes != nullptr && valid ? __ldg(p.slopes + head) : 0.f;
+      const float slope = MODS && p.slopes != nullptr && valid ? p.slopes[head] : 0.f;
       const float cap2 = MODS && p.softcap > 0.f ? 2.f * 1.4426950408889634f / p.softcap : 0.f;
       float m = -1e30f, l = 0.f, lvref = -1e30f;
       bool ok = true;
@@ -580,7 +590,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
         return make_float2(__uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u));
       }
       const int64_t at = static_cast<int64_t>(id) * p.c.heads + u.h;
-      return make_float2(__ldg(p.c.k_scale + at), __ldg(p.c.v_scale + at));
+      return make_float2(p.c.k_scale[at], p.c.v_scale[at]);
     };
     prod.locate(p, u, 0);
     prod.fetch(p, u, 0, p.c.k, raw);

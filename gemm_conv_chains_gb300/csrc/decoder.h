@@ -90,10 +90,10 @@ cudaError_t launch_early(void (*fn)(P...), int64_t grid, int block, int smem, cu
   return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
 }
 
-cudaError_t launch_rotary(bool bf16, const RotaryParams& p, cudaStream_t s);
+cudaError_t launch_rotary(bool bf16, const RotaryParams& p, int num_sms, cudaStream_t s);
 cudaError_t launch_rotary_table(float2* table, int64_t n, int32_t half, const double* params,
                                 cudaStream_t s);
-cudaError_t launch_append(bool bf16, const AppendParams& p, cudaStream_t s);
+cudaError_t launch_append(bool bf16, const AppendParams& p, int num_sms, cudaStream_t s);
 
 // CTAs of the split kernel that an SM holds at once: its registers decide (one row tile of 8 at
 // head sizes up to 128: 168 per thread).  More warps hide more of each strip's latencies.

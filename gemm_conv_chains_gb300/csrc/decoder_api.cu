@@ -114,9 +114,14 @@ struct SplitChoice {
   int64_t bytes;
 };
 
-// The shortest run of 64-token tiles that is worth a CTA of its own: a cut costs the joining
-// kernel about as long as 512 tokens take one CTA.
-constexpr int kMinTiles = 8;
+// The shortest run of 64-token tiles that gets a CTA of its own.  1 sequence of 1500 tokens, 32 query
+// heads on 8 of 128: 11.3 us with runs of 8 tiles, 9.8 of 4, 9.3 of 2; 8 sequences of 1000: 12.5,
+// 11.5, 13.2.
+constexpr int kMinTiles = 4;
+// Contexts of up to this many tokens (a page table's room) are not cut, which saves the joining
+// kernel: 1 sequence of 700 tokens, 4 heads of 64: 8.5 us whole, 11.0 cut; 8 sequences of 1000
+// tokens, 8 kv heads of 128: 12.0 whole, 11.5 cut.
+constexpr int kWholeTokens = 768;
 
 // Whether the tcgen05 kernel takes a call, `rows` query rows per sequence and kv head.  Its time goes
 // with the key tiles of the longest unit (256 rows of one sequence and head) and the waves of units
@@ -130,10 +135,10 @@ constexpr int kMinTiles = 8;
 //   16 sequences, 128 new tokens, 4000 cached: split 606 us, tcgen05 169
 // The split kernel also has the longer start and a second launch: it has to be 15 % ahead.  On
 // contexts of up to 512 tokens, where it does not cut sequences, it falls behind earlier.
-bool prompt_pays(int32_t D, int64_t rows, int64_t heads, bool whole, int num_sms) {
+bool prompt_pays(int32_t D, int64_t rows, int64_t heads, bool few_keys, int num_sms) {
   if (D > 128 || rows <= 32) return false;
   const double pieces = static_cast<double>((rows + 31) / 32) * heads;      // of the split kernel
-  if (whole) return pieces >= 150;
+  if (few_keys) return pieces >= 150;
   const double units = static_cast<double>((rows + 255) / 256) * heads;
   const double waves = units > num_sms ? units / num_sms : 1.0;
   const double split_ns = D == 64 ? 5.1 : D == 96 ? 6.3 : 7.5;
@@ -149,12 +154,12 @@ SplitChoice split_of(const b2b_cache* c, int32_t q_heads, int num_sms) {
   s.nt = rows <= 8 ? 1 : rows <= 16 || c->head_dim > 128 ? 2 : 4;
   s.grid = attend_ctas_per_sm(c->head_dim, s.nt) * num_sms;
   const int64_t most = static_cast<int64_t>(c->max_pages) * c->page_size;
-  s.whole = most <= kMinTiles * 64 ? 1 : 0;
+  s.whole = most <= kWholeTokens ? 1 : 0;
   // no more CTAs than there can be runs
   const int64_t pieces = (rows + 8 * s.nt - 1) / (8 * s.nt) * c->heads * c->batch;
   const int64_t runs = s.whole ? pieces : pieces * ((most / 64 + kMinTiles - 1) / kMinTiles);
   if (runs < s.grid) s.grid = static_cast<int>(runs);
-  s.prompt = prompt_pays(c->head_dim, rows, static_cast<int64_t>(c->batch) * c->heads, s.whole != 0,
+  s.prompt = prompt_pays(c->head_dim, rows, static_cast<int64_t>(c->batch) * c->heads, most <= 512,
                          num_sms);
   s.bytes = s.prompt  ? prompt_workspace(rows, c->batch)
             : s.whole ? 0
@@ -241,7 +246,7 @@ b2b_status b2b_rotary(b2b_dtype dt, int64_t T, int32_t H, int32_t D, int32_t rot
   p.interleaved = layout == B2B_ROTARY_INTERLEAVED;
   p.inverse = inverse;
   p.err = d->err;
-  return launched(launch_rotary(dt == B2B_BF16, p, static_cast<cudaStream_t>(stream)));
+  return launched(launch_rotary(dt == B2B_BF16, p, d->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 b2b_status b2b_cache_append(b2b_dtype dt, const b2b_cache* cache, int64_t T, const void* k,
@@ -289,7 +294,7 @@ b2b_status b2b_cache_append(b2b_dtype dt, const b2b_cache* cache, int64_t T, con
   p.q_heads = q_heads;
   p.rot = rot;
   p.interleaved = layout == B2B_ROTARY_INTERLEAVED;
-  return launched(launch_append(dt == B2B_BF16, p, static_cast<cudaStream_t>(stream)));
+  return launched(launch_append(dt == B2B_BF16, p, d->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 b2b_status b2b_cache_attention_workspace(const b2b_cache* cache, int64_t T, int32_t q_heads,

@@ -14,6 +14,10 @@ __device__ __forceinline__ void index_error(uint32_t* err, uint32_t kernel, uint
   record_error(err, kCodeIndex, kernel, what, index);
 }
 
+// The kernels read with plain loads, not __ldg: that promises data which stays the same for the
+// whole kernel, and a kernel launched early starts while the one that writes its inputs still
+// runs (and an in-place call writes what it reads).
+
 // One sequence of a call: its rows among the new tokens and its length in the cache.
 // Values that leave the rows or the page table are cut down to what fits and recorded.
 struct Sequence {
@@ -26,8 +30,8 @@ __device__ __forceinline__ Sequence load_sequence(const CacheView& c, int b, uin
   Sequence s;
   int64_t end;
   if (c.starts != nullptr) {
-    s.row = __ldg(c.starts + b);
-    end = __ldg(c.starts + b + 1);
+    s.row = c.starts[b];
+    end = c.starts[b + 1];
   } else {
     const int each = static_cast<int>(c.T / c.B);
     s.row = b * each;
@@ -39,7 +43,7 @@ __device__ __forceinline__ Sequence load_sequence(const CacheView& c, int b, uin
     index_error(c.err, kernel, DEC_ERR_STARTS, b);
     s.n = (s.row < 0 || n < 0 || end > c.T) ? 0 : c.max_new;
   }
-  s.len = __ldg(c.lens + b);
+  s.len = c.lens[b];
   const int64_t most = static_cast<int64_t>(c.max_pages) << c.page_shift;
   if (s.len < s.n || s.len > most) {
     index_error(c.err, kernel, DEC_ERR_LENGTH, b);
@@ -129,9 +133,9 @@ struct RawUnit {
 };
 __device__ __forceinline__ RawUnit load_raw(const uint16_t* row, const UnitAt& a, int rot) {
   RawUnit r;
-  r.lo = __ldg(reinterpret_cast<const uint4*>(row + a.d));
+  r.lo = *reinterpret_cast<const uint4*>(row + a.d);
   r.hi = r.lo;
-  if (a.pair) r.hi = __ldg(reinterpret_cast<const uint4*>(row + a.d + rot / 2));
+  if (a.pair) r.hi = *reinterpret_cast<const uint4*>(row + a.d + rot / 2);
   return r;
 }
 
@@ -143,7 +147,7 @@ struct Angles {
 };
 struct AngleRow {
   const float4* t;
-  __device__ __forceinline__ float4 operator[](int i) const { return __ldg(t + i); }
+  __device__ __forceinline__ float4 operator[](int i) const { return t[i]; }
 };
 __device__ __forceinline__ AngleRow angle_row(const float2* row, const UnitAt& a, int interleaved) {
   return AngleRow{reinterpret_cast<const float4*>(row + (interleaved ? a.d / 2 : a.d))};

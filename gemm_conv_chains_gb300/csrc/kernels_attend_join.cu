@@ -55,8 +55,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, 
       v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (at < parts) {
         const float* part = at == 0 ? first : rest + 2 * (at - 1) * part_floats;
-        lse[k] = __ldg(part + RT * D + rr);
-        v[k] = __ldg(reinterpret_cast<const float4*>(part + rr * D + d));
+        lse[k] = part[RT * D + rr];
+        v[k] = *reinterpret_cast<const float4*>(part + rr * D + d);
       }
     }
     float top = m;

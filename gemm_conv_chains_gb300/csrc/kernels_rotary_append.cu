@@ -20,9 +20,9 @@ __device__ __forceinline__ void begin() {
 // unit of a row (16 bytes, or two times 16 that are partners in the half layout; whole sectors
 // either way) for all the heads and tokens that it walks, its angles in registers, and copies
 // what it will turn into a ring of its own in shared memory, kAhead units ahead (cp.async, no
-// barrier: it reads back what it copied itself).  Without the ring the same walk ran 79 us on
-// 16384 tokens of 40 heads (4.2 TB/s), whether a thread asked for one, two or four units at a
-// time in registers: more registers per thread cost as many threads.
+// barrier: it reads back what it copied itself).  16384 tokens of 40 heads of 128 take 54 us so,
+// 6.2 TB/s, 0.92 of the copy rate; one unit per thread, without ring or walk, 66 (and asking for two
+// or four units at a time in registers costs as many threads as it gains requests).
 constexpr int kTurnThreads = 256;
 constexpr int kAhead = 8;
 
@@ -55,10 +55,9 @@ __device__ __forceinline__ void turn_one(const TurnRows& r, int64_t t, int h, in
 // (units, groups of heads, rows side by side where they are short) in x, idle beyond.
 template <bool BF16, class Position>
 __device__ __forceinline__ void turn_rows(const TurnRows& r, int64_t t0, int64_t t1, int units,
-                                          Position position) {
+                                          int G, Position position) {
   extern __shared__ __align__(16) uint4 ring[];
-  const int groups = static_cast<int>(blockDim.x) / units;
-  const int G = groups < r.H ? groups : r.H, Z = groups / G;     // heads and rows side by side
+  const int Z = static_cast<int>(blockDim.x) / units / G;        // rows side by side
   const int group = static_cast<int>(threadIdx.x) / units;
   const int z = group / G, first = group - z * G;
   const UnitAt at = unit_at(threadIdx.x - group * units, r.rot, r.interleaved);
@@ -117,18 +116,37 @@ int turn_units(int D, int rot, int interleaved) {
 }
 constexpr int kTurnSmem = kAhead * 2 * kTurnThreads * 16;
 
-// Rows per block of the walk: about 16 units per thread, or 0 where that leaves too few blocks to
-// fill the SMs twice over, and one unit per thread is faster (8193 rows of 12 heads of 64: 5.3 us
-// against 7.5; 16384 rows of 40 heads of 128: 79 us against 68).
-int64_t turn_rows_per_block(int64_t T, int H, int units) {
-  const int64_t per_row = static_cast<int64_t>(H) * units;
-  const int64_t rows = (16 * kTurnThreads + per_row - 1) / per_row;
-  return T / rows >= 1024 ? rows : 0;
+// How a call is cut for the walk: heads of a row side by side in a block, and rows per block (0:
+// no walk).  A thread takes at least 8 heads of a row, so that its angles, which come from a
+// dependent load, serve 8 units; of the splits that allow it, the one that leaves the fewest
+// threads idle, and then the widest.  Six waves of blocks: the SMs do not finish alike, and blocks
+// of one full wave ran 93 us where these run 82 (32768 rows of 32 heads of 128).  Where a wave
+// leaves a thread fewer than 8 units, one unit per thread is faster (16384 rows of 12 heads of 64:
+// 11.2 us against 12.1; 8192 rows of 32 heads of 128: 27.0 against 24.8, 16384 of 40: 66 against 54).
+struct Walk {
+  int heads;
+  int64_t rows;
+};
+constexpr int kWalkCtas = 3;           // per SM, what the rings leave room for
+Walk walk_of(int64_t T, int H, int units, int num_sms) {
+  constexpr int kLeast = 8, kWaves = 6;
+  const int64_t slots = static_cast<int64_t>(num_sms) * kWalkCtas;
+  if (T * H * units < kLeast * slots * kTurnThreads) return Walk{1, 0};
+  const int groups = kTurnThreads / units;
+  int heads = 1, most = 0;
+  for (int G = 1; G <= groups && (G == 1 || (H + G - 1) / G >= kLeast); ++G) {
+    const int64_t mine = (H + G - 1) / G;
+    const int busy = static_cast<int>(int64_t{1024} * H / (mine * G) * (groups / G * G) / groups);
+    if (busy >= most) most = busy, heads = G;
+  }
+  const int Z = groups / heads;        // rows side by side
+  const int64_t rows = (T + slots * kWaves - 1) / (slots * kWaves);
+  return Walk{heads, (rows + Z - 1) / Z * Z};
 }
 
 // position(t) of rotary: the given one, if the table has it.
 __device__ __forceinline__ int rotary_position(const RotaryParams& p, int64_t t) {
-  const int pos = __ldg(p.positions + t);
+  const int pos = p.positions[t];
   if (pos >= 0 && pos < p.table_len) return pos;
   index_error(p.err, DK_ROTARY, DEC_ERR_POSITION, static_cast<uint32_t>(t));
   return -1;
@@ -140,11 +158,11 @@ __device__ __forceinline__ TurnRows rows_of(const RotaryParams& p) {
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kTurnThreads, 3) rotary_walk_kernel(const RotaryParams p, int units,
-                                                                      int64_t rows) {
+__global__ void __launch_bounds__(kTurnThreads, kWalkCtas) rotary_walk_kernel(const RotaryParams p, int units,
+                                                                      int heads, int64_t rows) {
   begin();
   const int64_t t0 = blockIdx.x * rows, t1 = t0 + rows < p.T ? t0 + rows : p.T;
-  turn_rows<BF16>(rows_of(p), t0, t1, units, [&](int64_t t) { return rotary_position(p, t); });
+  turn_rows<BF16>(rows_of(p), t0, t1, units, heads, [&](int64_t t) { return rotary_position(p, t); });
 }
 
 template <bool BF16>
@@ -171,16 +189,17 @@ cudaError_t allow_smem(const void* fn, int bytes, int& set_on) {
   return e;
 }
 
-cudaError_t launch_rotary(bool bf16, const RotaryParams& p, cudaStream_t s) {
+cudaError_t launch_rotary(bool bf16, const RotaryParams& p, int num_sms, cudaStream_t s) {
   const int units = turn_units(p.D, p.rot, p.interleaved);
   if (units > kTurnThreads) return cudaErrorInvalidConfiguration;
-  if (const int64_t rows = turn_rows_per_block(p.T, p.H, units); rows > 0) {
+  if (const Walk w = walk_of(p.T, p.H, units, num_sms); w.rows > 0) {
     static thread_local int set_on[2] = {-1, -1};
     auto* fn = bf16 ? rotary_walk_kernel<true> : rotary_walk_kernel<false>;
     if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), kTurnSmem, set_on[bf16]);
         e != cudaSuccess)
       return e;
-    return launch_early(fn, (p.T + rows - 1) / rows, kTurnThreads, kTurnSmem, s, p, units, rows);
+    return launch_early(fn, (p.T + w.rows - 1) / w.rows, kTurnThreads, kTurnSmem, s, p, units, w.heads,
+                        w.rows);
   }
   const int per_token = p.H * units;
   const int tpb = per_token >= kTurnThreads ? 1 : kTurnThreads / per_token;
@@ -242,7 +261,7 @@ cudaError_t launch_rotary_table(float2* table, int64_t n, int32_t half, const do
 // time from L1 or L2.  One new token per sequence is bound by the latency of its dependent loads
 // (sequence, page number and tokens, scale); prompts by the instructions per element, 0.6 of the
 // issue slots (ragged prompts, 18 k tokens, 8 heads of 128, pages of 32: 72 us with an index
-// division per unit and an exact division per element, PAGES_US so).
+// division per unit and an exact division per element, 41 us so).
 // The queries of few tokens are turned by further blocks of the same launch; those of many by a
 // launch of the walk above.
 constexpr int kAppendThreads = 128;
@@ -307,7 +326,7 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int b, int j,
   const int lo_tok = first_slot > start ? first_slot : start;
   const int hi_tok = s.len - first_slot > page ? first_slot + page : s.len;
   const int held = first_slot < start ? start - first_slot : 0;
-  const int id = __ldg(c.page_table + static_cast<int64_t>(b) * c.max_pages + pi);
+  const int id = c.page_table[static_cast<int64_t>(b) * c.max_pages + pi];
   const int rot = ROTATION != 0 ? p.rot : 0;
   constexpr int inter = ROTATION != 2;                // without a rotation: plain vectors
   const int units = row_units(c.D, rot, inter);
@@ -415,7 +434,7 @@ __device__ __forceinline__ int sequence_of(const CacheView& c, int64_t t) {
   const int lane = threadIdx.x & 31;
   int count = 0;
   for (int b0 = 0; b0 < c.B; b0 += 32) {
-    const bool in = b0 + lane < c.B && __ldg(c.starts + b0 + lane) <= t;
+    const bool in = b0 + lane < c.B && c.starts[b0 + lane] <= t;
     const uint32_t vote = __ballot_sync(0xffffffffu, in);
     count += __popc(vote);
     if (vote != 0xffffffffu) break;
@@ -448,12 +467,12 @@ __device__ __forceinline__ TurnRows rows_of(const AppendParams& p) {
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kTurnThreads, 3) query_walk_kernel(const AppendParams p, int units,
-                                                                     int64_t rows) {
+__global__ void __launch_bounds__(kTurnThreads, kWalkCtas) query_walk_kernel(const AppendParams p, int units,
+                                                                     int heads, int64_t rows) {
   begin();
   const int64_t t0 = blockIdx.x * rows, t1 = t0 + rows < p.c.T ? t0 + rows : p.c.T;
   QueryPosition position(p, t0);
-  turn_rows<BF16>(rows_of(p), t0, t1, units, [&](int64_t t) { return position(t); });
+  turn_rows<BF16>(rows_of(p), t0, t1, units, heads, [&](int64_t t) { return position(t); });
 }
 
 template <bool BF16, int ROTATION>
@@ -481,27 +500,28 @@ __global__ void __launch_bounds__(kAppendThreads, 8) append_kernel(const AppendP
   else append_page<BF16, ROTATION>(p, b, j, h, false);
 }
 
-cudaError_t launch_append(bool bf16, const AppendParams& p, cudaStream_t s) {
+cudaError_t launch_append(bool bf16, const AppendParams& p, int num_sms, cudaStream_t s) {
   const int page = 1 << p.c.page_shift;
   // max_new tokens from any slot on touch at most this many pages
   const int per_seq = (p.c.max_new - 1 + page - 1) / page + 1;
   const int64_t page_blocks = static_cast<int64_t>(p.c.B) * per_seq * p.c.heads * 2;
   const int units = turn_units(p.c.D, p.rot, p.interleaved);
-  const int64_t rows = p.q != nullptr ? turn_rows_per_block(p.c.T, p.q_heads, units) : 0;
-  const int64_t blocks = page_blocks + (p.q != nullptr && rows == 0 ? p.c.T : 0);
+  const Walk w = p.q != nullptr ? walk_of(p.c.T, p.q_heads, units, num_sms) : Walk{1, 0};
+  const int64_t blocks = page_blocks + (p.q != nullptr && w.rows == 0 ? p.c.T : 0);
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   auto* append = p.table == nullptr ? (bf16 ? append_kernel<true, 0> : append_kernel<false, 0>)
                  : p.interleaved    ? (bf16 ? append_kernel<true, 1> : append_kernel<false, 1>)
                                     : (bf16 ? append_kernel<true, 2> : append_kernel<false, 2>);
   if (cudaError_t e = launch_early(append, blocks, kAppendThreads, 0, s, p, page_blocks, per_seq);
-      e != cudaSuccess || rows == 0)
+      e != cudaSuccess || w.rows == 0)
     return e;
   static thread_local int set_on[2] = {-1, -1};
   auto* fn = bf16 ? query_walk_kernel<true> : query_walk_kernel<false>;
   if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), kTurnSmem, set_on[bf16]);
       e != cudaSuccess)
     return e;
-  return launch_early(fn, (p.c.T + rows - 1) / rows, kTurnThreads, kTurnSmem, s, p, units, rows);
+  return launch_early(fn, (p.c.T + w.rows - 1) / w.rows, kTurnThreads, kTurnSmem, s, p, units, w.heads,
+                      w.rows);
 }
 
 }  // namespace b2b

@@ -214,7 +214,10 @@ b2b_status maxpool2x2_nhwc(b2b_dtype dt, int32_t N, int32_t H, int32_t W, int32_
  * heads and channels are dense within a row), since they are usually slices of one fused
  * projection; and numbers that only the device knows (lengths, page numbers, positions) are
  * checked there: one out of range is never followed, but recorded in an error word of these
- * operators (b2b_get_cache_error), and the outputs that depend on it are unspecified. */
+ * operators (b2b_get_cache_error), and the outputs that depend on it are unspecified.  Waits
+ * in their kernels are bounded by one second each, whatever b2b_set_wait_limit_ns says, and one
+ * that runs out is recorded in that word too.  All launches are asynchronous on `stream`, and
+ * none allocates: a call can be captured into a graph. */
 
 /* The rotation's channel pairs: HALF pairs channel i with i + rot / 2, INTERLEAVED pairs 2i
  * with 2i + 1; i < rot / 2 in both. */
@@ -247,7 +250,7 @@ b2b_status b2b_rotary(b2b_dtype dt, int64_t T, int32_t H, int32_t D, int32_t rot
                       void* out, int64_t ldo, void* stream);
 
 /* A paged cache and the sequences of one call.  Codes are e4m3 (no infinities, one NaN); the
- * value of a code is code * scale, one fp32 scale per page and kv head.  Position j of sequence
+ * value of a code is code * scale, one fp32 scale per page and kv head, >= 0.  Position j of sequence
  * s lies in slot j % page_size of page page_table[s][j / page_size].  The call's new tokens are
  * rows [starts[s], starts[s + 1]) of its inputs, positions lens[s] - n .. lens[s] - 1.  Page
  * numbers of positions at or past lens[s] are not read.  Every array is a device array. */
@@ -276,7 +279,7 @@ typedef struct b2b_cache {
  *   s' = max(s, A / 448, 2^-64),   new codes = e4m3(y / s'),
  *   and where s' > s the page's older codes become e4m3(code * (s / s'))
  * in fp32, to nearest even, saturating (an infinity becomes +-448 s'; a NaN stays one).  Calling
- * again with the same arguments changes nothing.  Pages that are written belong to one
+ * again with the same arguments leaves the cache as it is.  Pages that are written belong to one
  * sequence.  k, v: T rows of heads x head_dim, strides ldk, ldv. */
 b2b_status b2b_cache_append(b2b_dtype dt, const b2b_cache* cache, int64_t T, const void* k,
                             int64_t ldk, const void* v, int64_t ldv, const float* table,
@@ -289,12 +292,14 @@ b2b_status b2b_cache_append(b2b_dtype dt, const b2b_cache* cache, int64_t T, con
  *   z_j = cap(scale * q . k_j) + slopes[h] * (j - i),   cap(x) = softcap * tanh(x / softcap)
  * (softcap 0: none; slopes NULL: no bias; slopes: device fp32 [q_heads]).  A row that sees no
  * key is zero.  Sums, softmax and bias in fp32; the probabilities are rounded to fp16 before
- * the second product (11 bits, relative to the row's maximum), out once to dt.
+ * the second product (11 bits; few rows per sequence with an fp16 output: twice that), out once
+ * to dt.
  * q: T rows of q_heads x head_dim, stride ldq; out: dense [T][q_heads][head_dim], not q.
  * Nothing past a row's reach enters it, whatever its slots hold.
  * workspace: device memory of at least the bytes that b2b_cache_attention_workspace gives for
  * the same cache, T and q_heads (16-byte aligned; NULL where that is 0), free again when the
- * call's work on `stream` is done; its contents need no preparation. */
+ * call's work on `stream` is done; its contents need no preparation.
+ * B2B_ERR_UNSUPPORTED also for a call of more than 2e9 (64 keys x one tile of query rows). */
 b2b_status b2b_cache_attention_workspace(const b2b_cache* cache, int64_t T, int32_t q_heads,
                                          int64_t* bytes);
 b2b_status b2b_cache_attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, const void* q,

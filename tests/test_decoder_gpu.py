@@ -74,6 +74,30 @@ def test_rotary_strided_and_in_place(layout):
     assert torch.equal(rows[:, :1], keep[:, :1]) and torch.equal(rows[:, 1 + H:], keep[:, 1 + H:])
 
 
+@pytest.mark.parametrize("dt,layout,T,H,D,rot,in_place", [
+    ("f16", "half", 7501, 33, 64, 64, False), ("bf16", "interleaved", 5003, 20, 96, 96, True),
+    ("bf16", "half", 30011, 7, 96, 48, True), ("f16", "half", 70001, 3, 48, 16, False),
+    ("f16", "interleaved", 30001, 1, 256, 256, False), ("bf16", "interleaved", 4001, 1, 2048, 2048, False),
+    ("bf16", "half", 2049, 130, 64, 64, True), ("f16", "interleaved", 9000, 11, 128, 64, True)])
+def test_rotary_of_many_rows(dt, layout, T, H, D, rot, in_place):
+    """Enough rows for the kernel that walks them; strided, and the same bits as short calls give."""
+    rows = _randn(T, T, H + 1, D).to(DT[dt]).cuda()
+    x = rows[:, :H]
+    was = x.cpu()
+    table = ops.rotary_table(2000, rot)
+    pos = torch.randint(2000, (T,), generator=torch.Generator().manual_seed(2), dtype=torch.int32)
+    cuda_pos = pos.cuda()
+    pieces = [(a, min(a + 50, T)) for a in (0, T // 3, T - 50)]
+    short = [ops.rotary(x[a:b], table, cuda_pos[a:b], layout) for a, b in pieces]
+    beside = rows[:, H].clone()
+    y = ops.rotary(x, table, cuda_pos, layout, out=x) if in_place else \
+        ops.rotary(x, table, cuda_pos, layout)
+    assert torch.equal(rows[:, H], beside)
+    for (a, b), want in zip(pieces, short):
+        assert torch.equal(y[a:b], want)
+    _check_rotary(y, was, table.cpu().double()[pos.long()], layout)
+
+
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 def test_rotary_gradient_is_the_inverse(layout):
     """<rotary(x), w> differentiated: by the formula (the inverse of w) and by differences."""
@@ -202,6 +226,23 @@ def test_append(dt, layout, older, new, heads, D, rot, page):
                      layout=layout)
     for x, y in zip(again, (kc, vc, ks, vs)):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_append_turns_the_queries_of_many_rows(layout):
+    """Enough query rows for the kernel that walks them, over ragged and empty sequences."""
+    older, new, heads, D, q_heads = [5, 0, 100, 3, 0], [1500, 0, 2111, 1, 700], 1, 64, 61
+    c = ref.Cache(older, new, heads, D, 32, seed=9)
+    rows = _randn(D, c.T, 2 * heads + q_heads, D).to(torch.bfloat16)
+    dev = rows.cuda()
+    table = ops.rotary_table(max(c.lens), D)
+    kc, vc, ks, vs, *rest = c.args()
+    q = dev[:, 2 * heads:]
+    q_out = ops.cache_append(dev[:, :heads], dev[:, heads:2 * heads], kc, vc, ks, vs, *rest,
+                             table=table, layout=layout, q=q)
+    pos = torch.cat([torch.arange(a, a + n) for a, n in zip(older, new)]).int()
+    _check_rotary(q_out, rows[:, 2 * heads:], table.cpu().double()[pos.long()], layout)
+    assert torch.equal(q_out[1400:1600], ops.rotary(q[1400:1600], table, pos[1400:1600].cuda(), layout))
 
 
 def test_append_without_rotation_or_starts():
