@@ -254,14 +254,17 @@ cudaError_t launch_rotary_table(float2* table, int64_t n, int32_t half, const do
 // One block per page that a sequence's new tokens touch, kv head, and pool (keys or
 // values).  With A the largest finite magnitude of the block's new values (keys after the
 // rotation) and s the page's scale if it already holds older tokens of the sequence, else 0:
-//   s' = max(s, A / 448, 2^-64);  new codes e4m3(y / s'), saturating;
+//   s' = max(s, A / 448, 2^-64);  new codes e4m3(y / s'), saturating (where s' is A / 448, the
+//   quotient is y 448 / A, without the rounding of s': an exact tie between two codes, frequent in
+//   values of 8 or 11 bits, stays one and goes to even);
 //   older codes e4m3(code * (s / s')) if s' > s, else untouched.
 // A thread keeps one unit of a row, asks for its first tokens' along with the page number and holds
-// them between the maximum and the codes; what a page has beyond that is read twice, the second
-// time from L1 or L2.  One new token per sequence is bound by the latency of its dependent loads
+// them between the maximum and the codes; what a page has beyond that is read twice, in batches, the
+// second time from L1 or L2.  One new token per sequence is bound by the latency of its dependent loads
 // (sequence, page number and tokens, scale); prompts by the instructions per element, 0.6 of the
 // issue slots (ragged prompts, 18 k tokens, 8 heads of 128, pages of 32: 72 us with an index
-// division per unit and an exact division per element, 41 us so).
+// division per unit and an exact division per element, 43 us so; fewer blocks of several heads each,
+// larger blocks, or more of them on fewer registers: 2 to 25 % slower).
 // The queries of few tokens are turned by further blocks of the same launch; those of many by a
 // launch of the walk above.
 constexpr int kAppendThreads = 128;
@@ -276,19 +279,24 @@ __device__ __forceinline__ void most_of(const float (&v)[8], float& most) {
   }
 }
 
-// Eight values as codes of a scale and its reciprocal.  FINITE: the quotients by the reciprocal, each
-// corrected once by its residual y - q s (Markstein's step), which rounds like the quotient itself
-// and not like the product; an infinity has no residual and takes the exact division.
+// What values are divided by on the way to their codes: code = (y * up) / by.
+struct Divisor {
+  float up, by, inv;
+};
+// Eight values as codes.  FINITE: the quotients by the reciprocal, each corrected once by its
+// residual q s - y (Markstein's step; with this sign -0 stays -0), which rounds like the quotient
+// itself and not like the product; an infinity has no residual and takes the exact division.
 template <bool FINITE>
-__device__ __forceinline__ void store_codes(uint8_t* dst, const float (&v)[8], float scale, float inv) {
+__device__ __forceinline__ void store_codes(uint8_t* dst, const float (&v)[8], const Divisor& s) {
   float q[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
+    const float y = v[e] * s.up;
     if (FINITE) {
-      q[e] = v[e] * inv;
-      q[e] = fmaf(fmaf(-q[e], scale, v[e]), inv, q[e]);
+      q[e] = y * s.inv;
+      q[e] = fmaf(fmaf(q[e], s.by, -y), -s.inv, q[e]);
     } else {
-      q[e] = __fdiv_rn(v[e], scale);
+      q[e] = __fdiv_rn(y, s.by);
     }
   }
   uint32_t w[4];
@@ -340,12 +348,17 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int b, int j,
   if (ROTATION == 0) at.turned = false;
   if (ROTATION != 2) at.pair = false;
   const int count = first < G ? hi_tok - lo_tok : 0;
-  // the first of them are asked for together with the page number
+  // a batch of them is in registers at a time; the first is asked for together with the page number
   constexpr int kHeld = ROTATION == 2 ? 2 : 4;        // a pair unit is two vectors
   RawUnit held_raw[kHeld];
+  auto ask = [&](int batch) {
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k)
-    if (first + k * G < count) held_raw[k] = load_raw(src + (first + k * G) * ld, at, rot);
+    for (int k = 0; k < kHeld; ++k) {
+      const int tok = first + (batch * kHeld + k) * G;
+      if (tok < count) held_raw[k] = load_raw(src + tok * ld, at, rot);
+    }
+  };
+  ask(0);
   if (id < 0 || id >= c.pages) {
     if (threadIdx.x == 0) index_error(c.err, DK_APPEND, DEC_ERR_PAGE, static_cast<uint32_t>(b));
     return;
@@ -359,22 +372,26 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int b, int j,
   uint8_t* codes = (value ? c.v : c.k) + (page_at << c.page_shift) * c.D;
   const float before = held > 0 ? *scale_at : 0.f;
 
-  // this thread's units, turned: f(token, lo, hi)
+  // this thread's units, turned: f(token, lo, hi); every other time from the last batch to the first,
+  // so that each pass begins with the one that the last pass ended with
+  const int batches = (hi_tok - lo_tok + kHeld * G - 1) / (kHeld * G);
+  int batch = 0, step = 1;
   auto each = [&](auto f) {
     float lo[8], hi[8];
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-      const int tok = first + k * G;
-      if (tok >= count) break;
-      turn_unit<BF16>(held_raw[k], at, angle_row(cs + tok * (rot / 2), at, inter), inter, 1.f, lo, hi);
-      f(tok, lo, hi);
-    }
 #pragma unroll 1
-    for (int tok = first + kHeld * G; tok < count; tok += G) {
-      turn_unit<BF16>(load_raw(src + tok * ld, at, rot), at, angle_row(cs + tok * (rot / 2), at, inter),
-                      inter, 1.f, lo, hi);
-      f(tok, lo, hi);
+    for (int i = 0;;) {
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        const int tok = first + (batch * kHeld + k) * G;
+        if (tok >= count) break;
+        turn_unit<BF16>(held_raw[k], at, angle_row(cs + tok * (rot / 2), at, inter), inter, 1.f, lo, hi);
+        f(tok, lo, hi);
+      }
+      if (++i == batches) break;
+      batch += step;
+      ask(batch);
     }
+    step = -step;
   };
   float most = 0.f;
   each([&](int, const float (&lo)[8], const float (&hi)[8]) {
@@ -391,19 +408,24 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int b, int j,
     });
     most = block_max(most);
   }
-  const float after = fmaxf(fmaxf(before, __fdiv_rn(most, kE4m3Max)), kScaleMin);
-  const float inv = __fdiv_rn(1.f, after);
+  const float fit = __fdiv_rn(most, kE4m3Max);
+  const float after = fmaxf(fmaxf(before, fit), kScaleMin);
+  // 448 = 0.875 * 2^9: both factors leave 16-bit values exact.  (An equal older scale counts as A's,
+  // so that the same call again gives the same codes.)
+  Divisor by{1.f, after, 0.f};
+  if (after == fit) by = Divisor{0.875f, most * 0.001953125f, 0.f};
+  by.inv = __fdiv_rn(1.f, by.by);
 
   uint8_t* dst = codes + (lo_tok - first_slot) * c.D + at.d;
   if (finite) {
     each([&](int tok, const float (&lo)[8], const float (&hi)[8]) {
-      store_codes<true>(dst + tok * c.D, lo, after, inv);
-      if (at.pair) store_codes<true>(dst + tok * c.D + rot / 2, hi, after, inv);
+      store_codes<true>(dst + tok * c.D, lo, by);
+      if (at.pair) store_codes<true>(dst + tok * c.D + rot / 2, hi, by);
     });
   } else {
     each([&](int tok, const float (&lo)[8], const float (&hi)[8]) {
-      store_codes<false>(dst + tok * c.D, lo, after, inv);
-      if (at.pair) store_codes<false>(dst + tok * c.D + rot / 2, hi, after, inv);
+      store_codes<false>(dst + tok * c.D, lo, by);
+      if (at.pair) store_codes<false>(dst + tok * c.D + rot / 2, hi, by);
     });
   }
   if (held > 0 && after > before) {

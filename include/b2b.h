@@ -278,7 +278,8 @@ typedef struct b2b_cache {
  * tokens of the sequence (else 0):
  *   s' = max(s, A / 448, 2^-64),   new codes = e4m3(y / s'),
  *   and where s' > s the page's older codes become e4m3(code * (s / s'))
- * in fp32, to nearest even, saturating (an infinity becomes +-448 s'; a NaN stays one).  Calling
+ * in fp32, to nearest even, saturating (y / s' as y * 448 / A where that is s', so that exact
+ * ties between two codes go to even; an infinity becomes +-448 s'; a NaN stays one).  Calling
  * again with the same arguments leaves the cache as it is.  Pages that are written belong to one
  * sequence.  k, v: T rows of heads x head_dim, strides ldk, ldv. */
 b2b_status b2b_cache_append(b2b_dtype dt, const b2b_cache* cache, int64_t T, const void* k,

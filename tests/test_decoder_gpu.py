@@ -245,6 +245,33 @@ def test_append_turns_the_queries_of_many_rows(layout):
     assert torch.equal(q_out[1400:1600], ops.rotary(q[1400:1600], table, pos[1400:1600].cuda(), layout))
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_append_sends_exact_ties_to_even(dt):
+    """Values of few bits: y * 448 / A often lies exactly between two codes.  The quotient of such
+    short numbers is never close to a tie without being one, so the codes have one right answer."""
+    c = ref.Cache([0, 0], [64, 70], 2, 64, 32, seed=5)
+    v = (_randn(21, c.T, 2, 64) * 37).round().clamp(-112, 112).to(DT[dt])
+    v[:64, 0] *= 2 ** -5
+    v[3, 1, 7] = 126                                  # pages whose A is not a power of two times 7
+    v[90, 0, 1] = -121
+    kc, vc, ks, vs, *rest = c.args()
+    ops.cache_append(torch.zeros_like(v).cuda(), v.cuda(), kc, vc, ks, vs, *rest)
+    vc = vc.cpu()
+    ties = 0
+    for b, (at, n) in enumerate([(0, 64), (64, 70)]):
+        for j in range(-(-n // 32)):
+            part = v[at + 32 * j: at + min(n, 32 * j + 32)].double().transpose(0, 1)
+            A = part.abs().amax((1, 2), keepdim=True)
+            x = part * 448 / A
+            want = x.float().to(F8)
+            got = vc[c.table[b, j], :, : part.shape[1]]
+            assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+            down = (x.float() * (1 - 2.0 ** -20)).to(F8).float()
+            up = (x.float() * (1 + 2.0 ** -20)).to(F8).float()
+            ties += int((down != up).sum())
+    assert ties > 100
+
+
 def test_append_without_rotation_or_starts():
     c = ref.Cache([30, 0, 5], [2, 2, 2], 2, 64, 16, seed=2)
     k, v = _randn(1, 6, 2, 64).half(), _randn(2, 6, 2, 64).half() * 0.001
