@@ -33,8 +33,8 @@
 // scales go into P before the rounding, relative to a running power of two, so that they cannot
 // under- or overflow it.
 //
-// Measured: 128 sequences of 8192 tokens, 32 query heads on 8 of 128 channels: 333 us, 6.45 TB/s,
-// 0.95 of the copy rate; 64 ragged ones of up to 4096: 63 us, 4.8 TB/s (a run's start, its page
+// Measured: 128 sequences of 8192 tokens, 32 query heads on 8 of 128 channels: 339 us, 6.34 TB/s,
+// 0.94 of the copy rate; 64 ragged ones of up to 4096: 63 us, 4.8 TB/s (a run's start, its page
 // numbers and the joining weigh more); 5 drafted tokens, 256 channels, softcap and bias: 47 us,
 // 3.2 TB/s, where the arithmetic counts too (two CTAs per SM for the registers of 16 rows).
 #pragma once

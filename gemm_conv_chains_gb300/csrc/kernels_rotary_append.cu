@@ -261,7 +261,7 @@ cudaError_t launch_rotary_table(float2* table, int64_t n, int32_t half, const do
 // A thread keeps one unit of a row, asks for its first tokens' along with the page number and holds
 // them between the maximum and the codes; what a page has beyond that is read twice, in batches, the
 // second time from L1 or L2.  One new token per sequence is bound by the latency of its dependent loads
-// (sequence, page number and tokens, scale); prompts by the instructions per element, 0.6 of the
+// (sequence, page number and tokens, scale); prompts by their instructions, 0.74 of the
 // issue slots (ragged prompts, 18 k tokens, 8 heads of 128, pages of 32: 72 us with an index
 // division per unit and an exact division per element, 44 us so; fewer blocks of several heads each,
 // larger blocks, or more of them on fewer registers: 2 to 25 % slower).
