@@ -546,6 +546,42 @@ def test_attention_past_32_bit_offsets():
     assert torch.equal(ks[shift:], args[2])
 
 
+def test_prompts_past_32_bit_offsets():
+    """The same for prompts, with query rows that lie 2^24 elements apart."""
+    heads, page, D, Hq = 8, 32, 128, 16
+    pages = 2 ** 32 // (heads * page * D) + 200
+    small = _prompt_case(17, new=40)
+    q = _randn(8, small.T, Hq, D).half().cuda()
+    far = torch.empty(small.T * 2 ** 24, dtype=torch.float16, device="cuda").as_strided(
+        (small.T, Hq, D), (2 ** 24, D, 1))
+    far.copy_(q)
+    kc = torch.empty(pages, heads, page, D, dtype=F8, device="cuda")
+    vc = torch.empty_like(kc)
+    ks = torch.empty(pages, heads, device="cuda")
+    vs = torch.empty_like(ks)
+    shift = pages - small.pages
+    kc[shift:], vc[shift:] = small.k.cuda(), small.v.cuda()
+    ks[shift:], vs[shift:] = small.ks.cuda(), small.vs.cuda()
+    args = small.args()
+    table = torch.where(args[4] >= 0, args[4] + shift, -1).to(torch.int32)
+    got = ops.cache_attention(far, kc, vc, ks, vs, table, *args[5:])
+    assert torch.equal(got, ops.cache_attention(q, *args))
+
+
+@pytest.mark.parametrize("T", [260, 9000])
+def test_rotary_past_32_bit_offsets(T):
+    """Rows far apart, few of them and enough for the kernel that walks them."""
+    H, D = 20, 64
+    ld = 2 ** 33 // T // 8 * 8
+    x = _randn(T, T, H, D).bfloat16().cuda()
+    far = torch.empty(T * ld, dtype=torch.bfloat16, device="cuda").as_strided((T, H, D), (ld, D, 1))
+    far.copy_(x)
+    table = ops.rotary_table(100, D)
+    pos = (torch.arange(T, dtype=torch.int32) % 100).cuda()
+    want = ops.rotary(x, table, pos, "interleaved")
+    assert torch.equal(ops.rotary(far, table, pos, "interleaved", out=far), want)
+
+
 def test_attention_index_errors_are_recorded():
     c = ref.Cache([100, 40], [1, 1], 2, 64, 16, seed=17)
     q = _randn(5, 2, 4, 64).half().cuda()
