@@ -30,8 +30,9 @@
 // bf16 output.  For fp16 outputs, whose own rounding is no coarser, the rest that this rounding
 // leaves is multiplied as well (one token over 250001 cached, error against 64 bits 3.0e-4
 // without it, 2.1e-4 with it, which is the output's own rounding; 30.8 us -> 32).  The value
-// scales go into P before the rounding, relative to a running power of two, so that they cannot
-// under- or overflow it.
+// scales go into P before the rounding, and a row's running reference is that of the products (of
+// z + log2 scale), not of z alone: what a row's output mostly consists of keeps all of P's bits,
+// whatever the scales of the pages that it attends to less.
 //
 // Measured: 128 sequences of 8192 tokens, 32 query heads on 8 of 128 channels: 339 us, 6.34 TB/s,
 // 0.94 of the copy rate; 64 ragged ones of up to 4096: 63 us, 4.8 TB/s (a run's start, its page
@@ -52,6 +53,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float rcp_fast(float x) {
@@ -368,8 +374,10 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
     }
     uint32_t qf[NT == 1 ? KS : 1][2];
     float qfactor[NT][2];                            // of rows 8 nt + 2 t, + 1
-    int limit[NT][2];                                // last key each of them sees
-    float slope[NT][2], behind[NT][2];               // behind: of the tile's last row, tokens
+    // The last key that each of them sees; with MODS as how far it lies behind the tile's last row's,
+    // which gives the distance of key and row as well.
+    int limit[MODS ? 1 : NT][2];
+    float slope[MODS ? NT : 1][2], behind[MODS ? NT : 1][2];
     {
       float amax = 0.f;
 #pragma unroll
@@ -417,11 +425,13 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
         const bool valid = r < rows;
         const int tq = valid ? r / p.group : 0;
         qfactor[nt][i] = row_units[8 * nt + 2 * t + i] * p.scale * (MODS ? 1.f : kLog2e);
-        limit[nt][i] = valid ? start + tq : 0x7FFFFFFF;
-        slope[nt][i] = 0.f;
-        behind[nt][i] = static_cast<float>(valid ? high_limit - limit[nt][i] : 0);
-        if (MODS && p.slopes != nullptr && valid)
-          slope[nt][i] = p.slopes[h * p.group + (r - tq * p.group)];
+        if constexpr (MODS) {
+          behind[nt][i] = static_cast<float>(valid ? high_limit - (start + tq) : 0);
+          slope[nt][i] = 0.f;
+          if (p.slopes != nullptr && valid) slope[nt][i] = p.slopes[h * p.group + (r - tq * p.group)];
+        } else {
+          limit[nt][i] = valid ? start + tq : 0x7FFFFFFF;
+        }
       }
 
     float o[KS][NT][4];
@@ -437,7 +447,6 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
       m[nt][0] = m[nt][1] = kNoMax;
       l[nt][0] = l[nt][1] = 0.f;
     }
-    float vref = 0.f, vref_inv = 0.f;
 
     // ---- the strips ----
     for (int stage = 0; strip < strip_end; strip += kAttendWarps) {
@@ -477,27 +486,33 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
       const bool edge = strip * kStrip + kStrip - 1 > low_limit;
       // scores in the log2 domain
       const float away = MODS ? static_cast<float>(tok0 - high_limit) : 0.f;
+      auto hidden = [&](int nt, int i, int k) -> bool {      // token tok0 + 8 k from row 8 nt + 2 t + i
+        if constexpr (MODS) return away + static_cast<float>(8 * k) + behind[nt][i] > 0.f;
+        else return tok0 + 8 * k > limit[nt][i];
+      };
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float z = (x[nt][e] + x2[nt][e]) * (qfactor[nt][e & 1] * sc.x);
-          if (MODS) {
+          if constexpr (MODS) {
             if (p.softcap > 0.f)                     // cap tanh(z / cap); tanh y = 1 - 2 / (e^2y + 1)
               z = p.softcap - 2.f * p.softcap *
                       rcp_fast(exp2_fast(z * (2.f * kLog2e / p.softcap)) + 1.f);
             z = fmaf(slope[nt][e & 1], away + static_cast<float>(8 * (e >> 1)) + behind[nt][e & 1], z) * kLog2e;
           }
-          if (edge && tok0 + 8 * (e >> 1) > limit[nt][e & 1]) z = -INFINITY;
+          if (edge && hidden(nt, e & 1, e >> 1)) z = -INFINITY;
           x[nt][e] = z;
         }
-      // The running maximum is only a reference: it moves when a score is more than 2^8 above
-      // it (P stays below 2^8, well inside fp16), so most strips neither reduce nor rescale.
+      // A row's reference m is for e = 2^(z - m) times the page's value scale, which is P: it moves
+      // when one would be above 2^15, inside fp16, and then to where that one is 2^7, so that most
+      // strips neither reduce nor rescale.  e itself, which the row sum takes, stays below 2^96.
+      const float room = fminf(15.f - log2_fast(sc.y), 96.f);
       bool above = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) above |= x[nt][e] > m[nt][e & 1] + 8.f;
+        for (int e = 0; e < 4; ++e) above |= x[nt][e] > m[nt][e & 1] + room;
       if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -507,7 +522,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float now = fmaxf(m[nt][i], top);
+            const float now = fmaxf(m[nt][i], top - (room - 8.f));
             const float f = exp2_fast(m[nt][i] - now);
             m[nt][i] = now;
             l[nt][i] *= f;
@@ -518,19 +533,6 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
             }
           }
       }
-      if (!(sc.y <= vref)) {                         // the same for the value scales
-        const float old = vref;
-        vref = __uint_as_float((__float_as_uint(sc.y) & 0x7F800000u) + 0x00800000u);
-        vref_inv = 1.f / vref;
-        const float f = old * vref_inv;
-#pragma unroll
-        for (int u = 0; u < KS; ++u)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[u][nt][e] *= f;
-      }
-      const float vs = sc.y * vref_inv;
       uint32_t pf[NT][2], rest[NT][2];     // P, and for fp16 outputs what its rounding left
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float a = e[2 * i] * vs, z = e[2 * i + 1] * vs;
+          const float a = e[2 * i] * sc.y, z = e[2 * i + 1] * sc.y;
           const uint32_t r = narrow2<false>(a, z);
           pf[nt][i] = transpose8x8(r);
           if constexpr (F16) {
@@ -585,8 +587,8 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-              seen[nt][i] = transpose8x8((tok0 + 8 * i <= limit[nt][0] ? 0x3C00u : 0u) |
-                                         (tok0 + 8 * i <= limit[nt][1] ? 0x3C000000u : 0u));
+              seen[nt][i] = transpose8x8((hidden(nt, 0, i) ? 0u : 0x3C00u) |
+                                         (hidden(nt, 1, i) ? 0u : 0x3C000000u));
           uint32_t keep[4][C::kVBytes / 4];
 #pragma unroll
           for (int tok = 0; tok < 4; ++tok)
@@ -658,9 +660,9 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
       for (int nt = 0; nt < NT; ++nt) {
         const int r = 8 * nt + 2 * t;
         *reinterpret_cast<float2*>(mine + r * kRow + d) =
-            make_float2(o[i][nt][0] * vref, o[i][nt][2] * vref);
+            make_float2(o[i][nt][0], o[i][nt][2]);
         *reinterpret_cast<float2*>(mine + (r + 1) * kRow + d) =
-            make_float2(o[i][nt][1] * vref, o[i][nt][3] * vref);
+            make_float2(o[i][nt][1], o[i][nt][3]);
       }
     }
     if (g == 0) {

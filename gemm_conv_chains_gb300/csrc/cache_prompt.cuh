@@ -17,10 +17,10 @@
 // other (P V of this key tile, then Q K^T of the next; MMAs of one thread run in issue order,
 // so S of the next tile follows the products that read the P it covers).
 //
-// Precision as in cache_attention.cuh.  The scales of the value pages enter the exponent
-// (log2, relative to a running power of two) and are divided out of the row sum, so that a
-// probability costs one multiply-add, one exponential and one addition.  The row maximum only
-// moves when it is exceeded by 2^8, and O, in TMEM, is rescaled only then.
+// Precision as in cache_attention.cuh.  The scales of the value pages enter the exponent (as log2)
+// and are divided out of the row sum, so that a probability costs one multiply-add, one exponential
+// and one addition.  A row's reference, of z + log2 scale, only moves when a product would be above
+// 2^15, and O, in TMEM, is rescaled only then.
 //
 // Measured: prompts of 451 to 2048 tokens behind 1192 to 4096 cached ones (4 sequences, 32 query
 // heads on 8 of 128 channels): 236 us, 1.04 PFLOP/s, 0.54 of the library's dense bf16 rate.  The
@@ -151,9 +151,15 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-// A page's value scale relative to the reference (log2), not below 2^-60: a scale of zero stands
-// for that (its codes' share vanishes, the row's sum does not); a NaN stays one.
-__device__ __forceinline__ float low_of(float lv) { return lv < -60.f ? -60.f : lv; }
+// A page's value scale as the exponent that it adds.  A scale of zero stands for 2^-96: that page
+// takes its weight in the row sum, and what comes out of it is less than any other's by so much that
+// fp16 has nothing of it; a row that sees no other pages is told by its sum (kNoValues).  A NaN
+// stays one.
+constexpr float kNoValues = 5.0706024e30f;          // 2^102: 2^-64, the least scale of an append, over 2^23 tokens
+__device__ __forceinline__ float exponent_of(float scale) {
+  const float lv = log2f(scale);
+  return lv < -96.f ? -96.f : lv;
+}
 
 // What a CTA works on: up to 256 query rows of one sequence and kv head.
 struct PromptUnit {
@@ -385,7 +391,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       const int low_limit = u.start + (u.row0 + 128 * t) / p.group;
       const float slope = MODS && p.slopes != nullptr && valid ? p.slopes[head] : 0.f;
       const float cap2 = MODS && p.softcap > 0.f ? 2.f * 1.4426950408889634f / p.softcap : 0.f;
-      float m = -1e30f, l = 0.f, lvref = -1e30f;
+      float m = -1e30f, l = 0.f;                   // m: the reference of z + log2 value scale
       bool ok = true;
 
       for (int i = 0; i < u.tiles && ok; ++i) {
@@ -410,9 +416,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
           }
           return z;
         };
-        // ---- the tile's largest score; capped, biased or masked scores go back to TMEM ----
+        // ---- the tile's largest z + log2 value scale; capped, biased or masked scores go back to TMEM ----
         uint32_t r[32];
-        float top = -INFINITY, lvtop = -INFINITY;
+        float top = -INFINITY;
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           tmem_load32(tm + s_col + 32 * q, r);
@@ -421,38 +427,34 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
           for (int g = 0; g < 2; ++g) {
             const float2 s2 = sc[2 * q + g];
             const float f = fac * s2.x;
-            lvtop = fmaxf(lvtop, s2.y);
             uint32_t* x = &r[16 * g];
+            float most = -INFINITY;                  // of the granule's tokens that the row sees
             if constexpr (SCORES) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const int tok = tok0 + 32 * q + 16 * g + e;
                 const float z = tok > limit ? -INFINITY : score(x[e], f, tok);
                 x[e] = __float_as_uint(z);
-                top = fmaxf(top, z);
+                most = fmaxf(most, z);
               }
             } else {
               float a = __uint_as_float(x[0]);
 #pragma unroll
               for (int e = 1; e + 1 < 16; e += 2)
                 a = max3(a, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-              top = fmaxf(top, fmaxf(a, __uint_as_float(x[15])) * f);
+              most = fmaxf(a, __uint_as_float(x[15])) * f;
             }
+            top = fmaxf(top, most + s2.y);
           }
           if constexpr (SCORES) tmem_st32(tm + s_col + 32 * q, r);
         }
         if constexpr (SCORES) tmem_wait_st();
-        // ---- the references, and what O has to be scaled by for them ----
+        // ---- the reference, and what O and the row's sum have to be scaled by for it ----
         float f = 1.f;
-        if (top > m + 8.f) {
-          f = ex2(m - top);
-          m = top;
+        if (top > m + 15.f) {
+          f = ex2(m - (top - 7.f));
+          m = top - 7.f;
           l *= f;
-        }
-        if (lvtop > lvref) {
-          const float now = floorf(lvtop) + 1.f;
-          f *= ex2(lvref - now);
-          lvref = now;
         }
         if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
@@ -474,8 +476,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
           for (int g = 0; g < 2; ++g) {
             const float2 s2 = sc[2 * q + g];
             const float fg = SCORES ? 1.f : fac * s2.x;
-            const float lv = low_of(s2.y - lvref);
-            const float back = ex2(-lv), c = lv - m;
+            const float back = ex2(-s2.y), c = s2.y - m;
             const float2 f2 = make_float2(fg, fg), c2 = make_float2(c, c);
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -492,45 +493,39 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
           tmem_store16(tm + s_col + 16 * q, pk);
         }
         };
-        // Inner tiles of a plain softmax take one pass with the references as they are: P and the
-        // sums are formed while the columns arrive, and only if some exponent turns out above 8
-        // (or a value scale above its reference) is the tile done again in two passes.
+        // Inner tiles of a plain softmax take one pass with the reference as it is: P and the sums are
+        // formed while the columns arrive, and only if some exponent turns out above 15 is the tile
+        // done again in two passes.
         bool done = false;
-        if (!MODS && !edge) {
-          float lvtop = sc[0].y;
+        if (!MODS && !edge && __all_sync(0xffffffffu, m > -1e29f)) {
+          uint32_t r[2][16], pk[4][16];
+          float high = -INFINITY, more = 0.f;
+          tmem_ld16(tm + s_col, r[0]);
 #pragma unroll
-          for (int g = 1; g < kGranules; ++g) lvtop = fmaxf(lvtop, sc[g].y);
-          if (lvtop <= lvref) {
-            uint32_t r[2][16], pk[4][16];
-            float high = -INFINITY, more = 0.f;
-            tmem_ld16(tm + s_col, r[0]);
+          for (int g = 0; g < kGranules; ++g) {
+            tmem_wait_ld(r[g & 1]);
+            if (g + 1 < kGranules) tmem_ld16(tm + s_col + 16 * (g + 1), r[(g + 1) & 1]);
+            const float2 s2 = sc[g];
+            const float fg = fac * s2.x, back = ex2(-s2.y), c = s2.y - m;
+            const float2 f2 = make_float2(fg, fg), c2 = make_float2(c, c);
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int g = 0; g < kGranules; ++g) {
-              tmem_wait_ld(r[g & 1]);
-              if (g + 1 < kGranules) tmem_ld16(tm + s_col + 16 * (g + 1), r[(g + 1) & 1]);
-              const float2 s2 = sc[g];
-              const float fg = fac * s2.x, lv = low_of(s2.y - lvref);
-              const float back = ex2(-lv), c = lv - m;
-              const float2 f2 = make_float2(fg, fg), c2 = make_float2(c, c);
-              float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const uint32_t* x = &r[g & 1][e];
-                float2 y = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), f2, c2);
-                high = max3(high, y.x, y.y);
-                y.x = ex2(y.x);
-                y.y = ex2(y.y);
-                sum = add2(sum, y);
-                pk[g / 2][8 * (g & 1) + e / 2] = narrow2<false>(y.x, y.y);
-              }
-              more = fmaf(sum.x + sum.y, back, more);
+            for (int e = 0; e < 16; e += 2) {
+              const uint32_t* x = &r[g & 1][e];
+              float2 y = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), f2, c2);
+              high = max3(high, y.x, y.y);
+              y.x = ex2(y.x);
+              y.y = ex2(y.y);
+              sum = add2(sum, y);
+              pk[g / 2][8 * (g & 1) + e / 2] = narrow2<false>(y.x, y.y);
             }
-            if (!__any_sync(0xffffffffu, high > 8.f)) {
-              l += more;
+            more = fmaf(sum.x + sum.y, back, more);
+          }
+          if (!__any_sync(0xffffffffu, high > 15.f)) {
+            l += more;
 #pragma unroll
-              for (int q = 0; q < 4; ++q) tmem_store16(tm + s_col + 16 * q, pk[q]);
-              done = true;
-            }
+            for (int q = 0; q < 4; ++q) tmem_store16(tm + s_col + 16 * q, pk[q]);
+            done = true;
           }
         }
         if (!done) {
@@ -546,7 +541,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       // ---- the output row ----
       if (ok && wait(&bars->ofull[t], 0, PS_OFULL)) {
         tc_fence_after_sync();
-        const float inv = l == 0.f ? 0.f : ex2(lvref) / l;
+        const float inv = l == 0.f || l > kNoValues ? 0.f : 1.f / l;
         const int tq_out = valid ? tq : 0;
         uint16_t* dst = p.out + ((u.s.row + static_cast<int64_t>(tq_out)) * p.q_heads + head) * D;
         const bool nans = bars->nan_any != 0u;
@@ -565,7 +560,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
               float o[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                o[k] = l == 0.f ? 0.f : __uint_as_float(r[e + k]) * inv;
+                o[k] = inv == 0.f ? 0.f : __uint_as_float(r[e + k]) * inv;
                 if ((bad >> (e + k)) & 1u) o[k] = __uint_as_float(0x7FC00000u);
               }
               *reinterpret_cast<uint4*>(dst + 32 * q + e) = p.is_bf16 ? narrow8<true>(o) : narrow8<false>(o);
@@ -602,7 +597,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       if (i >= 2) ok = wait(&bars->kempty[slot], ((i >> 1) - 1) & 1, PS_KEMPTY);
       if (!ok) break;
       prod.store(raw, base + L::kK + slot * L::kTile);
-      if (prod.tid < kGranules) scales[(i & 3) * kGranules + prod.tid] = make_float2(s2.x, log2f(s2.y));
+      if (prod.tid < kGranules) scales[(i & 3) * kGranules + prod.tid] = make_float2(s2.x, exponent_of(s2.y));
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->kfull[slot]));

@@ -250,7 +250,10 @@ b2b_status b2b_rotary(b2b_dtype dt, int64_t T, int32_t H, int32_t D, int32_t rot
                       void* out, int64_t ldo, void* stream);
 
 /* A paged cache and the sequences of one call.  Codes are e4m3 (no infinities, one NaN); the
- * value of a code is code * scale, one fp32 scale per page and kv head, >= 0.  Position j of sequence
+ * value of a code is code * scale, one fp32 scale per page and kv head, >= 0.  (The attention's stated
+ * precision holds where the value scales of a sequence and head are at most 2^96 and, those above 0,
+ * within a factor of 2^100 of one another, and below 2^13 if others are 0.  An append makes none
+ * below 2^-64, and of fp16 values none above 2^8.)  Position j of sequence
  * s lies in slot j % page_size of page page_table[s][j / page_size].  The call's new tokens are
  * rows [starts[s], starts[s + 1]) of its inputs, positions lens[s] - n .. lens[s] - 1.  Page
  * numbers of positions at or past lens[s] are not read.  Every array is a device array. */
