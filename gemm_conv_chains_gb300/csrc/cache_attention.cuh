@@ -490,11 +490,13 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
         if constexpr (MODS) return away + static_cast<float>(8 * k) + behind[nt][i] > 0.f;
         else return tok0 + 8 * k > limit[nt][i];
       };
+      // (a value scale that is no number enters here, so that rows that do not reach its page stay clear)
+      const float bad = sc.y - sc.y, vs = bad == 0.f ? sc.y : 0.f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float z = (x[nt][e] + x2[nt][e]) * (qfactor[nt][e & 1] * sc.x);
+          float z = fmaf(x[nt][e] + x2[nt][e], qfactor[nt][e & 1] * sc.x, bad);
           if constexpr (MODS) {
             if (p.softcap > 0.f)                     // cap tanh(z / cap); tanh y = 1 - 2 / (e^2y + 1)
               z = p.softcap - 2.f * p.softcap *
@@ -507,7 +509,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
       // A row's reference m is for e = 2^(z - m) times the page's value scale, which is P: it moves
       // when one would be above 2^15, inside fp16, and then to where that one is 2^7, so that most
       // strips neither reduce nor rescale.  e itself, which the row sum takes, stays below 2^96.
-      const float room = fminf(15.f - log2_fast(sc.y), 96.f);
+      const float room = fminf(15.f - log2_fast(vs), 96.f);
       bool above = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float a = e[2 * i] * sc.y, z = e[2 * i + 1] * sc.y;
+          const float a = e[2 * i] * vs, z = e[2 * i + 1] * vs;
           const uint32_t r = narrow2<false>(a, z);
           pf[nt][i] = transpose8x8(r);
           if constexpr (F16) {

@@ -476,7 +476,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
           for (int g = 0; g < 2; ++g) {
             const float2 s2 = sc[2 * q + g];
             const float fg = SCORES ? 1.f : fac * s2.x;
-            const float back = ex2(-s2.y), c = s2.y - m;
+            // (a page that the row does not reach may have any scale, a NaN too)
+            const bool past = SCORES && tok0 + 32 * q + 16 * g > limit;
+            const float back = past ? 0.f : ex2(-s2.y), c = past ? 0.f : s2.y - m;
             const float2 f2 = make_float2(fg, fg), c2 = make_float2(c, c);
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll

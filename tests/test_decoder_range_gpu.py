@@ -149,3 +149,40 @@ def test_value_scales_of_zero_and_of_nothing_appended(older, new, heads, group, 
                 c.vs[c.table[b, j].long()] = s
     out = ops.cache_attention(q.cuda(), *c.args())
     _check(out, c, q, D ** -0.5)
+
+
+# ------------------------------------------------------------------------------------
+# pages past a row's reach
+# ------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("older,new,heads,group,D,page", [
+    ([30], [8], 2, 1, 64, 16), ([14, 100], [5, 14], 1, 4, 128, 16), ([60], [8], 1, 2, 256, 16),
+    ([0, 50] * 4, [40, 40] * 4, 8, 2, 128, 16), ([10, 0], [150, 200], 8, 4, 64, 32),
+    ([100, 250], [64, 70], 8, 3, 96, 16)])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_a_page_that_a_row_does_not_reach_leaves_it_alone(older, new, heads, group, D, page, softcap):
+    """The last page of each sequence: scales that are NaN or infinite, then a page number outside the
+    pool.  Rows before it keep their bits, rows that see it do not stay finite."""
+    c = ref.Cache(older, new, heads, D, page, seed=8)
+    q = _randn(D, c.T, heads * group, D).half()
+    want = ops.cache_attention(q.cuda(), *c.args(), softcap=softcap).cpu()
+    pos = torch.cat([torch.arange(a, a + n) for a, n in zip(older, new)])
+    last = torch.cat([torch.full((n,), (a + n - 1) // page * page) for a, n in zip(older, new)])
+    before = pos < last
+    assert before.any() and not before.all()
+    pids = [int(c.table[b, (n - 1) // page]) for b, n in enumerate(c.lens)]
+    for name, value in (("vs", math.nan), ("vs", math.inf), ("ks", math.nan), ("ks", math.inf)):
+        keep = getattr(c, name).clone()
+        getattr(c, name)[pids] = value
+        got = ops.cache_attention(q.cuda(), *c.args(), softcap=softcap).cpu()
+        setattr(c, name, keep)
+        assert torch.equal(got[before], want[before]), (name, value)
+        if name == "vs":
+            assert not got[~before].isfinite().all(-1).any()
+    args = c.args()
+    for b, n in enumerate(c.lens):
+        args[4][b, (n - 1) // page] = c.pages + 5
+    got = ops.cache_attention(q.cuda(), *args, softcap=softcap).cpu()
+    st, info = ops.get_cache_error()
+    assert st == 2 and info[2] == 2
+    assert torch.equal(got[before], want[before])
