@@ -48,24 +48,12 @@ constexpr int kAttendWarps = 4;
 constexpr int kTileTokens = 64;        // tokens per numbered tile: one strip per warp
 constexpr int kStrip = 16;
 constexpr float kNoMax = -1e30f;       // "no key seen": finite, so that no inf - inf arises
-constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float log2_fast(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float rcp_fast(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                              uint32_t b1) {
   asm(
@@ -498,9 +486,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
         for (int e = 0; e < 4; ++e) {
           float z = fmaf(x[nt][e] + x2[nt][e], qfactor[nt][e & 1] * sc.x, bad);
           if constexpr (MODS) {
-            if (p.softcap > 0.f)                     // cap tanh(z / cap); tanh y = 1 - 2 / (e^2y + 1)
-              z = p.softcap - 2.f * p.softcap *
-                      rcp_fast(exp2_fast(z * (2.f * kLog2e / p.softcap)) + 1.f);
+            if (p.softcap > 0.f) z = capped(z, p.softcap, p.inv_softcap);
             z = fmaf(slope[nt][e & 1], away + static_cast<float>(8 * (e >> 1)) + behind[nt][e & 1], z) * kLog2e;
           }
           if (edge && hidden(nt, e & 1, e >> 1)) z = -INFINITY;

@@ -113,12 +113,6 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
                : "memory");
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 template <int N>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -381,7 +375,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
           }
           st_shared16(dst + (i / 8) * 16384 + (((i % 8) ^ (threadIdx.x & 7)) << 4), w.x, w.y, w.z, w.w);
         }
-        fac = unit * fabsf(p.scale) * (MODS ? 1.f : 1.4426950408889634f);
+        fac = unit * fabsf(p.scale) * (MODS ? 1.f : kLog2e);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -390,7 +384,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       const int limit = valid ? u.start + tq : 0x7FFFFFFF;
       const int low_limit = u.start + (u.row0 + 128 * t) / p.group;
       const float slope = MODS && p.slopes != nullptr && valid ? p.slopes[head] : 0.f;
-      const float cap2 = MODS && p.softcap > 0.f ? 2.f * 1.4426950408889634f / p.softcap : 0.f;
       float m = -1e30f, l = 0.f;                   // m: the reference of z + log2 value scale
       bool ok = true;
 
@@ -407,12 +400,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
         auto score = [&](uint32_t raw, float f, int tok) -> float {
           float z = __uint_as_float(raw) * f;
           if (MODS) {
-            if (cap2 > 0.f) {                      // cap tanh(z / cap)
-              float r;
-              asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(z * cap2) + 1.f));
-              z = p.softcap - 2.f * p.softcap * r;
-            }
-            z = fmaf(slope, static_cast<float>(tok - limit), z) * 1.4426950408889634f;
+            if (p.softcap > 0.f) z = capped(z, p.softcap, p.inv_softcap);
+            z = fmaf(slope, static_cast<float>(tok - limit), z) * kLog2e;
           }
           return z;
         };
@@ -452,7 +441,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
         // ---- the reference, and what O and the row's sum have to be scaled by for it ----
         float f = 1.f;
         if (top > m + 15.f) {
-          f = ex2(m - (top - 7.f));
+          f = exp2_fast(m - (top - 7.f));
           m = top - 7.f;
           l *= f;
         }
@@ -478,15 +467,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
             const float fg = SCORES ? 1.f : fac * s2.x;
             // (a page that the row does not reach may have any scale, a NaN too)
             const bool past = SCORES && tok0 + 32 * q + 16 * g > limit;
-            const float back = past ? 0.f : ex2(-s2.y), c = past ? 0.f : s2.y - m;
+            const float back = past ? 0.f : exp2_fast(-s2.y), c = past ? 0.f : s2.y - m;
             const float2 f2 = make_float2(fg, fg), c2 = make_float2(c, c);
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
               float2 y = fma2(make_float2(__uint_as_float(r[16 * g + e]),
                                           __uint_as_float(r[16 * g + e + 1])), f2, c2);
-              y.x = ex2(y.x);
-              y.y = ex2(y.y);
+              y.x = exp2_fast(y.x);
+              y.y = exp2_fast(y.y);
               sum = add2(sum, y);
               pk[8 * g + e / 2] = narrow2<false>(y.x, y.y);
             }
@@ -508,7 +497,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
             tmem_wait_ld(r[g & 1]);
             if (g + 1 < kGranules) tmem_ld16(tm + s_col + 16 * (g + 1), r[(g + 1) & 1]);
             const float2 s2 = sc[g];
-            const float fg = fac * s2.x, back = ex2(-s2.y), c = s2.y - m;
+            const float fg = fac * s2.x, back = exp2_fast(-s2.y), c = s2.y - m;
             const float2 f2 = make_float2(fg, fg), c2 = make_float2(c, c);
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -516,8 +505,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
               const uint32_t* x = &r[g & 1][e];
               float2 y = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), f2, c2);
               high = max3(high, y.x, y.y);
-              y.x = ex2(y.x);
-              y.y = ex2(y.y);
+              y.x = exp2_fast(y.x);
+              y.y = exp2_fast(y.y);
               sum = add2(sum, y);
               pk[g / 2][8 * (g & 1) + e / 2] = narrow2<false>(y.x, y.y);
             }

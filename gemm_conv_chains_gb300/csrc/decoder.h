@@ -66,6 +66,7 @@ struct AttendParams {
   int64_t ldq;
   int32_t q_heads, group, is_bf16;
   float scale, softcap;       // softcap 0: none
+  float inv_softcap;
   int32_t grid, min_tiles, whole;
   float* part;                // split workspace: see cache_attention.cuh
   uint32_t* meta;             // [0]: tiles per run, [1 + b]: sequence b's first tile

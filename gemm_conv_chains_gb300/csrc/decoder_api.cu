@@ -336,7 +336,9 @@ b2b_status b2b_cache_attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, 
   p.group = q_heads / cache->heads;
   p.is_bf16 = dt == B2B_BF16;
   p.scale = scale;
-  p.softcap = softcap;
+  // a cap below 2^-100 is nothing beside any other score's rounding, and its inverse stays finite
+  p.softcap = softcap > 0.f && softcap < 7.8886091e-31f ? 7.8886091e-31f : softcap;
+  p.inv_softcap = softcap > 0.f ? 1.f / p.softcap : 0.f;
   p.grid = sc.grid;
   p.min_tiles = kMinTiles;
   p.whole = sc.whole;

@@ -205,6 +205,29 @@ __device__ __forceinline__ void store_turned(uint16_t* row, const RawUnit& r, co
   if (a.pair) *reinterpret_cast<uint4*>(row + a.d + rot / 2) = narrow8<BF16>(hi);
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// cap tanh(z / cap).  tanh y = 1 - 2 / (e^2y + 1) cancels for small y, by 2^-23 of the cap whatever z
+// is; below 1/4 it is y (1 - y^2 / 3 + 2 y^4 / 15 - 17 y^6 / 315), the start of its series, whose rest
+// is below 2^-21 of y there.
+__device__ __forceinline__ float capped(float z, float cap, float inv_cap) {
+  const float y = z * inv_cap, yy = y * y;
+  const float near = z * fmaf(yy, fmaf(yy, fmaf(yy, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+  const float far = cap - 2.f * cap * rcp_fast(exp2_fast(y * (2.f * kLog2e)) + 1.f);
+  return fabsf(y) < 0.25f ? near : far;
+}
+
 // Two fp32 values to e4m3, nearest even, saturating; a NaN stays one.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;

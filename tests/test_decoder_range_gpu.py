@@ -186,3 +186,21 @@ def test_a_page_that_a_row_does_not_reach_leaves_it_alone(older, new, heads, gro
     st, info = ops.get_cache_error()
     assert st == 2 and info[2] == 2
     assert torch.equal(got[before], want[before])
+
+
+# ------------------------------------------------------------------------------------
+# caps far above the scores, and far below
+# ------------------------------------------------------------------------------------
+
+CAPPED = [([700], [1], 2, 4, 64, 16), ([300, 20], [5, 3], 1, 4, 128, 32), ([100], [6], 1, 2, 256, 64),
+          ([0, 200], [150, 70], 8, 4, 128, 16), ([30] * 6, [60] * 6, 8, 2, 64, 32)]
+
+
+@pytest.mark.parametrize("softcap", [1e-40, 1e-3, 0.5, 50.0, 1e3, 1e4, 1e6, 1e30])
+@pytest.mark.parametrize("older,new,heads,group,D,page", CAPPED)
+def test_caps_from_tiny_to_huge(softcap, older, new, heads, group, D, page):
+    c = ref.Cache(older, new, heads, D, page, seed=4)
+    q = (_randn(D + 1, c.T, heads * group, D) * 6).half()
+    q[0] = 0                                          # scores of zero
+    out = ops.cache_attention(q.cuda(), *c.args(), softcap=softcap)
+    _check(out, c, q, D ** -0.5, softcap)
