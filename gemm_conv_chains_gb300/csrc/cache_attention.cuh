@@ -25,7 +25,8 @@
 // second small kernel joins.  A CTA's four warps take the 16-token strips in turn, each with a
 // running maximum and sum of its own, joined in shared memory.
 //
-// Precision: codes, and with a per-row power of two also bf16 queries, are exact in fp16; the
+// Precision: codes are exact in fp16, and so are bf16 queries down to 2^-31 of the largest channel of
+// their row, which a power of two puts near the top of fp16 (smaller channels to 2^-39 of it); the
 // products sum in fp32; the softmax is fp32.  P is rounded to fp16: 11 bits, much finer than a
 // bf16 output.  For fp16 outputs, whose own rounding is no coarser, the rest that this rounding
 // leaves is multiplied as well (one token over 250001 cached, error against 64 bits 3.0e-4
@@ -88,17 +89,6 @@ __device__ __forceinline__ void load_words(const uint8_t* src, uint32_t* w) {
   } else {
     w[0] = *reinterpret_cast<const uint32_t*>(src);
   }
-}
-
-// A query row's fp16 form: bf16 rows are divided by the power of two of their largest
-// magnitude (put back into the scores in fp32), fp16 rows are taken as they are.
-__device__ __forceinline__ float row_unit_of(float amax, bool bf16, float& inv) {
-  inv = 1.f;
-  if (!bf16) return 1.f;
-  uint32_t e = (__float_as_uint(amax) >> 23) & 0xFFu;
-  if (e == 0u || e >= 253u) return 1.f;          // zero, subnormal, huge, infinite or NaN
-  inv = __uint_as_float((254u - e) << 23);
-  return __uint_as_float(e << 23);
 }
 
 template <int D_, int NT>
@@ -377,7 +367,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       float inv;
-      const float unit = row_unit_of(amax, !F16, inv);
+      const float unit = row_unit<!F16>(amax, inv);
       // (q_frags and row_units are free: the last piece ended in a block barrier)
       if (t == 0 && (NT == 1 ? warp == 0 : warp < NT)) row_units[8 * q_nt + g] = unit;
 #pragma unroll

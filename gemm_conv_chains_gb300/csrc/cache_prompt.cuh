@@ -349,11 +349,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
 #pragma unroll
             for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
           }
-          const uint32_t e = (__float_as_uint(amax) >> 23) & 0xFFu;
-          if (e != 0u && e < 253u) {               // as in the split kernel
-            inv = __uint_as_float((254u - e) << 23);
-            unit = __uint_as_float(e << 23);
-          }
+          unit = row_unit<true>(amax, inv);
         }
         if (p.scale < 0.f) inv = -inv;             // the maximum below wants positive factors
         const uint32_t dst = base + L::kQ + t * L::kTile + (threadIdx.x & 127) * 128;

@@ -205,6 +205,18 @@ __device__ __forceinline__ void store_turned(uint16_t* row, const RawUnit& r, co
   if (a.pair) *reinterpret_cast<uint4*>(row + a.d + rot / 2) = narrow8<BF16>(hi);
 }
 
+// A query row's fp16 form: fp16 rows are taken as they are; bf16 rows are multiplied by the power of
+// two `inv` (at most 2^126) that brings their largest magnitude to 2^14 .. 2^15, and its inverse, which
+// is returned, is put back into the scores in fp32.
+template <bool BF16>
+__device__ __forceinline__ float row_unit(float amax, float& inv) {
+  inv = 1.f;
+  if (!BF16) return 1.f;
+  const uint32_t e = (__float_as_uint(amax) >> 23) & 0xFFu, u = e > 15u ? e - 14u : 1u;
+  inv = __uint_as_float((254u - u) << 23);
+  return __uint_as_float(u << 23);
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_fast(float x) {

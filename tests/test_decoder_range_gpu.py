@@ -204,3 +204,31 @@ def test_caps_from_tiny_to_huge(softcap, older, new, heads, group, D, page):
     q[0] = 0                                          # scores of zero
     out = ops.cache_attention(q.cuda(), *c.args(), softcap=softcap)
     _check(out, c, q, D ** -0.5, softcap)
+
+
+# ------------------------------------------------------------------------------------
+# query rows whose channels lie far apart
+# ------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("spread", [12, 18, 22, 27])
+@pytest.mark.parametrize("older,new,heads,group,D,page", CAPPED)
+def test_bf16_queries_with_channels_far_apart(spread, older, new, heads, group, D, page):
+    """One channel is 2^spread times the others, and the keys have next to nothing in it."""
+    c = ref.Cache(older, new, heads, D, page, seed=5)
+    c.ks *= 2.0 ** (spread - 3)
+    c.k[..., 3] = 0.0
+    q = _randn(D + 2, c.T, heads * group, D) * 2.0 ** -spread
+    q[..., 3] = _randn(D, c.T, heads * group).clamp(-2, 2)
+    q = q.bfloat16()
+    out = ops.cache_attention(q.cuda(), *c.args(), scale=8 * D ** -0.5)
+    _check(out, c, q, 8 * D ** -0.5)
+
+
+@pytest.mark.parametrize("exponent", [-130, -120, -60, 60, 112, 122])
+@pytest.mark.parametrize("older,new,heads,group,D,page", [CAPPED[1], CAPPED[3]])
+def test_bf16_queries_of_any_size(exponent, older, new, heads, group, D, page):
+    c = ref.Cache(older, new, heads, D, page, seed=6)
+    q = (_randn(D + 3, c.T, heads * group, D).double() * 2.0 ** exponent).bfloat16()
+    scale = 2.0 ** (-exponent if exponent > -120 else 119)
+    out = ops.cache_attention(q.cuda(), *c.args(), scale=scale * D ** -0.5)
+    _check(out, c, q, float(torch.tensor(scale * D ** -0.5)), 0.0)
