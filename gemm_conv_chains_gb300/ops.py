@@ -2,7 +2,8 @@
 decoder-block operators, which run once per token, by the extension of csrc/binding.cpp).
 
 Every function takes CUDA tensors, checks dtypes, shapes and contiguity (the C ABI sees
-only pointers and sizes), allocates the output with torch when none is given, and calls
+only pointers and sizes), allocates the output with torch when none is given (from the memory of
+the stream that the call runs on, as torch does under torch.cuda.stream), and calls
 the entry point of the same name on the current torch stream.  All arithmetic runs in the
 library's kernels; there is no other code path, and a missing or unloadable library
 raises instead of falling back.
@@ -185,6 +186,22 @@ def _stream(stream, device=None) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """torch.empty from the memory of the stream that will write it: a block that the current stream
+    has freed may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    device = torch.device(device)
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else \
+            torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _raise(status: int, what: str) -> None:
     if status != 0:
         raise B2BError(status, what)
@@ -207,7 +224,7 @@ def b2b_gemm(A, W0, b0, W1, b1, epi0="relu", epi1="relu", out=None, stream=None)
     if b1 is not None:
         _check_tensor(b1, "b1", dt, (N1,))
     if out is None:
-        out = torch.empty((M, N1), dtype=dt, device=A.device)
+        out = _empty((M, N1), dt, A.device, stream)
     _check_tensor(out, "out", dt, (M, N1))
     dev = _common_device(A=A, W0=W0, b0=b0, W1=W1, b1=b1, out=out)
     with torch.cuda.device(dev):
@@ -236,7 +253,7 @@ def b2b_gemm3(A, W0, b0, W1, b1, W2, b2, epi0="relu", epi1="relu", epi2="relu", 
         if b is not None:
             _check_tensor(b, name, dt, (n,))
     if out is None:
-        out = torch.empty((M, N2), dtype=dt, device=A.device)
+        out = _empty((M, N2), dt, A.device, stream)
     _check_tensor(out, "out", dt, (M, N2))
     dev = _common_device(A=A, W0=W0, b0=b0, W1=W1, b1=b1, W2=W2, b2=b2, out=out)
     with torch.cuda.device(dev):
@@ -273,7 +290,7 @@ def _b2b_conv(x, W0, b0, W1, b1, pad, stride, epi0, epi1, out, stream):
         _check_tensor(b1, "b1", dt, (C1,))
     Ho, Wo = _conv_out(H, pad, R, stride), _conv_out(W, pad, S, stride)
     if out is None:
-        out = torch.empty((N, Ho, Wo, C1), dtype=dt, device=x.device)
+        out = _empty((N, Ho, Wo, C1), dt, x.device, stream)
     _check_tensor(out, "out", dt, (N, Ho, Wo, C1))
     dev = _common_device(x=x, W0=W0, b0=b0, W1=W1, b1=b1, out=out)
     with torch.cuda.device(dev):
@@ -301,7 +318,7 @@ def conv_relu_maxpool(x, Wt, b, out=None, stream=None):
     if b is not None:
         _check_tensor(b, "b", dt, (Cout,))
     if out is None:
-        out = torch.empty((N, H // 2, W // 2, Cout), dtype=dt, device=x.device)
+        out = _empty((N, H // 2, W // 2, Cout), dt, x.device, stream)
     _check_tensor(out, "out", dt, (N, H // 2, W // 2, Cout))
     dev = _common_device(x=x, Wt=Wt, b=b, out=out)
     with torch.cuda.device(dev):
@@ -324,7 +341,7 @@ def gemm_bias_act(A, W, b, epi="relu", out=None, stream=None):
     if b is not None:
         _check_tensor(b, "b", dt, (N,))
     if out is None:
-        out = torch.empty((M, N), dtype=dt, device=A.device)
+        out = _empty((M, N), dt, A.device, stream)
     _check_tensor(out, "out", dt, (M, N))
     dev = _common_device(A=A, W=W, b=b, out=out)
     with torch.cuda.device(dev):
@@ -353,7 +370,7 @@ def _conv_single(x, Wt, b, pad, stride, epi, out, stream):
         _check_tensor(b, "b", dt, (Co,))
     Ho, Wo = _conv_out(H, pad, R, stride), _conv_out(W, pad, S, stride)
     if out is None:
-        out = torch.empty((N, Ho, Wo, Co), dtype=dt, device=x.device)
+        out = _empty((N, Ho, Wo, Co), dt, x.device, stream)
     _check_tensor(out, "out", dt, (N, Ho, Wo, Co))
     dev = _common_device(x=x, Wt=Wt, b=b, out=out)
     with torch.cuda.device(dev):
@@ -383,8 +400,8 @@ def fold_batchnorm(W, b, gamma, beta, mean, var, eps=1e-5, out_inner=False, W_ou
         _check_tensor(b, "b", dt, (Co,))
     for name, v in (("gamma", gamma), ("beta", beta), ("mean", mean), ("var", var)):
         _check_tensor(v, name, torch.float32, (Co,))
-    W_out = torch.empty_like(W) if W_out is None else W_out
-    b_out = torch.empty((Co,), dtype=dt, device=W.device) if b_out is None else b_out
+    W_out = _empty(W.shape, dt, W.device, stream) if W_out is None else W_out
+    b_out = _empty((Co,), dt, W.device, stream) if b_out is None else b_out
     _check_tensor(W_out, "W_out", dt, tuple(W.shape))
     _check_tensor(b_out, "b_out", dt, (Co,))
     dev = _common_device(W=W, b=b, gamma=gamma, beta=beta, mean=mean, var=var, W_out=W_out,
@@ -403,7 +420,7 @@ def maxpool2x2_nhwc(x, out=None, stream=None):
     N, H, W, C = x.shape
     _check_tensor(x, "x", dt, (N, H, W, C))
     if out is None:
-        out = torch.empty((N, H // 2, W // 2, C), dtype=dt, device=x.device)
+        out = _empty((N, H // 2, W // 2, C), dt, x.device, stream)
     _check_tensor(out, "out", dt, (N, H // 2, W // 2, C))
     dev = _common_device(x=x, out=out)
     with torch.cuda.device(dev):
@@ -438,7 +455,7 @@ def rotary_table(positions, rot, base=10000.0, scaling="plain", factor=1.0, orig
     device = torch.device(device)
     if device.type != "cuda":
         raise ValueError(f"device must be a CUDA device, got {device}")
-    out = torch.empty((positions, rot // 2, 2), dtype=torch.float32, device=device)
+    out = _empty((positions, rot // 2, 2), torch.float32, device, stream)
     with torch.cuda.device(out.device):
         _raise(lib().b2b_rotary_table(positions, rot, base, SCALINGS[scaling], factor, original,
                                       low, high, gain, _ptr(out), _stream(stream, out.device)),
