@@ -466,15 +466,47 @@ def rotary_table(positions, rot, base=10000.0, scaling="plain", factor=1.0, orig
 # What the calls below allocate (outputs, workspace) comes from the memory of the stream they run
 # on; the checks and their messages are in csrc/binding.cpp.
 
-def rotary(x, table, positions, layout="half", inverse=False, out=None, stream=None):
-    """x [T, H, D] (token stride free) with the first rot channels of each head turned by the
-    angles of positions [T] (int32), table [P, rot / 2, 2] (rotary_table); the inverse turns
-    back, which is the gradient.  out may be x (b2b_rotary)."""
+class _Rotary(torch.autograd.Function):
+    """A rotation that is differentiated: the gradient is the inverse rotation."""
+
+    @staticmethod
+    def forward(ctx, x, table, positions, layout, inverse, stream):
+        out = _rotary(x, table, positions, layout, inverse, None, stream)
+        ctx.save_for_backward(table, positions)
+        ctx.layout, ctx.inverse = layout, inverse
+        return out
+
+    @staticmethod
+    def backward(ctx, grad):
+        table, positions = ctx.saved_tensors
+        # (a gradient may be broadcast, or lie in any order)
+        return rotary(grad.contiguous(), table, positions, ctx.layout, not ctx.inverse), \
+            None, None, None, None, None
+
+
+def _rotary(x, table, positions, layout, inverse, out, stream):
     got = (_native or _binding()).rotary(x, table, positions, _layout(layout), 1 if inverse else 0,
                                          out, stream)
     if type(got) is int:
         raise B2BError(got, "b2b_rotary")
     return got
+
+
+def rotary(x, table, positions, layout="half", inverse=False, out=None, stream=None):
+    """x [T, H, D] (token stride free) with the first rot channels of each head turned by the
+    angles of positions [T] (int32), table [P, rot / 2, 2] (rotary_table); the inverse turns
+    back, which is the gradient: where x requires one, the result carries it (by autograd, on the
+    stream that is current; not into a given out, and not for the table).  out may be x
+    (b2b_rotary)."""
+    if torch.is_grad_enabled() and (getattr(x, "requires_grad", False) or
+                                    getattr(table, "requires_grad", False) or
+                                    getattr(out, "requires_grad", False)):
+        if out is not None:
+            raise ValueError("out is given, but a rotation into it cannot be differentiated")
+        if getattr(table, "requires_grad", False):
+            raise ValueError("table requires a gradient, which the rotation does not give")
+        return _Rotary.apply(x, table, positions, layout, inverse, stream)
+    return _rotary(x, table, positions, layout, inverse, out, stream)
 
 
 def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts=None,
@@ -486,7 +518,8 @@ def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, sta
 
     page_table [B, pages per sequence], lens [B] (the new tokens included) and starts [B + 1]
     (rows of each sequence among the T; None: T / B each) are int32; max_new is the most new
-    tokens of a sequence (default: T, or T / B without starts)."""
+    tokens of a sequence (default: T, or T / B without starts).  It has no gradient: what it
+    returns and writes requires none."""
     got = (_native or _binding()).cache_append(
         k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts, max_new, table,
         _layout(layout), q, q_out, stream)
@@ -502,7 +535,8 @@ def cache_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, sta
     sequences' cached tokens, causal within the new ones: [T, q heads, D] (b2b_cache_attention).
     The cache and its sequences as in cache_append; scale defaults to D^-1/2; softcap caps the
     scores by a tanh, slopes [q heads] (float32) add slope * (key position - query position).
-    workspace (uint8, at least cache_attention_workspace's bytes): allocated when not given."""
+    workspace (uint8, at least cache_attention_workspace's bytes): allocated when not given.  It
+    has no gradient: the output requires none."""
     got = (_native or _binding()).cache_attention(
         q, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts, max_new, scale, softcap,
         slopes, out, workspace, stream)
