@@ -13,6 +13,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -337,7 +338,8 @@ PyObject* cache_attention_workspace(PyObject* const* a) {
   return PyLong_FromLongLong(st == B2B_OK ? bytes : -static_cast<int64_t>(st));
 }
 
-// No C++ exception leaves the module.
+// No C++ exception leaves the module: the refusals above as what they are, torch's own (memory that
+// has run out, say) as torch's Python functions raise them.
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != N) {
@@ -351,10 +353,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   } catch (const ValueRefusal& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
   } catch (const PythonError&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {
-    PyErr_SetString(PyExc_RuntimeError, "unknown error");
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

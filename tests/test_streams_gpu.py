@@ -63,3 +63,20 @@ def test_outputs_come_from_the_memory_of_the_stream_that_writes_them(name):
     with torch.cuda.stream(side):
         assert pools(None) == {side.cuda_stream}
         assert pools(0) == {0}
+
+
+def test_memory_that_runs_out_is_torch_s_error():
+    """Rows that overlap: operands of some MB, outputs of 2 TB."""
+    rows, head = 2 ** 20, 2 ** 20
+    x = torch.zeros(rows * 8 + head, dtype=torch.float16, device="cuda").as_strided((rows, 1, head), (8, head, 1))
+    positions = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        ops.rotary(x, ops.rotary_table(4, 64), positions)
+    cache = [torch.zeros(1, 1, 16, 64, device="cuda").to(torch.float8_e4m3fn) for _ in range(2)] + \
+        [torch.ones(1, 1, device="cuda") for _ in range(2)] + \
+        [torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")]
+    q = x[:, :, :64].expand(rows, head, 64).as_strided((rows, head // 64, 64), (8, 64, 1))
+    assert q.numel() == rows * head
+    with pytest.raises(torch.OutOfMemoryError):
+        ops.cache_attention(q, *cache)
+    torch.cuda.synchronize()
