@@ -66,6 +66,36 @@ b2b_status check_ld(int64_t ld, int64_t n) {
   return ld % 8 == 0 ? B2B_OK : B2B_ERR_ALIGN;
 }
 
+// T rows of n 16-bit elements, ld apart.
+struct RowSet {
+  const void* at;
+  int64_t ld, n;
+};
+// Whether a row of one is written while a row of the other may still have to be read.  Usually the two
+// lie apart as a whole; rows of one buffer (its columns side by side) are looked at row by row.
+bool overlap(const RowSet& a, const RowSet& b, int64_t T) {
+  // differences of addresses in elements; both are 16-byte aligned
+  const int64_t b0 = (static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.at)) -
+                      static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.at))) / 2;
+  const int64_t a_end = (T - 1) * a.ld + a.n, b_end = b0 + (T - 1) * b.ld + b.n;
+  if (b0 >= a_end || b_end <= 0) return false;
+  if (a.ld == b.ld) {                        // row t of one against rows t + d of the other
+    const int64_t d = b0 >= 0 ? b0 / a.ld : -((a.ld - 1 - b0) / a.ld), rest = b0 - d * a.ld;
+    return (rest < a.n && d < T && d > -T) || (rest + b.n > a.ld && d + 1 < T && d + 1 > -T);
+  }
+  for (int64_t t = 0; t < T; ++t) {
+    const int64_t lo = t * a.ld - b0, hi = lo + a.n;         // row t of a, in b's elements
+    if (hi <= 0) continue;
+    const int64_t first = lo < b.n ? 0 : (lo - b.n) / b.ld + 1;   // the first row of b that ends past lo
+    if (first >= T) break;
+    if (first * b.ld < hi) return true;
+  }
+  return false;
+}
+bool same_rows(const RowSet& a, const RowSet& b, int64_t T) {
+  return a.at == b.at && (a.ld == b.ld || T == 1) && a.n == b.n;
+}
+
 b2b_status check_cache(const b2b_cache* c, int64_t T) {
   if (c == nullptr) return B2B_ERR_NULL;
   if (c->pages < 0 || c->heads <= 0 || c->batch < 0 || c->max_pages < 0 || c->max_new < 0 || T < 0)
@@ -231,6 +261,8 @@ b2b_status b2b_rotary(b2b_dtype dt, int64_t T, int32_t H, int32_t D, int32_t rot
     return B2B_ERR_ALIGN;
   DecoderDevice* d = decoder_device();
   if (d == nullptr) return B2B_ERR_CUDA;
+  const RowSet in{x, ldx, static_cast<int64_t>(H) * D}, to{out, ldo, static_cast<int64_t>(H) * D};
+  if (!same_rows(in, to, T) && overlap(in, to, T)) return B2B_ERR_UNSUPPORTED;
   RotaryParams p;
   p.x = static_cast<const uint16_t*>(x);
   p.out = static_cast<uint16_t*>(out);
@@ -279,6 +311,13 @@ b2b_status b2b_cache_append(b2b_dtype dt, const b2b_cache* cache, int64_t T, con
   if (per_seq * cache->batch * cache->heads * 2 + T > 0x7FFFFFFF) return B2B_ERR_UNSUPPORTED;
   DecoderDevice* d = decoder_device();
   if (d == nullptr) return B2B_ERR_CUDA;
+  if (q != nullptr) {
+    const int64_t q_row = static_cast<int64_t>(q_heads) * cache->head_dim;
+    const RowSet from{q, ldq, q_row}, to{q_out, ldqo, q_row};
+    if ((!same_rows(from, to, T) && overlap(from, to, T)) || overlap(to, RowSet{k, ldk, row}, T) ||
+        overlap(to, RowSet{v, ldv, row}, T))
+      return B2B_ERR_UNSUPPORTED;
+  }
   AppendParams p;
   p.c = view_of(cache, T, d->err);
   p.k = static_cast<const uint16_t*>(k);
@@ -323,6 +362,8 @@ b2b_status b2b_cache_attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, 
     return B2B_ERR_ALIGN;
   DecoderDevice* d = decoder_device();
   if (d == nullptr) return B2B_ERR_CUDA;
+  const int64_t row = static_cast<int64_t>(q_heads) * cache->head_dim;
+  if (overlap(RowSet{q, ldq, row}, RowSet{out, row, row}, T)) return B2B_ERR_UNSUPPORTED;
   const SplitChoice sc = split_of(cache, q_heads, d->num_sms);
   if (sc.bytes > 0 && workspace == nullptr) return B2B_ERR_NULL;
   if (workspace_bytes < sc.bytes) return B2B_ERR_SHAPE;

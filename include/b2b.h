@@ -242,7 +242,7 @@ b2b_status b2b_rotary_table(int64_t positions, int32_t rot, double base, b2b_rot
  * once; channels past rot are copied.  inverse = 1 turns back (s -> -s), which is also the
  * gradient: dx = inverse rotation of dy (exactly so for gain 1; with another gain both carry
  * it).  x, out: T rows of H x D, strides ldx, ldo; out may be x (same stride) for an in-place
- * rotation, and must not overlap it otherwise.  positions: device int32 [T].
+ * rotation; rows that overlap otherwise are B2B_ERR_UNSUPPORTED.  positions: device int32 [T].
  * D a multiple of 8 up to 2048, rot a multiple of 16, rot <= D. */
 b2b_status b2b_rotary(b2b_dtype dt, int64_t T, int32_t H, int32_t D, int32_t rot,
                       b2b_rotary_layout layout, int32_t inverse, const void* x, int64_t ldx,
@@ -284,7 +284,8 @@ typedef struct b2b_cache {
  * in fp32, to nearest even, saturating (y / s' as y * 448 / A where that is s', so that exact
  * ties between two codes go to even; an infinity becomes +-448 s'; a NaN stays one).  Calling
  * again with the same arguments leaves the cache as it is.  Pages that are written belong to one
- * sequence.  k, v: T rows of heads x head_dim, strides ldk, ldv. */
+ * sequence.  k, v: T rows of heads x head_dim, strides ldk, ldv.  Rows of q_out that overlap k, v
+ * or, unless it is q, q are B2B_ERR_UNSUPPORTED. */
 b2b_status b2b_cache_append(b2b_dtype dt, const b2b_cache* cache, int64_t T, const void* k,
                             int64_t ldk, const void* v, int64_t ldv, const float* table,
                             int64_t positions_in_table, int32_t rot, b2b_rotary_layout layout,
@@ -298,7 +299,8 @@ b2b_status b2b_cache_append(b2b_dtype dt, const b2b_cache* cache, int64_t T, con
  * key is zero.  Sums, softmax and bias in fp32; the probabilities are rounded to fp16 before
  * the second product (11 bits; few rows per sequence with an fp16 output: twice that), out once
  * to dt.
- * q: T rows of q_heads x head_dim, stride ldq; out: dense [T][q_heads][head_dim], not q.
+ * q: T rows of q_heads x head_dim, stride ldq; out: dense [T][q_heads][head_dim]
+ * (B2B_ERR_UNSUPPORTED where it overlaps q's rows).
  * Nothing past a row's reach enters it, whatever its slots hold.
  * workspace: device memory of at least the bytes that b2b_cache_attention_workspace gives for
  * the same cache, T and q_heads (16-byte aligned; NULL where that is 0), free again when the
