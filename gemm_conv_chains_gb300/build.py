@@ -7,7 +7,7 @@ Each .cu file under csrc/ is compiled in parallel to an object under _build/, th
 into gemm_conv_chains_gb300/libb2b.so.  The library links the shared CUDA runtime, so a
 process that already loaded libcudart (e.g. through torch) uses that same instance.
 csrc/binding.cpp becomes gemm_conv_chains_gb300/_binding.so, a CPython extension against the
-installed torch's headers that calls libb2b.so beside it.
+installed torch's headers that calls libb2b.so beside it; another torch or Python has it built anew.
 """
 from __future__ import annotations
 
@@ -27,6 +27,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libb2b.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING_PATH = os.path.join(HERE, "_binding.so")
+BINDING_FOR = os.path.join(BUILD_DIR, "binding.for")     # the torch and Python it was compiled against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -53,11 +54,27 @@ def _deps():
         + [os.path.join(INCLUDE, "b2b.h"), BINDING_SRC, os.path.abspath(__file__)]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
+def _newer_than_sources(path) -> bool:
+    if not os.path.exists(path):
         return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
+    t = os.path.getmtime(path)
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _binding_target() -> str:
+    import torch
+    return f"torch {torch.__version__} in {_torch_dir()}, {sysconfig.get_config_var('SOABI')}"
+
+
+def _binding_fits() -> bool:
+    if not os.path.exists(BINDING_FOR):
+        return False
+    with open(BINDING_FOR) as f:
+        return f.read() == _binding_target()
+
+
+def up_to_date() -> bool:
+    return _newer_than_sources(LIB_PATH) and _newer_than_sources(BINDING_PATH) and _binding_fits()
 
 
 def compile_flags(extra=()):
@@ -93,6 +110,8 @@ def _link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING_PATH)
+    with open(BINDING_FOR, "w") as f:
+        f.write(_binding_target())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -100,6 +119,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if not force and not extra_flags and up_to_date():
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
+    if not force and not extra_flags and _newer_than_sources(LIB_PATH):     # another torch or Python
+        _link_binding(_compile_binding())
+        return LIB_PATH
     nvcc = _nvcc()
     flags = compile_flags(extra_flags)
 
