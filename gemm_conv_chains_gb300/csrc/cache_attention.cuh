@@ -30,15 +30,15 @@
 // products sum in fp32; the softmax is fp32.  P is rounded to fp16: 11 bits, much finer than a
 // bf16 output.  For fp16 outputs, whose own rounding is no coarser, the rest that this rounding
 // leaves is multiplied as well (one token over 250001 cached, error against 64 bits 3.0e-4
-// without it, 2.1e-4 with it, which is the output's own rounding; 30.8 us -> 32).  The value
+// without it, 2.1e-4 with it, which is the output's own rounding; 30.8 us -> 31.9).  The value
 // scales go into P before the rounding, and a row's running reference is that of the products (of
 // z + log2 scale), not of z alone: what a row's output mostly consists of keeps all of P's bits,
 // whatever the scales of the pages that it attends to less.
 //
-// Measured: 128 sequences of 8192 tokens, 32 query heads on 8 of 128 channels: 339 us, 6.34 TB/s,
-// 0.94 of the copy rate; 64 ragged ones of up to 4096: 63 us, 4.8 TB/s (a run's start, its page
-// numbers and the joining weigh more); 5 drafted tokens, 256 channels, softcap and bias: 47 us,
-// 3.2 TB/s, where the arithmetic counts too (two CTAs per SM for the registers of 16 rows).
+// Measured: 128 sequences of 8192 tokens, 32 query heads on 8 of 128 channels: 334 us, 6.45 TB/s,
+// 0.95 of the copy rate; 64 ragged ones of up to 4096: 62 us, 4.9 TB/s (a run's start, its page
+// numbers and the joining weigh more); 5 drafted tokens, 256 channels, softcap and bias: 49.5 us,
+// 3.1 TB/s, where the arithmetic counts too (two CTAs per SM for the registers of 16 rows).
 #pragma once
 
 #include "decoder_device.cuh"

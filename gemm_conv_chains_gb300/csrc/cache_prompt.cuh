@@ -23,14 +23,16 @@
 // 2^15, and O, in TMEM, is rescaled only then.
 //
 // Measured: prompts of 451 to 2048 tokens behind 1192 to 4096 cached ones (4 sequences, 32 query
-// heads on 8 of 128 channels): 236 us, 1.04 PFLOP/s, 0.54 of the library's dense bf16 rate.  The
-// split kernel took 1480 us on them.  The tensor pipe is busy for 42 % of the time: a key tile's
+// heads on 8 of 128 channels): 228 us, 1.07 PFLOP/s, 0.56 of the library's dense bf16 rate.  The
+// split kernel took 1480 us on them.  The tensor pipe is busy for 44 % of the time: a key tile's
 // chain (S ready, 128 columns read, exponentials, P written, P V and the next Q K^T issued) takes
-// ~3800 clocks, of which the products are ~1100 and a softmax warp's work ~1600; the rest are
-// hand-offs.  64 channels take as long per key tile as 128, so the bound is this latency.  Slower:
-// one issuing warp per row tile (353 us: the softmaxes fall into step and the tensor core idles;
-// 264 when the two take turns), waits that spin (238), rolled MMA loops (246), the operand waits
-// hidden behind the other row tile's products (239 to 252).
+// ~3700 clocks, of which the products are ~1100 and a softmax warp's work ~1500; the rest are
+// hand-offs.  64 channels take nearly as long per key tile as 128 (187 us for the same prompts), so
+// the bound is this latency; the tensor memory that they leave free is not used.  Capped or biased
+// scores take two passes over every tile (with a cap, up to 1024 tokens behind up to 2048: 417 us for 116).  Tried on an earlier form of
+// 236 us, and slower: one issuing warp per row tile (353 us: the softmaxes fall into step and the
+// tensor core idles; 264 when the two take turns), waits that spin (238), rolled MMA loops (246), the
+// operand waits hidden behind the other row tile's products (239 to 252).
 #pragma once
 
 #include <type_traits>

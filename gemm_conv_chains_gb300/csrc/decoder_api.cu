@@ -157,14 +157,17 @@ constexpr int kWholeTokens = 768;
 // with the key tiles of the longest unit (256 rows of one sequence and head) and the waves of units
 // over the SMs: 1.85 us per 128 keys (1.45 where a unit has only one row tile), whatever the head
 // size, latency between its softmax and its products.  The split kernel's goes with all the work,
-// cut evenly over the SMs: per 32 rows and 128 keys 7.5 ns at head size 128, 5.1 at 64.  Measured
-// over 1, 4 and 16 sequences of 300 to 30000 tokens, e.g. 8 kv heads of 128, 4 query heads each:
-//   1 sequence,   128 new tokens, 4000 cached: split  57 us, tcgen05  69
-//   1 sequence,   256 new tokens, 4000 cached: split  96 us, tcgen05  71
-//   4 sequences,   33 new tokens, 4000 cached: split  64 us, tcgen05  64
-//   16 sequences, 128 new tokens, 4000 cached: split 606 us, tcgen05 169
+// cut evenly over the SMs: per 32 rows and 128 keys 7.5 ns at head size 128, 5.1 at 64.  (Fitted over 1,
+// 4 and 16 sequences of 300 to 30000 tokens on forms of the kernels that have since become 3 to 6 %
+// slower, the split one, and 6 to 15 % faster, the tcgen05 one.)  Measured on 8 kv heads of 128, 4
+// query heads each, as the kernels are:
+//   1 sequence,   128 new tokens, 4000 cached: split  59 us, tcgen05  65
+//   1 sequence,   256 new tokens, 4000 cached: split 100 us, tcgen05  66
+//   4 sequences,   33 new tokens, 4000 cached: split  66 us, tcgen05  59
+//   16 sequences, 128 new tokens, 4000 cached: split 649 us, tcgen05 143
 // The split kernel also has the longer start and a second launch: it has to be 15 % ahead.  On
-// contexts of up to 512 tokens, where it does not cut sequences, it falls behind earlier.
+// contexts of up to 512 tokens, where it does not cut sequences, it falls behind earlier.  (Rows and
+// contexts are those that max_new and the page table leave room for: the host knows no others.)
 bool prompt_pays(int32_t D, int64_t rows, int64_t heads, bool few_keys, int num_sms) {
   if (D > 128 || rows <= 32) return false;
   const double pieces = static_cast<double>((rows + 31) / 32) * heads;      // of the split kernel

@@ -255,8 +255,11 @@ b2b_status b2b_rotary(b2b_dtype dt, int64_t T, int32_t H, int32_t D, int32_t rot
  * within a factor of 2^100 of one another, and below 2^13 if others are 0.  An append makes none
  * below 2^-64, and of fp16 values none above 2^8.)  Position j of sequence
  * s lies in slot j % page_size of page page_table[s][j / page_size].  The call's new tokens are
- * rows [starts[s], starts[s + 1]) of its inputs, positions lens[s] - n .. lens[s] - 1.  Page
- * numbers of positions at or past lens[s] are not read.  Every array is a device array. */
+ * rows [starts[s], starts[s + 1]) of its inputs, positions lens[s] - n .. lens[s] - 1; rows of no
+ * sequence have their outputs left as they are.  Page numbers of positions at or past lens[s] are not
+ * read.  Calls are planned on the host, which knows max_new and the room of the page table only: a
+ * max_new far above the batch's or a table with room for much longer sequences costs time, and so
+ * does one long chunk among single tokens (two calls take less).  Every array is a device array. */
 typedef struct b2b_cache {
     void* k;                    /* e4m3 [pages][heads][page_size][head_dim] */
     void* v;                    /* the same */
@@ -295,7 +298,8 @@ b2b_status b2b_cache_append(b2b_dtype dt, const b2b_cache* cache, int64_t T, con
 /* out[t][h] = sum_j softmax_j(z) v_j over the keys j <= i of its sequence, i the position of
  * row t, kv head h / (q_heads / heads):
  *   z_j = cap(scale * q . k_j) + slopes[h] * (j - i),   cap(x) = softcap * tanh(x / softcap)
- * (softcap 0: none; slopes NULL: no bias; slopes: device fp32 [q_heads]).  A row that sees no
+ * (softcap 0: none, else any finite one, below 2^-100 taken as that; slopes NULL: no bias; slopes:
+ * device fp32 [q_heads]).  A bf16 q is exact down to 2^-31 of the largest channel of its row and head.  A row that sees no
  * key is zero.  Sums, softmax and bias in fp32; the probabilities are rounded to fp16 before
  * the second product (11 bits; few rows per sequence with an fp16 output: twice that), out once
  * to dt.
