@@ -136,8 +136,24 @@ constexpr int attend_smem() {
          (NT > 1 ? D / 16 * NT * 256 : 0) + NT * 8 * 4;
 }
 
-// MODS: capped or biased scores.  F16: fp16 queries and outputs, else bf16.
-template <int D, int NT, bool MODS, bool F16>
+// Which of the 16 tokens from the new token `off` on a row of a tree sees, as bits: its mask's, and
+// every older token (off < 0, above -16).  Nothing at or past the n new ones (off < n).
+__device__ __forceinline__ uint32_t tree_window(const uint32_t* mask, int words, int off, int n) {
+  uint32_t w;
+  if (off < 0) {
+    w = (mask[0] << -off) | ((1u << -off) - 1u);
+  } else {
+    const int i = off >> 5, sh = off & 31;
+    w = mask[i] >> sh;
+    if (sh > 16 && i + 1 < words) w |= mask[i + 1] << (32 - sh);
+  }
+  const int left = n - off;
+  return w & (left < 16 ? (1u << left) - 1u : 0xFFFFu);
+}
+
+// MODS: capped or biased scores.  F16: fp16 queries and outputs, else bf16.  TREE: new tokens are seen
+// by the rows whose masks name them, else by their own and the later rows of the sequence.
+template <int D, int NT, bool MODS, bool F16, bool TREE>
 __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) attend_kernel(const AttendParams p) {
   using C = CacheDims<D, NT>;
   constexpr int RT = NT * 8;
@@ -242,8 +258,9 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
     const int row0 = rt * RT;
     const int last_row = row0 + RT - 1 < rows ? row0 + RT - 1 : rows - 1;
     const int start = s.len - s.n;
-    const int low_limit = start + row0 / p.group;         // last key of the tile's first row
-    const int high_limit = start + last_row / p.group;    // and of its last
+    // the last key that every row of the tile sees, and the last that any does
+    const int low_limit = TREE ? start - 1 : start + row0 / p.group;
+    const int high_limit = TREE ? s.len - 1 : start + last_row / p.group;
     int strip = static_cast<int>(p.whole ? 0 : t0 * (kTileTokens / kStrip)) + warp;
     const int strips_all = high_limit / kStrip + 1;
     const int strips_run = p.whole ? strips_all : static_cast<int>(t1 * (kTileTokens / kStrip));
@@ -354,7 +371,8 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
     float qfactor[NT][2];                            // of rows 8 nt + 2 t, + 1
     // The last key that each of them sees; with MODS as how far it lies behind the tile's last row's,
     // which gives the distance of key and row as well.
-    int limit[MODS ? 1 : NT][2];
+    // (TREE: the row's number among the new tokens.)
+    int limit[MODS && !TREE ? 1 : NT][2];
     float slope[MODS ? NT : 1][2], behind[MODS ? NT : 1][2];
     {
       float amax = 0.f;
@@ -404,12 +422,14 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
         const int tq = valid ? r / p.group : 0;
         qfactor[nt][i] = row_units[8 * nt + 2 * t + i] * p.scale * (MODS ? 1.f : kLog2e);
         if constexpr (MODS) {
-          behind[nt][i] = static_cast<float>(valid ? high_limit - (start + tq) : 0);
+          int place = start + tq;
+          if (TREE && p.positions != nullptr && valid) place = p.positions[s.row + static_cast<int64_t>(tq)];
+          behind[nt][i] = static_cast<float>(valid ? high_limit - place : 0);
           slope[nt][i] = 0.f;
           if (p.slopes != nullptr && valid) slope[nt][i] = p.slopes[h * p.group + (r - tq * p.group)];
-        } else {
-          limit[nt][i] = valid ? start + tq : 0x7FFFFFFF;
         }
+        if constexpr (TREE) limit[nt][i] = tq;
+        else if constexpr (!MODS) limit[nt][i] = valid ? start + tq : 0x7FFFFFFF;
       }
 
     float o[KS][NT][4];
@@ -464,8 +484,30 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
       const bool edge = strip * kStrip + kStrip - 1 > low_limit;
       // scores in the log2 domain
       const float away = MODS ? static_cast<float>(tok0 - high_limit) : 0.f;
+      uint32_t window[TREE ? NT : 1][2];     // the strip's tokens that the rows see
+      float moved[2] = {0.f, 0.f};           // from a new token's slot to its position
+      if constexpr (TREE) {
+        if (edge) {
+          const int off = strip * kStrip - start;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              window[nt][i] = tree_window(p.masks + (s.row + static_cast<int64_t>(limit[nt][i])) * p.mask_words,
+                                          p.mask_words, off, s.n);
+          if (MODS && p.positions != nullptr) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int at_new = tok0 + 8 * k - start;
+              if (at_new >= 0 && at_new < s.n)
+                moved[k] = static_cast<float>(p.positions[s.row + static_cast<int64_t>(at_new)] - (tok0 + 8 * k));
+            }
+          }
+        }
+      }
       auto hidden = [&](int nt, int i, int k) -> bool {      // token tok0 + 8 k from row 8 nt + 2 t + i
-        if constexpr (MODS) return away + static_cast<float>(8 * k) + behind[nt][i] > 0.f;
+        if constexpr (TREE) return ((window[nt][i] >> (C::token_of_row(g) + 8 * k)) & 1u) == 0u;
+        else if constexpr (MODS) return away + static_cast<float>(8 * k) + behind[nt][i] > 0.f;
         else return tok0 + 8 * k > limit[nt][i];
       };
       // (a value scale that is no number enters here, so that rows that do not reach its page stay clear)
@@ -477,7 +519,9 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
           float z = fmaf(x[nt][e] + x2[nt][e], qfactor[nt][e & 1] * sc.x, bad);
           if constexpr (MODS) {
             if (p.softcap > 0.f) z = capped(z, p.softcap, p.inv_softcap);
-            z = fmaf(slope[nt][e & 1], away + static_cast<float>(8 * (e >> 1)) + behind[nt][e & 1], z) * kLog2e;
+            float far = away + static_cast<float>(8 * (e >> 1)) + behind[nt][e & 1];
+            if constexpr (TREE) far += moved[e >> 1];
+            z = fmaf(slope[nt][e & 1], far, z) * kLog2e;
           }
           if (edge && hidden(nt, e & 1, e >> 1)) z = -INFINITY;
           x[nt][e] = z;
@@ -693,11 +737,11 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
   }
 }
 
-template <int D, int NT, bool MODS, bool F16>
+template <int D, int NT, bool MODS, bool F16, bool TREE>
 cudaError_t launch_attend_one(const AttendParams& p, cudaStream_t s) {
   constexpr int smem = attend_smem<D, NT>();
   static_assert(smem * attend_ctas_per_sm(D, NT) <= 226 * 1024, "CTAs per SM");
-  auto* fn = attend_kernel<D, NT, MODS, F16>;
+  auto* fn = attend_kernel<D, NT, MODS, F16, TREE>;
   // per device: a process that moves between devices sets it again, which is harmless
   static thread_local int set_on = -1;
   int dev = -1;
@@ -711,20 +755,22 @@ cudaError_t launch_attend_one(const AttendParams& p, cudaStream_t s) {
   return launch_early(fn, p.grid, kAttendWarps * 32, smem, s, p);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool TREE>
 cudaError_t launch_attend_nt(const AttendParams& p, cudaStream_t s) {
   if (p.softcap > 0.f || p.slopes != nullptr)
-    return p.is_bf16 ? launch_attend_one<D, NT, true, false>(p, s) : launch_attend_one<D, NT, true, true>(p, s);
-  return p.is_bf16 ? launch_attend_one<D, NT, false, false>(p, s) : launch_attend_one<D, NT, false, true>(p, s);
+    return p.is_bf16 ? launch_attend_one<D, NT, true, false, TREE>(p, s)
+                     : launch_attend_one<D, NT, true, true, TREE>(p, s);
+  return p.is_bf16 ? launch_attend_one<D, NT, false, false, TREE>(p, s)
+                   : launch_attend_one<D, NT, false, true, TREE>(p, s);
 }
 
-template <int D>
+template <int D, bool TREE>
 cudaError_t launch_attend_d(int nt, const AttendParams& p, cudaStream_t s) {
-  if (nt == 1) return launch_attend_nt<D, 1>(p, s);
+  if (nt == 1) return launch_attend_nt<D, 1, TREE>(p, s);
   if constexpr (D <= 128) {
-    if (nt == 4) return launch_attend_nt<D, 4>(p, s);
+    if (nt == 4) return launch_attend_nt<D, 4, TREE>(p, s);
   }
-  return launch_attend_nt<D, 2>(p, s);
+  return launch_attend_nt<D, 2, TREE>(p, s);
 }
 
 }  // namespace b2b

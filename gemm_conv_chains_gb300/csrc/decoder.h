@@ -1,5 +1,6 @@
 // decoder.h -- internal interface of the decoder-block operators (rotary positions, the
-// append to a paged e4m3 cache, the attention over it): launch parameters and launchers.
+// append to a paged e4m3 cache, the attention over it, the cache's pages): launch parameters and
+// launchers.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -13,9 +14,14 @@ enum DecoderError : uint32_t {
   DEC_ERR_POSITION = 1,   // a position outside the rotary table
   DEC_ERR_PAGE = 2,       // a page number outside the pool
   DEC_ERR_LENGTH = 3,     // a length that is below its new tokens or above its page table
-  DEC_ERR_STARTS = 4      // starts that decrease, leave the rows or exceed max_new
+  DEC_ERR_STARTS = 4,     // starts that decrease, leave the rows or exceed max_new
+  DEC_ERR_PARENT = 5,     // a parent that is no row of the page table
+  DEC_ERR_TOKEN = 6       // a kept token outside its sequence or out of order
 };
-enum DecoderKernel : uint32_t { DK_ROTARY = 32, DK_APPEND = 33, DK_ATTEND = 34, DK_PROMPT = 35 };
+enum DecoderKernel : uint32_t {
+  DK_ROTARY = 32, DK_APPEND = 33, DK_ATTEND = 34, DK_PROMPT = 35, DK_PAGES = 36, DK_COPY = 37,
+  DK_COMPACT = 38
+};
 constexpr uint32_t kCodeIndex = 2;   // B2B_ERR_SHAPE: a length, page number or position out of range
 
 constexpr float kE4m3Max = 448.f;
@@ -63,6 +69,9 @@ struct AttendParams {
   const uint16_t* q;
   uint16_t* out;              // [T][q_heads][D]
   const float* slopes;        // [q_heads] or null
+  const uint32_t* masks;      // drafted trees: [T][mask_words] bits, else null
+  const int32_t* positions;   // of the new tokens [T], or null: their slots
+  int32_t mask_words;
   int64_t ldq;
   int32_t q_heads, group, is_bf16;
   float scale, softcap;       // softcap 0: none
@@ -73,22 +82,62 @@ struct AttendParams {
   uint64_t wait_limit_ns;
 };
 
+// The page table of a step's sequences from the last step's.
+struct PagesParams {
+  const int32_t* table;       // [B][width]
+  const int32_t* lens;        // [B]
+  const int32_t* parents;     // [rows], or null: row r follows r
+  const int32_t* kept;        // [rows], or null: all of the parent's tokens
+  const int32_t* fresh;       // [rows], or null: no new tokens
+  int32_t* table_out;         // [rows][width]
+  int32_t* lens_out;          // [rows]
+  int32_t* copies;            // [rows][3]
+  int32_t* left;              // [1]
+  uint32_t* owners;           // [pages], or null: in shared memory
+  int64_t pages;
+  int32_t B, width, rows, page_shift;
+  uint32_t* err;
+};
+
+struct CopyParams {
+  CacheView c;
+  const int32_t* copies;      // [n][3]: from, to, tokens
+  int64_t n;
+};
+
+struct CompactParams {
+  CacheView c;
+  const int32_t* first;       // [B]
+  const int32_t* tokens;      // [B][max_tokens]
+  const int32_t* counts;      // [B]
+  int32_t max_tokens;
+};
+
 // Launches with programmatic stream serialisation, as the chain kernels: the kernel may be scheduled
 // while the one before it in the stream finishes, and waits for that (griddepcontrol.wait) before
 // it touches global memory.
+// `cluster`: consecutive CTAs of one thread-block cluster.
 template <class... P, class... A>
-cudaError_t launch_early(void (*fn)(P...), int64_t grid, int block, int smem, cudaStream_t s, A... args) {
+cudaError_t launch_early_clusters(void (*fn)(P...), int64_t grid, int cluster, int block, int smem,
+                                  cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(static_cast<unsigned>(block));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
+}
+template <class... P, class... A>
+cudaError_t launch_early(void (*fn)(P...), int64_t grid, int block, int smem, cudaStream_t s, A... args) {
+  return launch_early_clusters(fn, grid, 1, block, smem, s, args...);
 }
 
 cudaError_t launch_rotary(bool bf16, const RotaryParams& p, int num_sms, cudaStream_t s);
@@ -101,17 +150,29 @@ cudaError_t launch_append(bool bf16, const AppendParams& p, int num_sms, cudaStr
 __host__ __device__ constexpr int attend_ctas_per_sm(int D, int nt) {
   return nt == 1 && D <= 128 ? 3 : 2;
 }
-// The split kernel with row tiles of 8 nt query rows, per head size.
+// The split kernel with row tiles of 8 nt query rows, per head size; tree: of drafted trees.
 cudaError_t launch_attend_64(int nt, const AttendParams& p, cudaStream_t s);
 cudaError_t launch_attend_96(int nt, const AttendParams& p, cudaStream_t s);
 cudaError_t launch_attend_128(int nt, const AttendParams& p, cudaStream_t s);
 cudaError_t launch_attend_192(int nt, const AttendParams& p, cudaStream_t s);
 cudaError_t launch_attend_256(int nt, const AttendParams& p, cudaStream_t s);
+cudaError_t launch_attend_tree_64(int nt, const AttendParams& p, cudaStream_t s);
+cudaError_t launch_attend_tree_96(int nt, const AttendParams& p, cudaStream_t s);
+cudaError_t launch_attend_tree_128(int nt, const AttendParams& p, cudaStream_t s);
+cudaError_t launch_attend_tree_192(int nt, const AttendParams& p, cudaStream_t s);
+cudaError_t launch_attend_tree_256(int nt, const AttendParams& p, cudaStream_t s);
 // The tcgen05 kernel for prompts (head sizes 64, 96, 128).
 cudaError_t launch_prompt(const AttendParams& p, cudaStream_t s);
 // Bytes of workspace that it takes for `rows` query rows per sequence and kv head (p.meta).
 int64_t prompt_workspace(int64_t rows, int32_t B);
 // Joins what the split kernel left in parts.
 cudaError_t launch_attend_combine(const AttendParams& p, int nt, int num_sms, cudaStream_t s);
+
+// Bytes of workspace that the page table's kernel takes, and the most rows that it does.
+int64_t pages_workspace(int64_t pages);
+constexpr int32_t kMostPageRows = 4096;
+cudaError_t launch_pages(const PagesParams& p, cudaStream_t s);
+cudaError_t launch_copy(const CopyParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_compact(const CompactParams& p, int num_sms, cudaStream_t s);
 
 }  // namespace b2b

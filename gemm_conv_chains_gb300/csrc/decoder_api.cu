@@ -96,6 +96,21 @@ bool same_rows(const RowSet& a, const RowSet& b, int64_t T) {
   return a.at == b.at && (a.ld == b.ld || T == 1) && a.n == b.n;
 }
 
+// The pool by itself, without the sequences of a call.
+b2b_status check_pool(const b2b_cache* c) {
+  if (c == nullptr) return B2B_ERR_NULL;
+  if (c->pages < 0 || c->heads <= 0) return B2B_ERR_SHAPE;
+  if (!head_size(c->head_dim)) return B2B_ERR_UNSUPPORTED;
+  const int32_t ps = c->page_size;
+  if (ps < 16 || ps > 256 || (ps & (ps - 1)) != 0) return B2B_ERR_UNSUPPORTED;
+  return c->pages > (int64_t{1} << 30) || c->heads > 65536 ? B2B_ERR_UNSUPPORTED : B2B_OK;
+}
+b2b_status check_pool_pointers(const b2b_cache* c) {
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale) return B2B_ERR_NULL;
+  return !aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)
+             ? B2B_ERR_ALIGN : B2B_OK;
+}
+
 b2b_status check_cache(const b2b_cache* c, int64_t T) {
   if (c == nullptr) return B2B_ERR_NULL;
   if (c->pages < 0 || c->heads <= 0 || c->batch < 0 || c->max_pages < 0 || c->max_new < 0 || T < 0)
@@ -181,7 +196,7 @@ bool prompt_pays(int32_t D, int64_t rows, int64_t heads, bool few_keys, int num_
 // The limit of each on-chip wait of the tcgen05 kernel.
 constexpr uint64_t kDecoderWaitNs = 1000000000ull;
 
-SplitChoice split_of(const b2b_cache* c, int32_t q_heads, int num_sms) {
+SplitChoice split_of(const b2b_cache* c, int32_t q_heads, bool tree, int num_sms) {
   SplitChoice s;
   const int64_t rows = static_cast<int64_t>(c->max_new) * (q_heads / c->heads);
   s.nt = rows <= 8 ? 1 : rows <= 16 || c->head_dim > 128 ? 2 : 4;
@@ -192,8 +207,8 @@ SplitChoice split_of(const b2b_cache* c, int32_t q_heads, int num_sms) {
   const int64_t pieces = (rows + 8 * s.nt - 1) / (8 * s.nt) * c->heads * c->batch;
   const int64_t runs = s.whole ? pieces : pieces * ((most / 64 + kMinTiles - 1) / kMinTiles);
   if (runs < s.grid) s.grid = static_cast<int>(runs);
-  s.prompt = prompt_pays(c->head_dim, rows, static_cast<int64_t>(c->batch) * c->heads, most <= 512,
-                         num_sms);
+  s.prompt = !tree && prompt_pays(c->head_dim, rows, static_cast<int64_t>(c->batch) * c->heads,
+                                  most <= 512, num_sms);
   s.bytes = s.prompt  ? prompt_workspace(rows, c->batch)
             : s.whole ? 0
                     : 16 * ((static_cast<int64_t>(c->batch) + 4) / 4) +
@@ -214,6 +229,98 @@ b2b_status check_attention(const b2b_cache* c, int64_t T, int32_t q_heads, float
                        std::ceil(static_cast<double>(rows) / c->heads / 8) * c->heads * c->batch;
   if (tiles > 2.0e9) return B2B_ERR_UNSUPPORTED;
   return B2B_OK;
+}
+
+// What tells the attention of drafted trees from the causal one: mask null for that.
+struct TreeArgs {
+  const uint64_t* masks;
+  int32_t words;
+  const int32_t* positions;
+};
+
+b2b_status attention_workspace(const b2b_cache* cache, int64_t T, int32_t q_heads, bool tree,
+                               int64_t* bytes) {
+  if (bytes == nullptr) return B2B_ERR_NULL;
+  *bytes = 0;
+  if (b2b_status st = check_attention(cache, T, q_heads, 1.f, 0.f); st != B2B_OK) return st;
+  if (T == 0) return B2B_OK;
+  DecoderDevice* d = decoder_device();
+  if (d == nullptr) return B2B_ERR_CUDA;
+  *bytes = split_of(cache, q_heads, tree, d->num_sms).bytes;
+  return B2B_OK;
+}
+
+b2b_status attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, const void* q, int64_t ldq,
+                     int32_t q_heads, const TreeArgs* tree, float scale, float softcap,
+                     const float* slopes, void* out, void* workspace, int64_t workspace_bytes,
+                     void* stream) {
+  if (dt != B2B_F16 && dt != B2B_BF16) return B2B_ERR_UNSUPPORTED;
+  if (b2b_status st = check_attention(cache, T, q_heads, scale, softcap); st != B2B_OK) return st;
+  if (b2b_status st = check_ld(ldq, static_cast<int64_t>(q_heads) * cache->head_dim); st != B2B_OK)
+    return st;
+  if (tree != nullptr && (tree->words <= 0 || static_cast<int64_t>(tree->words) * 64 < cache->max_new))
+    return B2B_ERR_SHAPE;
+  if (tree != nullptr && tree->words > (1 << 24)) return B2B_ERR_UNSUPPORTED;
+  if (T == 0) return B2B_OK;
+  if (!q || !out || (tree != nullptr && !tree->masks)) return B2B_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(slopes, 4) || !aligned(workspace, 16))
+    return B2B_ERR_ALIGN;
+  if (tree != nullptr && (!aligned(tree->masks, 8) || !aligned(tree->positions, 4))) return B2B_ERR_ALIGN;
+  DecoderDevice* d = decoder_device();
+  if (d == nullptr) return B2B_ERR_CUDA;
+  const int64_t row = static_cast<int64_t>(q_heads) * cache->head_dim;
+  if (overlap(RowSet{q, ldq, row}, RowSet{out, row, row}, T)) return B2B_ERR_UNSUPPORTED;
+  const SplitChoice sc = split_of(cache, q_heads, tree != nullptr, d->num_sms);
+  if (sc.bytes > 0 && workspace == nullptr) return B2B_ERR_NULL;
+  if (workspace_bytes < sc.bytes) return B2B_ERR_SHAPE;
+  AttendParams p;
+  p.c = view_of(cache, T, d->err);
+  p.q = static_cast<const uint16_t*>(q);
+  p.out = static_cast<uint16_t*>(out);
+  p.slopes = slopes;
+  p.masks = tree != nullptr ? reinterpret_cast<const uint32_t*>(tree->masks) : nullptr;
+  p.mask_words = tree != nullptr ? 2 * tree->words : 0;
+  p.positions = tree != nullptr ? tree->positions : nullptr;
+  p.ldq = ldq;
+  p.q_heads = q_heads;
+  p.group = q_heads / cache->heads;
+  p.is_bf16 = dt == B2B_BF16;
+  p.scale = scale;
+  // a cap below 2^-100 is nothing beside any other score's rounding, and its inverse stays finite
+  p.softcap = softcap > 0.f && softcap < 7.8886091e-31f ? 7.8886091e-31f : softcap;
+  p.inv_softcap = softcap > 0.f ? 1.f / p.softcap : 0.f;
+  p.grid = sc.grid;
+  p.min_tiles = kMinTiles;
+  p.whole = sc.whole;
+  p.meta = sc.bytes == 0 ? nullptr : static_cast<uint32_t*>(workspace);
+  p.part = sc.bytes == 0 || sc.prompt ? nullptr
+                    : reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                               16 * ((static_cast<int64_t>(cache->batch) + 4) / 4));
+  p.wait_limit_ns = kDecoderWaitNs;
+  auto s = static_cast<cudaStream_t>(stream);
+  if (sc.prompt) return launched(launch_prompt(p, s));
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (cache->head_dim) {
+    case 64: e = (tree != nullptr ? launch_attend_tree_64 : launch_attend_64)(sc.nt, p, s); break;
+    case 96: e = (tree != nullptr ? launch_attend_tree_96 : launch_attend_96)(sc.nt, p, s); break;
+    case 128: e = (tree != nullptr ? launch_attend_tree_128 : launch_attend_128)(sc.nt, p, s); break;
+    case 192: e = (tree != nullptr ? launch_attend_tree_192 : launch_attend_192)(sc.nt, p, s); break;
+    case 256: e = (tree != nullptr ? launch_attend_tree_256 : launch_attend_256)(sc.nt, p, s); break;
+    default: break;
+  }
+  if (e != cudaSuccess || sc.whole) return launched(e);
+  return launched(launch_attend_combine(p, sc.nt, d->num_sms, s));
+}
+
+bool apart(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a == nullptr || b == nullptr || x + static_cast<uint64_t>(a_bytes) <= y ||
+         y + static_cast<uint64_t>(b_bytes) <= x;
+}
+
+b2b_status check_pages(int64_t pages, int32_t rows) {
+  if (pages < 0 || rows < 0) return B2B_ERR_SHAPE;
+  return pages > (int64_t{1} << 30) || rows > kMostPageRows ? B2B_ERR_UNSUPPORTED : B2B_OK;
 }
 
 }  // namespace
@@ -341,69 +448,136 @@ b2b_status b2b_cache_append(b2b_dtype dt, const b2b_cache* cache, int64_t T, con
 
 b2b_status b2b_cache_attention_workspace(const b2b_cache* cache, int64_t T, int32_t q_heads,
                                          int64_t* bytes) {
-  if (bytes == nullptr) return B2B_ERR_NULL;
-  *bytes = 0;
-  if (b2b_status st = check_attention(cache, T, q_heads, 1.f, 0.f); st != B2B_OK) return st;
-  if (T == 0) return B2B_OK;
-  DecoderDevice* d = decoder_device();
-  if (d == nullptr) return B2B_ERR_CUDA;
-  *bytes = split_of(cache, q_heads, d->num_sms).bytes;
-  return B2B_OK;
+  return attention_workspace(cache, T, q_heads, false, bytes);
 }
 
 b2b_status b2b_cache_attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, const void* q,
                                int64_t ldq, int32_t q_heads, float scale, float softcap,
                                const float* slopes, void* out, void* workspace,
                                int64_t workspace_bytes, void* stream) {
-  if (dt != B2B_F16 && dt != B2B_BF16) return B2B_ERR_UNSUPPORTED;
-  if (b2b_status st = check_attention(cache, T, q_heads, scale, softcap); st != B2B_OK) return st;
-  if (b2b_status st = check_ld(ldq, static_cast<int64_t>(q_heads) * cache->head_dim); st != B2B_OK)
-    return st;
-  if (T == 0) return B2B_OK;
-  if (!q || !out) return B2B_ERR_NULL;
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(slopes, 4) || !aligned(workspace, 16))
+  return attention(dt, cache, T, q, ldq, q_heads, nullptr, scale, softcap, slopes, out, workspace,
+                   workspace_bytes, stream);
+}
+
+b2b_status b2b_cache_tree_attention_workspace(const b2b_cache* cache, int64_t T, int32_t q_heads,
+                                              int64_t* bytes) {
+  return attention_workspace(cache, T, q_heads, true, bytes);
+}
+
+b2b_status b2b_cache_tree_attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, const void* q,
+                                    int64_t ldq, int32_t q_heads, const uint64_t* masks,
+                                    int32_t mask_words, const int32_t* positions, float scale,
+                                    float softcap, const float* slopes, void* out, void* workspace,
+                                    int64_t workspace_bytes, void* stream) {
+  const TreeArgs tree{masks, mask_words, positions};
+  return attention(dt, cache, T, q, ldq, q_heads, &tree, scale, softcap, slopes, out, workspace,
+                   workspace_bytes, stream);
+}
+
+b2b_status b2b_cache_pages_workspace(int64_t pages, int32_t rows, int64_t* bytes) {
+  if (bytes == nullptr) return B2B_ERR_NULL;
+  *bytes = 0;
+  if (b2b_status st = check_pages(pages, rows); st != B2B_OK) return st;
+  *bytes = pages_workspace(pages);
+  return B2B_OK;
+}
+
+b2b_status b2b_cache_pages(int32_t page_size, int64_t pages, int32_t batch, int32_t max_pages,
+                           const int32_t* page_table, const int32_t* lens, int32_t rows,
+                           const int32_t* parents, const int32_t* kept, const int32_t* fresh,
+                           int32_t* table_out, int32_t* lens_out, int32_t* copies, int32_t* left,
+                           void* workspace, int64_t workspace_bytes, void* stream) {
+  if (b2b_status st = check_pages(pages, rows); st != B2B_OK) return st;
+  if (batch < 0 || max_pages < 0 || (parents == nullptr && rows != batch && rows != 0)) return B2B_ERR_SHAPE;
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0) return B2B_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(max_pages) * page_size > 0x7FFFFFFF - 4096 ||
+      static_cast<int64_t>(rows) * max_pages > 0x7FFFFFFF)
+    return B2B_ERR_UNSUPPORTED;
+  const int64_t in = static_cast<int64_t>(batch) * max_pages, to = static_cast<int64_t>(rows) * max_pages;
+  if (left == nullptr || (in > 0 && page_table == nullptr) || (batch > 0 && lens == nullptr) ||
+      (to > 0 && table_out == nullptr) || (rows > 0 && (lens_out == nullptr || copies == nullptr)))
+    return B2B_ERR_NULL;
+  const void* small[9] = {page_table, lens, parents, kept, fresh, table_out, lens_out, copies, left};
+  for (const void* a : small)
+    if (!aligned(a, 4)) return B2B_ERR_ALIGN;
+  if (!aligned(workspace, 16)) return B2B_ERR_ALIGN;
+  // nothing that is written lies over what is read, or over another output
+  const int64_t n = rows;
+  const int64_t bytes = pages_workspace(pages);
+  const void* read[5] = {page_table, lens, parents, kept, fresh};
+  const int64_t read_bytes[5] = {4 * in, 4 * static_cast<int64_t>(batch), 4 * n, 4 * n, 4 * n};
+  const void* written[5] = {table_out, lens_out, copies, left, bytes > 0 ? workspace : nullptr};
+  const int64_t written_bytes[5] = {4 * to, 4 * n, 12 * n, 4, bytes};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < 5; ++j)
+      if (!apart(written[i], written_bytes[i], read[j], read_bytes[j])) return B2B_ERR_UNSUPPORTED;
+    for (int j = 0; j < i; ++j)
+      if (!apart(written[i], written_bytes[i], written[j], written_bytes[j])) return B2B_ERR_UNSUPPORTED;
+  }
+  if (bytes > 0 && workspace == nullptr) return B2B_ERR_NULL;
+  if (workspace_bytes < bytes) return B2B_ERR_SHAPE;
+  DecoderDevice* d = decoder_device();
+  if (d == nullptr) return B2B_ERR_CUDA;
+  PagesParams p;
+  p.table = page_table;
+  p.lens = lens;
+  p.parents = parents;
+  p.kept = kept;
+  p.fresh = fresh;
+  p.table_out = table_out;
+  p.lens_out = lens_out;
+  p.copies = copies;
+  p.left = left;
+  p.owners = bytes > 0 ? static_cast<uint32_t*>(workspace) : nullptr;
+  p.pages = pages;
+  p.B = batch;
+  p.width = max_pages;
+  p.rows = rows;
+  p.page_shift = __builtin_ctz(static_cast<unsigned>(page_size));
+  p.err = d->err;
+  return launched(launch_pages(p, static_cast<cudaStream_t>(stream)));
+}
+
+b2b_status b2b_cache_copy(const b2b_cache* cache, int64_t n, const int32_t* copies, void* stream) {
+  if (b2b_status st = check_pool(cache); st != B2B_OK) return st;
+  if (n < 0) return B2B_ERR_SHAPE;
+  if (n > kMostRows) return B2B_ERR_UNSUPPORTED;
+  if (n == 0) return B2B_OK;
+  if (!copies) return B2B_ERR_NULL;
+  if (b2b_status st = check_pool_pointers(cache); st != B2B_OK) return st;
+  if (!aligned(copies, 4)) return B2B_ERR_ALIGN;
+  DecoderDevice* d = decoder_device();
+  if (d == nullptr) return B2B_ERR_CUDA;
+  CopyParams p;
+  p.c = view_of(cache, 0, d->err);
+  p.copies = copies;
+  p.n = n;
+  return launched(launch_copy(p, d->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+b2b_status b2b_cache_compact(const b2b_cache* cache, const int32_t* first, const int32_t* tokens,
+                             int32_t max_tokens, const int32_t* counts, void* stream) {
+  if (b2b_status st = check_pool(cache); st != B2B_OK) return st;
+  if (cache->batch < 0 || cache->max_pages < 0 || max_tokens < 0) return B2B_ERR_SHAPE;
+  if (static_cast<int64_t>(cache->max_pages) * cache->page_size > 0x7FFFFFFF - 4096)
+    return B2B_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(cache->batch) * cache->heads * 2 > 0x7FFFFFFF / 16) return B2B_ERR_UNSUPPORTED;
+  if (cache->batch == 0 || max_tokens == 0) return B2B_OK;
+  if (cache->pages == 0 || cache->max_pages == 0) return B2B_ERR_SHAPE;
+  if (!first || !tokens || !counts || !cache->page_table || !cache->lens) return B2B_ERR_NULL;
+  if (b2b_status st = check_pool_pointers(cache); st != B2B_OK) return st;
+  if (!aligned(first, 4) || !aligned(tokens, 4) || !aligned(counts, 4) || !aligned(cache->page_table, 4) ||
+      !aligned(cache->lens, 4))
     return B2B_ERR_ALIGN;
   DecoderDevice* d = decoder_device();
   if (d == nullptr) return B2B_ERR_CUDA;
-  const int64_t row = static_cast<int64_t>(q_heads) * cache->head_dim;
-  if (overlap(RowSet{q, ldq, row}, RowSet{out, row, row}, T)) return B2B_ERR_UNSUPPORTED;
-  const SplitChoice sc = split_of(cache, q_heads, d->num_sms);
-  if (sc.bytes > 0 && workspace == nullptr) return B2B_ERR_NULL;
-  if (workspace_bytes < sc.bytes) return B2B_ERR_SHAPE;
-  AttendParams p;
-  p.c = view_of(cache, T, d->err);
-  p.q = static_cast<const uint16_t*>(q);
-  p.out = static_cast<uint16_t*>(out);
-  p.slopes = slopes;
-  p.ldq = ldq;
-  p.q_heads = q_heads;
-  p.group = q_heads / cache->heads;
-  p.is_bf16 = dt == B2B_BF16;
-  p.scale = scale;
-  // a cap below 2^-100 is nothing beside any other score's rounding, and its inverse stays finite
-  p.softcap = softcap > 0.f && softcap < 7.8886091e-31f ? 7.8886091e-31f : softcap;
-  p.inv_softcap = softcap > 0.f ? 1.f / p.softcap : 0.f;
-  p.grid = sc.grid;
-  p.min_tiles = kMinTiles;
-  p.whole = sc.whole;
-  p.meta = sc.bytes == 0 ? nullptr : static_cast<uint32_t*>(workspace);
-  p.part = sc.bytes == 0 || sc.prompt ? nullptr
-                    : reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                               16 * ((static_cast<int64_t>(cache->batch) + 4) / 4));
-  p.wait_limit_ns = kDecoderWaitNs;
-  auto s = static_cast<cudaStream_t>(stream);
-  if (sc.prompt) return launched(launch_prompt(p, s));
-  cudaError_t e = cudaErrorInvalidValue;
-  switch (cache->head_dim) {
-    case 64: e = launch_attend_64(sc.nt, p, s); break;
-    case 96: e = launch_attend_96(sc.nt, p, s); break;
-    case 128: e = launch_attend_128(sc.nt, p, s); break;
-    case 192: e = launch_attend_192(sc.nt, p, s); break;
-    case 256: e = launch_attend_256(sc.nt, p, s); break;
-    default: break;
-  }
-  if (e != cudaSuccess || sc.whole) return launched(e);
-  return launched(launch_attend_combine(p, sc.nt, d->num_sms, s));
+  CompactParams p;
+  p.c = view_of(cache, 0, d->err);
+  p.first = first;
+  p.tokens = tokens;
+  p.max_tokens = max_tokens;
+  p.counts = counts;
+  return launched(launch_compact(p, d->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 b2b_status b2b_get_cache_error(uint32_t info[4]) {

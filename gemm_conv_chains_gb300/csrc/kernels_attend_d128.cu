@@ -4,7 +4,7 @@
 namespace b2b {
 
 cudaError_t launch_attend_128(int nt, const AttendParams& p, cudaStream_t s) {
-  return launch_attend_d<128>(nt, p, s);
+  return launch_attend_d<128, false>(nt, p, s);
 }
 
 }  // namespace b2b

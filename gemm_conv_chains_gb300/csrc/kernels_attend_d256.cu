@@ -4,7 +4,7 @@
 namespace b2b {
 
 cudaError_t launch_attend_256(int nt, const AttendParams& p, cudaStream_t s) {
-  return launch_attend_d<256>(nt, p, s);
+  return launch_attend_d<256, false>(nt, p, s);
 }
 
 }  // namespace b2b

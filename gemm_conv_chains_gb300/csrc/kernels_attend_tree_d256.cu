@@ -1,0 +1,10 @@
+// kernels_attend_tree_d256.cu -- the split cache attention of drafted trees for head size 256.
+#include "cache_attention.cuh"
+
+namespace b2b {
+
+cudaError_t launch_attend_tree_256(int nt, const AttendParams& p, cudaStream_t s) {
+  return launch_attend_d<256, true>(nt, p, s);
+}
+
+}  // namespace b2b

@@ -555,6 +555,79 @@ def cache_attention_workspace(T, q_heads, k_cache, v_cache, k_scale, v_scale, pa
     return got
 
 
+def cache_tree_attention(q, masks, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts=None,
+                         max_new=None, positions=None, scale=None, softcap=0.0, slopes=None, out=None,
+                         workspace=None, stream=None):
+    """cache_attention of drafted trees: row t of q sees every older token of its sequence and those
+    new ones, token i of the sequence's, whose bit i % 64 of masks[t, i // 64] is set (int64
+    [T, words], usually a node's ancestors and itself; a row that sees nothing is zero).  positions
+    [T] (int32): the new tokens' positions for `slopes`' distances (None: their slots').  The tokens
+    are appended in any order (cache_append), their keys turned before by `rotary` with those
+    positions (b2b_cache_tree_attention)."""
+    got = (_native or _binding()).cache_tree_attention(
+        q, masks, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts, max_new, positions,
+        scale, softcap, slopes, out, workspace, stream)
+    if type(got) is int:
+        raise B2BError(got, "b2b_cache_tree_attention")
+    return got
+
+
+def cache_tree_attention_workspace(T, q_heads, k_cache, v_cache, k_scale, v_scale, page_table, lens,
+                                   starts=None, max_new=None) -> int:
+    """Bytes of workspace that cache_tree_attention takes for these arguments (0: none)."""
+    got = (_native or _binding()).cache_tree_attention_workspace(
+        T, q_heads, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts, max_new)
+    if got < 0:
+        raise B2BError(-got, "b2b_cache_tree_attention_workspace")
+    return got
+
+
+def cache_pages(page_table, lens, pages, page_size, parents=None, kept=None, new=None, out=None,
+                workspace=None, stream=None):
+    """The page table of the next step's sequences: (table [R, width], lens [R], copies [R, 3],
+    left [1]), int32 (b2b_cache_pages).  Row r follows row parents[r] of page_table [B, width] (-1:
+    an empty sequence; default: row r) for its first kept[r] tokens (default: all lens of it) and gets
+    room for new[r] more (default: none), which its new length counts; all int32 [R].  Pages that no
+    row keeps are free; rows that share the page that one of them writes on get copies of it, which
+    cache_copy has to make before the append.  left: the free pages that remain, or minus those that
+    were missing (their entries are -1).  out: the four results' tensors, none of them an input's
+    memory (the tables of a program that keeps two and takes them in turn).  workspace: uint8, for
+    pools above 327680 pages; allocated when not given."""
+    if out is None:
+        out = (None, None, None, None)
+    else:
+        out = tuple(out)
+        if len(out) != 4 or any(t is None for t in out):
+            raise ValueError("out must have four tensors: the table, the lengths, the copies, the "
+                             "count left")
+    got = (_native or _binding()).cache_pages(page_table, lens, pages, page_size, parents, kept, new,
+                                              *out, workspace, stream)
+    if type(got) is int:
+        raise B2BError(got, "b2b_cache_pages")
+    return got
+
+
+def cache_copy(k_cache, v_cache, k_scale, v_scale, copies, stream=None):
+    """Copies pages of the cache, in place: the first copies[i, 2] tokens of page copies[i, 0] to page
+    copies[i, 1], keys, values and scales (int32 [N, 3], as cache_pages gives them; negative pages:
+    none) (b2b_cache_copy)."""
+    got = (_native or _binding()).cache_copy(k_cache, v_cache, k_scale, v_scale, copies, stream)
+    if type(got) is int:
+        raise B2BError(got, "b2b_cache_copy")
+
+
+def cache_compact(k_cache, v_cache, k_scale, v_scale, page_table, lens, first, tokens, counts,
+                  stream=None):
+    """Moves the tokens that each sequence keeps together, in place: the token at position
+    tokens[b, i] (int32 [B, most], ascending from first[b] on) goes to position first[b] + i, for
+    i < counts[b]; lens [B] are the lengths before, first + counts those after.  The accepted path of
+    drafted tokens, or what an eviction leaves (b2b_cache_compact)."""
+    got = (_native or _binding()).cache_compact(k_cache, v_cache, k_scale, v_scale, page_table, lens,
+                                                first, tokens, counts, stream)
+    if type(got) is int:
+        raise B2BError(got, "b2b_cache_compact")
+
+
 def get_cache_error():
     """(status, info[4]) of the decoder-block operators' error word; reads and clears it
     (synchronises; b2b_get_cache_error)."""

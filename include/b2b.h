@@ -317,10 +317,72 @@ b2b_status b2b_cache_attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, 
                                const float* slopes, void* out, void* workspace,
                                int64_t workspace_bytes, void* stream);
 
+/* The attention of drafted trees: b2b_cache_attention with another rule for who sees whom.  Row t of
+ * sequence s sees every older token (positions below lens[s] - n) and, of the sequence's n new
+ * tokens, token i if bit i % 64 of masks[t][i / 64] is set: usually its ancestors in the tree and
+ * itself, but any set will do, an empty one too (a row that sees no key at all is zero); bits from n on
+ * are ignored.  masks: device uint64 [T][mask_words], mask_words * 64 >= max_new.  positions: device
+ * int32 [T], the position of each new token for the distance bias (a token's depth in the tree, counted
+ * from lens[s] - n), or NULL: its slot's.  Older tokens have their slots' positions.  The rest as there,
+ * with a workspace of its own size. */
+b2b_status b2b_cache_tree_attention_workspace(const b2b_cache* cache, int64_t T, int32_t q_heads,
+                                              int64_t* bytes);
+b2b_status b2b_cache_tree_attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, const void* q,
+                                    int64_t ldq, int32_t q_heads, const uint64_t* masks,
+                                    int32_t mask_words, const int32_t* positions, float scale,
+                                    float softcap, const float* slopes, void* out, void* workspace,
+                                    int64_t workspace_bytes, void* stream);
+
+/* The page table of a step's sequences, from the last step's: sequences go on, branch off others
+ * (sharing their pages), end, lose their last tokens and get room for new ones.
+ *   Row r of the new table follows row parents[r] of page_table [batch][max_pages] (-1: an empty
+ *   sequence; parents NULL: row r follows row r, rows = batch or 0) for its first kept[r] tokens (NULL: all
+ *   lens[parent]) and has room for fresh[r] more (NULL: none):
+ *   table_out [rows][max_pages], -1 past that room; lens_out[r] = kept + fresh, as an append wants it.
+ * Nothing is kept between calls: a page of the pool is free if no new row keeps it, so rows that
+ * nobody follows are freed, and a table has to name every sequence whose pages are to stay.  A row
+ * with new tokens whose kept ones end inside a page writes on that page.  If every row that keeps the
+ * page does so, the lowest of them goes on in it; the others, or all if some row only reads it, get a
+ * page of their own: copies[r] = {from, to, tokens} names the copy that b2b_cache_copy has to make
+ * before the append ({-1, -1, 0}: none).  Pages are given out in the order of their numbers, to the
+ * rows in the order of theirs, to a row in the order of its positions; pages that are copied from are
+ * not given out.  left[0] = the pages that are still free; below 0, so many were missing: the last
+ * rows' entries are then -1 (the append and the attention record an error for those and follow none).
+ * A parent, length or kept page out of range is recorded (b2b_get_cache_error) and cut down.
+ * Outputs overlap neither the inputs nor one another (B2B_ERR_UNSUPPORTED).  rows up to 4096.
+ * workspace: of b2b_cache_pages_workspace's bytes (0 for pools of up to 327680 pages), as for the
+ * attention. */
+b2b_status b2b_cache_pages_workspace(int64_t pages, int32_t rows, int64_t* bytes);
+b2b_status b2b_cache_pages(int32_t page_size, int64_t pages, int32_t batch, int32_t max_pages,
+                           const int32_t* page_table, const int32_t* lens, int32_t rows,
+                           const int32_t* parents, const int32_t* kept, const int32_t* fresh,
+                           int32_t* table_out, int32_t* lens_out, int32_t* copies, int32_t* left,
+                           void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Copies the first `tokens` tokens of page `from` to page `to`, keys, values and both scales of every
+ * head, for each of the n rows {from, to, tokens} of copies (device int32 [n][3]).  A row with a
+ * negative page number, with no tokens, or with from = to copies nothing; what lies behind the tokens
+ * stays.  No page is written by two rows, or read by one and written by another, of one call.  Of
+ * cache, only the pool's fields are used. */
+b2b_status b2b_cache_copy(const b2b_cache* cache, int64_t n, const int32_t* copies, void* stream);
+
+/* Moves the tokens that each sequence keeps together, in place: token tokens[s][i], i < counts[s], of
+ * sequence s goes to position first[s] + i (its own or a lower one: tokens [batch][max_tokens] ascend
+ * from first[s] on, below lens[s]); the tokens below first[s] stay, and the sequence then has
+ * first[s] + counts[s].  An accepted path of drafted tokens: first = lens - n, tokens its nodes.  An
+ * eviction: first = 0, tokens all that stay.  A page that receives tokens takes the largest scale s'
+ * of the pages that its tokens come from (its own among them if it keeps some), and codes of a
+ * smaller scale s become e4m3(code * (s / s')), in fp32, to nearest even; others are moved as they are.
+ * Slots past the sequence's new end are unspecified.  Pages that are written belong to one sequence.
+ * Of cache, the pool, page_table and lens are used.  A second call moves tokens again. */
+b2b_status b2b_cache_compact(const b2b_cache* cache, const int32_t* first, const int32_t* tokens,
+                             int32_t max_tokens, const int32_t* counts, void* stream);
+
 /* Reads and clears these operators' error word on the current device (synchronises it):
  * B2B_OK, B2B_ERR_SHAPE for a position outside the rotary table (info[2] = 1), a page number
  * outside the pool (2), a length below its new tokens or above its page table (3) or starts
- * that decrease, leave the T rows or exceed max_new (4), B2B_ERR_TIMEOUT for a wait given up.
+ * that decrease, leave the T rows or exceed max_new (4), a parent outside the page table (5), a kept
+ * token outside its sequence or out of order (6), B2B_ERR_TIMEOUT for a wait given up.
  * info[1] = kernel, info[3] = sequence (rotary: row).  info may be NULL. */
 b2b_status b2b_get_cache_error(uint32_t info[4]);
 
