@@ -136,21 +136,6 @@ constexpr int attend_smem() {
          (NT > 1 ? D / 16 * NT * 256 : 0) + NT * 8 * 4;
 }
 
-// Which of the 16 tokens from the new token `off` on a row of a tree sees, as bits: its mask's, and
-// every older token (off < 0, above -16).  Nothing at or past the n new ones (off < n).
-__device__ __forceinline__ uint32_t tree_window(const uint32_t* mask, int words, int off, int n) {
-  uint32_t w;
-  if (off < 0) {
-    w = (mask[0] << -off) | ((1u << -off) - 1u);
-  } else {
-    const int i = off >> 5, sh = off & 31;
-    w = mask[i] >> sh;
-    if (sh > 16 && i + 1 < words) w |= mask[i + 1] << (32 - sh);
-  }
-  const int left = n - off;
-  return w & (left < 16 ? (1u << left) - 1u : 0xFFFFu);
-}
-
 // MODS: capped or biased scores.  F16: fp16 queries and outputs, else bf16.  TREE: new tokens are seen
 // by the rows whose masks name them, else by their own and the later rows of the sequence.
 template <int D, int NT, bool MODS, bool F16, bool TREE>

@@ -161,6 +161,8 @@ __device__ __forceinline__ float exponent_of(float scale) {
 struct PromptUnit {
   Sequence s;
   int b, h, row0, rows, start, kv_end, tiles, row_tiles;
+  int t0;                              // trees: the piece's first key tile (tiles: how many),
+  int slot;                            // and where its part goes, -1: the unit is not cut
 };
 
 // Row tile rt of sequence b, for kv head h; false where the sequence has no such rows.
@@ -177,6 +179,57 @@ __device__ __forceinline__ bool prompt_unit(const AttendParams& p, int b, int h,
   u.start = u.s.len - u.s.n;
   u.kv_end = u.start + last / p.group + 1;
   u.tiles = (u.kv_end + kPromptKeys - 1) / kPromptKeys;
+  u.row_tiles = u.rows - u.row0 > 128 ? 2 : 1;
+  return true;
+}
+
+// Drafted trees.  All rows of a sequence see its older tokens, few of them new ones, so that a
+// sequence's units all walk the same key tiles, and one sequence may have nearly all of them.  Units of
+// more than L key tiles are cut into equal pieces of at most L, with a CTA each, and a further kernel
+// joins their parts; L is what an even share of all key tiles over the SMs comes to, at least
+// kMinPieceTiles.  A small kernel ahead writes the pieces down from the lengths.
+constexpr int kMinPieceTiles = 4;
+// The most new tokens of a sequence: what some rows see and others do not has to fit kEdgeTokens.
+constexpr int kMostTreeTokens = kEdgeTokens - kPromptKeys;
+
+struct TreePiece {
+  int b, h, rt, slot, t0, t1, pad[2];
+};
+// The workspace: [count of pieces, 3 unused], the pieces, per sequence {first slot, pieces of a unit},
+// the parts (256 rows of D sums, then 256 log2 sums, fp32).
+struct TreePlan {
+  int32_t* count;
+  TreePiece* pieces;
+  int2* cuts;
+  float* parts;
+};
+__host__ __device__ inline int64_t tree_plan_bytes(int64_t pieces, int64_t B) {
+  return 16 + pieces * static_cast<int64_t>(sizeof(TreePiece)) + (B + 1) / 2 * 16;
+}
+__host__ __device__ inline TreePlan tree_plan(void* workspace, int64_t pieces, int64_t B) {
+  TreePlan t;
+  char* at = static_cast<char*>(workspace);
+  t.count = reinterpret_cast<int32_t*>(at);
+  t.pieces = reinterpret_cast<TreePiece*>(at + 16);
+  t.cuts = reinterpret_cast<int2*>(at + 16 + pieces * static_cast<int64_t>(sizeof(TreePiece)));
+  t.parts = reinterpret_cast<float*>(at + tree_plan_bytes(pieces, B));
+  return t;
+}
+
+// The piece that CTA `i` works on; false where there are fewer.
+__device__ __forceinline__ bool tree_unit(const AttendParams& p, const TreePlan& plan, int i, PromptUnit& u) {
+  if (i >= *plan.count) return false;
+  const TreePiece piece = plan.pieces[i];
+  u.b = piece.b;
+  u.h = piece.h;
+  u.s = load_sequence(p.c, u.b, DK_PROMPT);
+  u.row0 = piece.rt * kPromptRows;
+  u.rows = u.s.n * p.group;
+  u.start = u.s.len - u.s.n;
+  u.kv_end = u.s.len;
+  u.t0 = piece.t0;
+  u.tiles = piece.t1 - piece.t0;
+  u.slot = piece.slot;
   u.row_tiles = u.rows - u.row0 > 128 ? 2 : 1;
   return true;
 }
@@ -264,7 +317,7 @@ struct PromptProducer {
   }
 };
 
-template <int D, bool MODS>
+template <int D, bool MODS, bool TREE>
 __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendParams p,
                                                                    int row_tiles) {
   using L = PromptSmem<D>;
@@ -282,12 +335,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
     int order = static_cast<int>(blockIdx.x) / p.c.heads;
     grid_launch_dependents();
     grid_dependency_wait();                                // launched early
-    if (p.meta != nullptr) {
-      order = static_cast<int>(p.meta[order]);
+    if constexpr (TREE) {
+      const TreePlan plan = tree_plan(p.meta, gridDim.x, p.c.B);
+      if (!tree_unit(p, plan, static_cast<int>(blockIdx.x), u)) return;                // the whole CTA
+    } else {
+      if (p.meta != nullptr) {
+        order = static_cast<int>(p.meta[order]);
+      }
+      plain_pair(p, row_tiles, order, b, rt);
+      if (!prompt_unit(p, b, static_cast<int>(blockIdx.x) % p.c.heads, rt, u)) return; // the whole CTA
     }
-    plain_pair(p, row_tiles, order, b, rt);
-    if (!prompt_unit(p, b, static_cast<int>(blockIdx.x) % p.c.heads, rt, u)) return;   // the whole CTA
   }
+  const int first_tile = TREE ? u.t0 : 0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -321,7 +380,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
                                              p.c.err, DK_PROMPT, site, blockIdx.x));
   };
   // first token that some row of the CTA does not see, down to its tile
-  const int edge0 = (u.start + u.row0 / p.group + 1) / kPromptKeys * kPromptKeys;
+  const int edge0 = (TREE ? u.start : u.start + u.row0 / p.group + 1) / kPromptKeys * kPromptKeys;
 
   if (warp < 8) {
     more_registers<kSoftmaxRegs>();
@@ -379,15 +438,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->qfull[t]));
 
-      const int limit = valid ? u.start + tq : 0x7FFFFFFF;
-      const int low_limit = u.start + (u.row0 + 128 * t) / p.group;
+      // the last token that the row sees; of a tree's, the position for the distance bias
+      int limit = valid ? u.start + tq : 0x7FFFFFFF;
+      if (TREE && MODS && p.positions != nullptr)
+        limit = p.positions[u.s.row + static_cast<int64_t>(tq)];
+      const int low_limit = TREE ? u.start - 1 : u.start + (u.row0 + 128 * t) / p.group;
+      // which of the 16 tokens from `tok` on the row sees
+      const uint32_t* mask = TREE ? p.masks + (u.s.row + static_cast<int64_t>(tq)) * p.mask_words : nullptr;
+      auto window = [&](int tok) -> uint32_t {
+        const int off = tok - u.start;
+        if (off <= -kGranule) return 0xFFFFu;
+        return off < u.s.n ? tree_window(mask, p.mask_words, off, u.s.n) : 0u;
+      };
       const float slope = MODS && p.slopes != nullptr && valid ? p.slopes[head] : 0.f;
       float m = -1e30f, l = 0.f;                   // m: the reference of z + log2 value scale
       bool ok = true;
 
       for (int i = 0; i < u.tiles && ok; ++i) {
         const float2* sc = scales + (i & 3) * kGranules;
-        const int tok0 = i * kPromptKeys;
+        const int tok0 = (first_tile + i) * kPromptKeys;
         const bool edge = tok0 + kPromptKeys - 1 > low_limit;
         ok = wait(&bars->sfull[t], i & 1, PS_SFULL);
         if (!ok) break;
@@ -399,7 +468,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
           float z = __uint_as_float(raw) * f;
           if (MODS) {
             if (p.softcap > 0.f) z = capped(z, p.softcap, p.inv_softcap);
-            z = fmaf(slope, static_cast<float>(tok - limit), z) * kLog2e;
+            int at = tok;
+            if (TREE && edge && p.positions != nullptr && tok >= u.start && tok < u.kv_end)
+              at = p.positions[u.s.row + static_cast<int64_t>(tok - u.start)];
+            z = fmaf(slope, static_cast<float>(at - limit), z) * kLog2e;
           }
           return z;
         };
@@ -417,10 +489,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
             uint32_t* x = &r[16 * g];
             float most = -INFINITY;                  // of the granule's tokens that the row sees
             if constexpr (SCORES) {
+              const uint32_t sees = TREE ? window(tok0 + 32 * q + 16 * g) : 0u;
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const int tok = tok0 + 32 * q + 16 * g + e;
-                const float z = tok > limit ? -INFINITY : score(x[e], f, tok);
+                const bool hidden = TREE ? ((sees >> e) & 1u) == 0u : tok > limit;
+                const float z = hidden ? -INFINITY : score(x[e], f, tok);
                 x[e] = __float_as_uint(z);
                 most = fmaxf(most, z);
               }
@@ -464,7 +538,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
             const float2 s2 = sc[2 * q + g];
             const float fg = SCORES ? 1.f : fac * s2.x;
             // (a page that the row does not reach may have any scale, a NaN too)
-            const bool past = SCORES && tok0 + 32 * q + 16 * g > limit;
+            const bool past = SCORES && (TREE ? window(tok0 + 32 * q + 16 * g) == 0u
+                                              : tok0 + 32 * q + 16 * g > limit);
             const float back = past ? 0.f : exp2_fast(-s2.y), c = past ? 0.f : s2.y - m;
             const float2 f2 = make_float2(fg, fg), c2 = make_float2(c, c);
             float2 sum = make_float2(0.f, 0.f);
@@ -531,6 +606,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       if (ok && wait(&bars->ofull[t], 0, PS_OFULL)) {
         tc_fence_after_sync();
         const float inv = l == 0.f || l > kNoValues ? 0.f : 1.f / l;
+        float* part = nullptr;
+        if (TREE && u.slot >= 0) {
+          part = tree_plan(p.meta, gridDim.x, p.c.B).parts +
+                 static_cast<int64_t>(u.slot) * (kPromptRows * (D + 1));
+          if (valid) part[kPromptRows * D + row - u.row0] = l == 0.f ? -1e30f : m + log2f(l);
+          part += static_cast<int64_t>(row - u.row0) * D;
+        }
         const int tq_out = valid ? tq : 0;
         uint16_t* dst = p.out + ((u.s.row + static_cast<int64_t>(tq_out)) * p.q_heads + head) * D;
         const bool nans = bars->nan_any != 0u;
@@ -540,9 +622,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
           tmem_load32(tm + o_col + 32 * q, r);
           tmem_wait32(r);
           uint32_t bad = 0u;
-          if (nans)
-            for (int tok = edge0; tok <= limit && tok < u.kv_end; ++tok)
+          if (nans) {
+            for (int tok = edge0; (TREE || tok <= limit) && tok < u.kv_end; ++tok) {
+              if (TREE && tok >= u.start && (window(tok) & 1u) == 0u) continue;
               bad |= nan_bits[(tok - edge0) * (D / 32) + q];
+            }
+          }
           if (valid) {
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
@@ -552,7 +637,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
                 o[k] = inv == 0.f ? 0.f : __uint_as_float(r[e + k]) * inv;
                 if ((bad >> (e + k)) & 1u) o[k] = __uint_as_float(0x7FC00000u);
               }
-              *reinterpret_cast<uint4*>(dst + 32 * q + e) = p.is_bf16 ? narrow8<true>(o) : narrow8<false>(o);
+              if (TREE && part != nullptr) {
+                *reinterpret_cast<float4*>(part + 32 * q + e) = make_float4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<float4*>(part + 32 * q + e + 4) = make_float4(o[4], o[5], o[6], o[7]);
+              } else {
+                *reinterpret_cast<uint4*>(dst + 32 * q + e) = p.is_bf16 ? narrow8<true>(o) : narrow8<false>(o);
+              }
             }
           }
         }
@@ -576,10 +666,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       const int64_t at = static_cast<int64_t>(id) * p.c.heads + u.h;
       return make_float2(p.c.k_scale[at], p.c.v_scale[at]);
     };
-    prod.locate(p, u, 0);
-    prod.fetch(p, u, 0, p.c.k, raw);
-    float2 s2 = scales_of(0, prod.page);
-    prod.locate(p, u, 1);
+    prod.locate(p, u, first_tile);
+    prod.fetch(p, u, first_tile, p.c.k, raw);
+    float2 s2 = scales_of(first_tile, prod.page);
+    prod.locate(p, u, first_tile + 1);
     bool ok = true;
     for (int i = 0; i < u.tiles && ok; ++i) {
       const int slot = i & 1;
@@ -591,9 +681,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->kfull[slot]));
       if (i + 1 < u.tiles) {
-        prod.fetch(p, u, i + 1, p.c.k, raw);
-        s2 = scales_of(i + 1, prod.page);
-        prod.locate(p, u, i + 2);
+        prod.fetch(p, u, first_tile + i + 1, p.c.k, raw);
+        s2 = scales_of(first_tile + i + 1, prod.page);
+        prod.locate(p, u, first_tile + i + 2);
       }
     }
   } else if (warp < 16) {
@@ -603,20 +693,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
     prod.tid = threadIdx.x - 384;
     constexpr int kEach = PromptProducer<D>::kEach;
     uint4 raw[kEach];
-    prod.locate(p, u, 0);
-    prod.fetch(p, u, 0, p.c.v, raw);
-    prod.locate(p, u, 1);
+    prod.locate(p, u, first_tile);
+    prod.fetch(p, u, first_tile, p.c.v, raw);
+    prod.locate(p, u, first_tile + 1);
     bool ok = true;
     for (int i = 0; i < u.tiles && ok; ++i) {
       const int slot = i & 1;
       if (i >= 2) ok = wait(&bars->vempty[slot], ((i >> 1) - 1) & 1, PS_VEMPTY);
       if (!ok) break;
-      if (i * kPromptKeys >= edge0) {
+      const int tile = first_tile + i;
+      if (tile * kPromptKeys >= edge0) {
         // Slots past every row's reach may hold anything: taken as zeros.  A NaN that only some rows
         // see comes out of the product too (0 * NaN is one) and is noted for the rows that see it.
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
-          if (i * kPromptKeys + prod.token(j) >= u.kv_end) raw[j] = make_uint4(0u, 0u, 0u, 0u);
+          if (tile * kPromptKeys + prod.token(j) >= u.kv_end) raw[j] = make_uint4(0u, 0u, 0u, 0u);
           uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
           uint32_t any = 0u;
 #pragma unroll
@@ -630,7 +721,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
                 w[e / 4] &= ~(0xFFu << (8 * (e % 4)));
               }
             raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
-            const int at = i * kPromptKeys + prod.token(j);
+            const int at = tile * kPromptKeys + prod.token(j);
             if (at - edge0 < kEdgeTokens && prod.piece() < PromptProducer<D>::kPieces) {
               atomicOr(&nan_bits[(at - edge0) * (D / 32) + prod.piece() / 2],
                        bits << (16 * (prod.piece() & 1)));
@@ -644,8 +735,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->vfull[slot]));
       if (i + 1 < u.tiles) {
-        prod.fetch(p, u, i + 1, p.c.v, raw);
-        prod.locate(p, u, i + 2);
+        prod.fetch(p, u, first_tile + i + 1, p.c.v, raw);
+        prod.locate(p, u, first_tile + i + 2);
       }
     }
   } else {
@@ -714,12 +805,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
   }
 }
 
-template <int D>
-cudaError_t launch_prompt_d(const AttendParams& p, int row_tiles, cudaStream_t s) {
+// `ctas`: one per unit, or for drafted trees at least one per piece.
+template <int D, bool TREE>
+cudaError_t launch_prompt_d(const AttendParams& p, int row_tiles, int64_t ctas, cudaStream_t s) {
   constexpr int smem = PromptSmem<D>::kAlloc;
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
   const bool mods = p.softcap > 0.f || p.slopes != nullptr;
-  auto* fn = mods ? prompt_kernel<D, true> : prompt_kernel<D, false>;
+  auto* fn = mods ? prompt_kernel<D, true, TREE> : prompt_kernel<D, false, TREE>;
   static thread_local int set_on[2] = {-1, -1};
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
@@ -729,8 +821,7 @@ cudaError_t launch_prompt_d(const AttendParams& p, int row_tiles, cudaStream_t s
     if (e != cudaSuccess) return e;
     set_on[mods] = dev;
   }
-  return launch_early(fn, static_cast<int64_t>(row_tiles) * p.c.heads * p.c.B, kPromptThreads, smem, s,
-                      p, row_tiles);
+  return launch_early(fn, ctas, kPromptThreads, smem, s, p, row_tiles);
 }
 
 }  // namespace b2b

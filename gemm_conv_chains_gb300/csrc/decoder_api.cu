@@ -207,9 +207,13 @@ SplitChoice split_of(const b2b_cache* c, int32_t q_heads, bool tree, int num_sms
   const int64_t pieces = (rows + 8 * s.nt - 1) / (8 * s.nt) * c->heads * c->batch;
   const int64_t runs = s.whole ? pieces : pieces * ((most / 64 + kMinTiles - 1) / kMinTiles);
   if (runs < s.grid) s.grid = static_cast<int>(runs);
-  s.prompt = !tree && prompt_pays(c->head_dim, rows, static_cast<int64_t>(c->batch) * c->heads,
-                                  most <= 512, num_sms);
-  s.bytes = s.prompt  ? prompt_workspace(rows, c->batch)
+  const CacheView view = view_of(c, 0, nullptr);
+  // (drafted trees, D = 128, 32 query heads on 8: 1 sequence, 64 nodes over 32000 cached 58 us for the split
+  // kernel's 171; 300 cached 23 for 16; 32 sequences, 16 nodes (64 rows) over up to 4000 143 for 127)
+  s.prompt = tree ? tree_fits(view) && rows > 64 && most > 1024
+                  : prompt_pays(c->head_dim, rows, static_cast<int64_t>(c->batch) * c->heads, most <= 512,
+                                num_sms);
+  s.bytes = s.prompt  ? (tree ? tree_workspace(rows, view, num_sms) : prompt_workspace(rows, c->batch))
             : s.whole ? 0
                     : 16 * ((static_cast<int64_t>(c->batch) + 4) / 4) +
                           static_cast<int64_t>(s.grid) * 2 * s.nt * 8 * (c->head_dim + 1) * 4;
@@ -298,7 +302,7 @@ b2b_status attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, const void
                                                16 * ((static_cast<int64_t>(cache->batch) + 4) / 4));
   p.wait_limit_ns = kDecoderWaitNs;
   auto s = static_cast<cudaStream_t>(stream);
-  if (sc.prompt) return launched(launch_prompt(p, s));
+  if (sc.prompt) return launched(tree != nullptr ? launch_tree(p, d->num_sms, s) : launch_prompt(p, s));
   cudaError_t e = cudaErrorInvalidValue;
   switch (cache->head_dim) {
     case 64: e = (tree != nullptr ? launch_attend_tree_64 : launch_attend_64)(sc.nt, p, s); break;

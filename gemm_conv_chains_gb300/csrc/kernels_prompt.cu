@@ -34,7 +34,8 @@ int64_t prompt_workspace(int64_t rows, int32_t B) {
 cudaError_t launch_prompt(const AttendParams& p, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.c.max_new) * p.group;
   const int64_t row_tiles = (rows + kPromptRows - 1) / kPromptRows;
-  if (row_tiles * p.c.heads * p.c.B > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  const int64_t ctas = row_tiles * p.c.heads * p.c.B;
+  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   if (p.meta != nullptr) {
     if (cudaError_t e = launch_early(prompt_order_kernel, 1, kRankedPairs, 0, s, p,
                                      static_cast<int>(row_tiles), reinterpret_cast<int*>(p.meta));
@@ -42,9 +43,9 @@ cudaError_t launch_prompt(const AttendParams& p, cudaStream_t s) {
       return e;
   }
   switch (p.c.D) {
-    case 64: return launch_prompt_d<64>(p, static_cast<int>(row_tiles), s);
-    case 96: return launch_prompt_d<96>(p, static_cast<int>(row_tiles), s);
-    case 128: return launch_prompt_d<128>(p, static_cast<int>(row_tiles), s);
+    case 64: return launch_prompt_d<64, false>(p, static_cast<int>(row_tiles), ctas, s);
+    case 96: return launch_prompt_d<96, false>(p, static_cast<int>(row_tiles), ctas, s);
+    case 128: return launch_prompt_d<128, false>(p, static_cast<int>(row_tiles), ctas, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -1,0 +1,157 @@
+// kernels_tree.cu -- the tcgen05 cache attention for wide drafted trees, head sizes 64, 96 and 128, and
+// the plan of its pieces.
+#include "cache_prompt.cuh"
+
+namespace b2b {
+namespace {
+
+constexpr int kPlanThreads = 256;
+
+struct TreeWork {
+  int units, tiles;                    // units of the sequence, and the key tiles of each
+};
+__device__ __forceinline__ TreeWork tree_work(const AttendParams& p, int b, int& row_tiles) {
+  const Sequence s = load_sequence(p.c, b, DK_PROMPT);
+  row_tiles = (s.n * p.group + kPromptRows - 1) / kPromptRows;
+  return TreeWork{p.c.heads * row_tiles, (s.len + kPromptKeys - 1) / kPromptKeys};
+}
+
+// Every block sums all sequences up and writes down its share of the pieces.
+__global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const AttendParams p, int64_t most, int num_sms,
+                                                                 int cut) {
+  __shared__ unsigned long long sums[kPlanThreads / 32];
+  __shared__ int piece_at[kPlanThreads + 1], slot_at[kPlanThreads], count_of[kPlanThreads], rows_of[kPlanThreads];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const TreePlan plan = tree_plan(p.meta, most, p.c.B);
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  // ---- the longest piece ----
+  int row_tiles;
+  int length = 0x7FFFFFFF;
+  if (cut) {
+    unsigned long long total = 0;
+    for (int b = t; b < p.c.B; b += kPlanThreads) {
+      const TreeWork w = tree_work(p, b, row_tiles);
+      total += static_cast<unsigned long long>(w.units) * w.tiles;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) sums[warp] = total;
+    __syncthreads();
+    total = 0;
+    for (int i = 0; i < kPlanThreads / 32; ++i) total += sums[i];
+    const unsigned long long share = (total + num_sms - 1) / num_sms;
+    length = share < kMinPieceTiles ? kMinPieceTiles : share > 0x7FFFFFFF ? 0x7FFFFFFF : static_cast<int>(share);
+    __syncthreads();
+  }
+  // ---- 256 sequences at a time: where their pieces and slots begin ----
+  int pieces = 0, slots = 0;
+  for (int b0 = 0; b0 < p.c.B; b0 += kPlanThreads) {
+    const int b = b0 + t;
+    int units = 0, per_unit = 0, tiles = 0;
+    row_tiles = 0;
+    if (b < p.c.B) {
+      const TreeWork w = tree_work(p, b, row_tiles);
+      units = w.units;
+      tiles = w.tiles;
+      per_unit = units > 0 ? (tiles - 1) / length + 1 : 0;
+    }
+    const int mine = units * per_unit, cut_here = per_unit > 1 ? mine : 0;
+    unsigned long long upto = static_cast<unsigned long long>(mine) | static_cast<unsigned long long>(cut_here) << 32;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    unsigned long long ahead = 0, all = 0;
+    for (int i = 0; i < kPlanThreads / 32; ++i) {
+      ahead += i < warp ? sums[i] : 0ull;
+      all += sums[i];
+    }
+    upto += ahead;
+    const int first_slot = slots + static_cast<int>(upto >> 32) - cut_here;
+    piece_at[t] = pieces + static_cast<int>(upto & 0xFFFFFFFFu) - mine;
+    slot_at[t] = per_unit > 1 ? first_slot : -1;
+    count_of[t] = per_unit;
+    rows_of[t] = tiles;
+    if (t == 0) piece_at[kPlanThreads] = pieces + static_cast<int>(all & 0xFFFFFFFFu);
+    if (blockIdx.x == 0 && b < p.c.B) plan.cuts[b] = make_int2(first_slot, per_unit);
+    __syncthreads();
+    // ---- their pieces ----
+    const int end = piece_at[kPlanThreads];
+    for (int i = pieces + static_cast<int>(blockIdx.x) * kPlanThreads + t; i < end;
+         i += static_cast<int>(gridDim.x) * kPlanThreads) {
+      int a = 0, z = kPlanThreads - 1;               // the last sequence whose first piece is at most i
+      while (a < z) {
+        const int mid = (a + z + 1) / 2;
+        if (piece_at[mid] <= i) a = mid;
+        else z = mid - 1;
+      }
+      const int n = count_of[a], k = i - piece_at[a], unit = k / n, at = k - unit * n;
+      TreePiece piece;
+      piece.b = b0 + a;
+      piece.h = unit % p.c.heads;
+      piece.rt = unit / p.c.heads;
+      piece.slot = -1;
+      if (slot_at[a] >= 0) {
+        const int row_tiles_a = (piece_at[a + 1] - piece_at[a]) / (n * p.c.heads);
+        piece.slot = slot_at[a] + (piece.h * row_tiles_a + piece.rt) * n + at;
+      }
+      piece.t0 = static_cast<int>(static_cast<int64_t>(rows_of[a]) * at / n);
+      piece.t1 = static_cast<int>(static_cast<int64_t>(rows_of[a]) * (at + 1) / n);
+      piece.pad[0] = piece.pad[1] = 0;
+      if (i < most) plan.pieces[i] = piece;
+    }
+    pieces = end;
+    slots += static_cast<int>(all >> 32);
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && t == 0) *plan.count = pieces < most ? pieces : static_cast<int>(most);
+}
+
+struct TreeShape {
+  int64_t pieces, slots;               // at most
+  bool cut;
+};
+// With many units there is little to gain from cutting them.
+TreeShape tree_shape(int64_t rows, const CacheView& c, int num_sms) {
+  TreeShape s;
+  const int64_t units = (rows + kPromptRows - 1) / kPromptRows * c.heads * c.B;
+  const int64_t tiles = ((static_cast<int64_t>(c.max_pages) << c.page_shift) + kPromptKeys - 1) / kPromptKeys;
+  s.cut = units < 4 * num_sms && tiles > kMinPieceTiles;
+  // pieces of at most L tiles, L >= all tiles / SMs: fewer than SMs besides one per unit, and fewer
+  // than 2 SMs in units that are cut
+  s.pieces = units + (s.cut ? num_sms : 0);
+  s.slots = s.cut ? 2 * static_cast<int64_t>(num_sms) : 0;
+  return s;
+}
+
+}  // namespace
+
+int64_t tree_workspace(int64_t rows, const CacheView& c, int num_sms) {
+  const TreeShape s = tree_shape(rows, c, num_sms);
+  return tree_plan_bytes(s.pieces, c.B) + s.slots * kPromptRows * (c.D + 1) * 4;
+}
+bool tree_fits(const CacheView& c) { return c.D <= 128 && c.max_new <= kMostTreeTokens; }
+
+cudaError_t launch_tree(const AttendParams& p, int num_sms, cudaStream_t s) {
+  const int64_t rows = static_cast<int64_t>(p.c.max_new) * p.group;
+  const TreeShape shape = tree_shape(rows, p.c, num_sms);
+  if (shape.pieces > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  const int64_t plan_blocks = (shape.pieces + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  cudaError_t e = launch_early(tree_plan_kernel, plan_blocks, kPlanThreads, 0, s, p, shape.pieces, num_sms,
+                               shape.cut ? 1 : 0);
+  if (e != cudaSuccess) return e;
+  switch (p.c.D) {
+    case 64: e = launch_prompt_d<64, true>(p, 0, shape.pieces, s); break;
+    case 96: e = launch_prompt_d<96, true>(p, 0, shape.pieces, s); break;
+    case 128: e = launch_prompt_d<128, true>(p, 0, shape.pieces, s); break;
+    default: return cudaErrorInvalidValue;
+  }
+  if (e != cudaSuccess || !shape.cut) return e;
+  return launch_tree_join(p, shape.pieces, num_sms, s);
+}
+
+}  // namespace b2b
