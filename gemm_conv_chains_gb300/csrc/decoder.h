@@ -93,7 +93,8 @@ struct PagesParams {
   int32_t* lens_out;          // [rows]
   int32_t* copies;            // [rows][3]
   int32_t* left;              // [1]
-  uint32_t* owners;           // [pages], or null: in shared memory
+  uint32_t* owners;           // [pages] in the workspace
+  void* kept_rows;            // [rows] of 16 bytes there
   int64_t pages;
   int32_t B, width, rows, page_shift;
   uint32_t* err;
@@ -174,9 +175,9 @@ cudaError_t launch_tree_join(const AttendParams& p, int64_t pieces, int num_sms,
 cudaError_t launch_attend_combine(const AttendParams& p, int nt, int num_sms, cudaStream_t s);
 
 // Bytes of workspace that the page table's kernel takes, and the most rows that it does.
-int64_t pages_workspace(int64_t pages);
+int64_t pages_workspace(int64_t pages, int64_t rows);
 constexpr int32_t kMostPageRows = 4096;
-cudaError_t launch_pages(const PagesParams& p, cudaStream_t s);
+cudaError_t launch_pages(PagesParams p, void* workspace, int num_sms, cudaStream_t s);
 cudaError_t launch_copy(const CopyParams& p, int num_sms, cudaStream_t s);
 cudaError_t launch_compact(const CompactParams& p, int num_sms, cudaStream_t s);
 

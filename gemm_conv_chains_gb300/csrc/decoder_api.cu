@@ -482,7 +482,7 @@ b2b_status b2b_cache_pages_workspace(int64_t pages, int32_t rows, int64_t* bytes
   if (bytes == nullptr) return B2B_ERR_NULL;
   *bytes = 0;
   if (b2b_status st = check_pages(pages, rows); st != B2B_OK) return st;
-  *bytes = pages_workspace(pages);
+  *bytes = pages_workspace(pages, rows);
   return B2B_OK;
 }
 
@@ -507,7 +507,7 @@ b2b_status b2b_cache_pages(int32_t page_size, int64_t pages, int32_t batch, int3
   if (!aligned(workspace, 16)) return B2B_ERR_ALIGN;
   // nothing that is written lies over what is read, or over another output
   const int64_t n = rows;
-  const int64_t bytes = pages_workspace(pages);
+  const int64_t bytes = pages_workspace(pages, rows);
   const void* read[5] = {page_table, lens, parents, kept, fresh};
   const int64_t read_bytes[5] = {4 * in, 4 * static_cast<int64_t>(batch), 4 * n, 4 * n, 4 * n};
   const void* written[5] = {table_out, lens_out, copies, left, bytes > 0 ? workspace : nullptr};
@@ -532,14 +532,15 @@ b2b_status b2b_cache_pages(int32_t page_size, int64_t pages, int32_t batch, int3
   p.lens_out = lens_out;
   p.copies = copies;
   p.left = left;
-  p.owners = bytes > 0 ? static_cast<uint32_t*>(workspace) : nullptr;
+  p.owners = nullptr;
+  p.kept_rows = nullptr;
   p.pages = pages;
   p.B = batch;
   p.width = max_pages;
   p.rows = rows;
   p.page_shift = __builtin_ctz(static_cast<unsigned>(page_size));
   p.err = d->err;
-  return launched(launch_pages(p, static_cast<cudaStream_t>(stream)));
+  return launched(launch_pages(p, workspace, d->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 b2b_status b2b_cache_copy(const b2b_cache* cache, int64_t n, const int32_t* copies, void* stream) {

@@ -592,7 +592,7 @@ def cache_pages(page_table, lens, pages, page_size, parents=None, kept=None, new
     cache_copy has to make before the append.  left: the free pages that remain, or minus those that
     were missing (their entries are -1).  out: the four results' tensors, none of them an input's
     memory (the tables of a program that keeps two and takes them in turn).  workspace: uint8, for
-    pools above 327680 pages; allocated when not given."""
+    more than 128 rows or pools above 40960 pages; allocated when not given."""
     if out is None:
         out = (None, None, None, None)
     else:

@@ -350,8 +350,8 @@ b2b_status b2b_cache_tree_attention(b2b_dtype dt, const b2b_cache* cache, int64_
  * rows' entries are then -1 (the append and the attention record an error for those and follow none).
  * A parent, length or kept page out of range is recorded (b2b_get_cache_error) and cut down.
  * Outputs overlap neither the inputs nor one another (B2B_ERR_UNSUPPORTED).  rows up to 4096.
- * workspace: of b2b_cache_pages_workspace's bytes (0 for pools of up to 327680 pages), as for the
- * attention. */
+ * workspace: of b2b_cache_pages_workspace's bytes (0 for up to 128 rows on a pool of up to 40960
+ * pages), as for the attention. */
 b2b_status b2b_cache_pages_workspace(int64_t pages, int32_t rows, int64_t* bytes);
 b2b_status b2b_cache_pages(int32_t page_size, int64_t pages, int32_t batch, int32_t max_pages,
                            const int32_t* page_table, const int32_t* lens, int32_t rows,

@@ -82,8 +82,9 @@ def test_pages_refusals(L, kw, expect):
 
 def test_pages_workspace(L):
     n = ctypes.c_int64(-1)
-    assert L.b2b_cache_pages_workspace(327680, 4, ctypes.byref(n)) == OK and n.value == 0
-    assert L.b2b_cache_pages_workspace(327681, 4, ctypes.byref(n)) == OK and n.value == 4 * 327681
+    assert L.b2b_cache_pages_workspace(40960, 128, ctypes.byref(n)) == OK and n.value == 0
+    assert L.b2b_cache_pages_workspace(40961, 4, ctypes.byref(n)) == OK and n.value == 163856 + 64
+    assert L.b2b_cache_pages_workspace(9, 129, ctypes.byref(n)) == OK and n.value == 48 + 129 * 16
     assert L.b2b_cache_pages_workspace(-1, 4, ctypes.byref(n)) == SHAPE
     assert L.b2b_cache_pages_workspace(5, 5000, ctypes.byref(n)) == UNSUP
     assert L.b2b_cache_pages_workspace(5, 4, None) == NULL

@@ -82,12 +82,13 @@ def test_steps(seed, B, rows, page, most, shared):
 
 
 def test_large_pools_and_wide_tables():
-    """Eight blocks of one cluster, the words in its shared memory and (the larger pool) outside."""
-    for pages, B, rows in ((327680, 60, 70), (327681, 60, 70), (1000003, 30, 1500), (45000, 200, 4096)):
+    """One block on a small pool; three kernels and a workspace on larger ones or for many rows."""
+    for pages, B, rows in ((40960, 60, 128), (40961, 60, 70), (1000003, 30, 1500), (45000, 200, 4096),
+                           (9000, 40, 129), (327680, 128, 128)):
         lens, width, parents, kept, new = _random_step(pages, B, rows, 16, 4000, 5, new=40)
         table = _table(lens, 16, width, pages, 1, 5)
         got = _check_pages(table, lens, pages, 16, width, parents, kept, new)
-        n = -(-pages // 4) * 16 if pages > 327680 else 0
+        n = -(-pages // 4) * 16 + 16 * rows if pages > 40960 or rows > 128 else 0
         if n:                                        # a workspace of the program's own, whatever it holds
             work = torch.full((n,), 0x11, dtype=torch.uint8, device="cuda")
             again = ops.cache_pages(_ints(table), _ints(lens), pages, 16, _ints(parents), _ints(kept),
@@ -296,7 +297,8 @@ def _check_compact(c, first, tokens, counts, stream=None):
     ([100, 0], [64, 40], [9, 40], 3, 96, 32), ([250, 3], [30, 200], [11, 77], 2, 128, 64),
     ([4, 0], [1500, 700], [600, 699], 2, 64, 16), ([4], [3000], [1111], 1, 128, 128),
     ([4, 9, 0], [900, 10, 0], [333, 10, 0], 2, 256, 256), ([0, 500], [5000, 3], [2500, 1], 1, 192, 32),
-    ([1], [9000], [4500], 1, 64, 64), ([60] * 90, [12] * 90, [1 + b % 12 for b in range(90)], 2, 64, 32),
+    ([1], [9000], [4500], 1, 64, 64), ([3], [9000], [6000], 1, 256, 256), ([0], [5000], [4100], 1, 96, 16),
+    ([60] * 90, [12] * 90, [1 + b % 12 for b in range(90)], 2, 64, 32),
 ])
 def test_compact(older, new, counts, heads, D, page):
     c = ref.Cache(older, new, heads, D, page, seed=D + page)
