@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas_per_sm(D, NT)) 
 #pragma unroll
             for (int i = 0; i < 2; ++i)
               window[nt][i] = tree_window(p.masks + (s.row + static_cast<int64_t>(limit[nt][i])) * p.mask_words,
-                                          p.mask_words, off, s.n);
+                                          1, p.mask_words, off, s.n);
           if (MODS && p.positions != nullptr) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {

@@ -69,6 +69,8 @@ struct PromptSmem {
   static constexpr int kBar = kNan + kEdgeTokens * (D / 32) * 4;
   static constexpr int kBytes = kBar + 256;
   static constexpr int kAlloc = kBytes + 1024;                  // the tiles start 1 KB aligned
+  static constexpr int kMasks = kBytes;                         // trees: [words][256 rows]
+  static constexpr int kTreeAlloc = kAlloc + (kEdgeTokens - kPromptKeys) / 32 * kPromptRows * 4;
 };
 
 struct PromptBars {
@@ -327,6 +329,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
   PromptBars* bars = reinterpret_cast<PromptBars*>(smem + L::kBar);
   float2* scales = reinterpret_cast<float2*>(smem + L::kScales);
   uint32_t* nan_bits = reinterpret_cast<uint32_t*>(smem + L::kNan);
+  [[maybe_unused]] uint32_t* masks = reinterpret_cast<uint32_t*>(smem + L::kMasks);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   PromptUnit u;
@@ -399,25 +402,41 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
         const uint16_t* src = p.q + (u.s.row + static_cast<int64_t>(tq)) * p.ldq +
                               static_cast<int64_t>(head) * D;
         float inv = 1.f, unit = 1.f;
+        // (a piece of a tree's unit is short: its whole row, and its mask, on their way at once)
+        uint4 held[TREE ? D / 8 : 1];
+        if constexpr (TREE) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            held[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (valid) held[i] = reinterpret_cast<const uint4*>(src)[i];
+          }
+          const uint32_t* mask = p.masks + (u.s.row + static_cast<int64_t>(tq)) * p.mask_words;
+          for (int i = 0; i < (u.s.n + 31) / 32; ++i) masks[i * kPromptRows + (threadIdx.x & 255)] = mask[i];
+        }
         if (p.is_bf16) {
           float amax = 0.f;
-#pragma unroll 4
-          for (int i = 0; i < D / 8; ++i) {
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (valid) w = reinterpret_cast<const uint4*>(src)[i];
+          auto most = [&](const uint4& w) {
             float f[8];
             widen8<true>(w, f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+          };
+          if constexpr (TREE) {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) most(held[i]);
+          } else {
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+              uint4 w = make_uint4(0u, 0u, 0u, 0u);
+              if (valid) w = reinterpret_cast<const uint4*>(src)[i];
+              most(w);
+            }
           }
           unit = row_unit<true>(amax, inv);
         }
         if (p.scale < 0.f) inv = -inv;             // the maximum below wants positive factors
         const uint32_t dst = base + L::kQ + t * L::kTile + (threadIdx.x & 127) * 128;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (valid) w = reinterpret_cast<const uint4*>(src)[i];
+        auto put = [&](int i, uint4 w) {
           if (p.is_bf16) {
             float f[8];
             widen8<true>(w, f);
@@ -431,6 +450,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
             w.w ^= 0x80008000u;
           }
           st_shared16(dst + (i / 8) * 16384 + (((i % 8) ^ (threadIdx.x & 7)) << 4), w.x, w.y, w.z, w.w);
+        };
+        if constexpr (TREE) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) put(i, held[i]);
+        } else {
+#pragma unroll 4
+          for (int i = 0; i < D / 8; ++i) {
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (valid) w = reinterpret_cast<const uint4*>(src)[i];
+            put(i, w);
+          }
         }
         fac = unit * fabsf(p.scale) * (MODS ? 1.f : kLog2e);
       }
@@ -443,12 +473,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       if (TREE && MODS && p.positions != nullptr)
         limit = p.positions[u.s.row + static_cast<int64_t>(tq)];
       const int low_limit = TREE ? u.start - 1 : u.start + (u.row0 + 128 * t) / p.group;
-      // which of the 16 tokens from `tok` on the row sees
-      const uint32_t* mask = TREE ? p.masks + (u.s.row + static_cast<int64_t>(tq)) * p.mask_words : nullptr;
+      // which of the 16 tokens from `tok` on the row sees (its thread has put its mask there)
       auto window = [&](int tok) -> uint32_t {
         const int off = tok - u.start;
         if (off <= -kGranule) return 0xFFFFu;
-        return off < u.s.n ? tree_window(mask, p.mask_words, off, u.s.n) : 0u;
+        return off < u.s.n ? tree_window(masks + (threadIdx.x & 255), kPromptRows, (u.s.n + 31) / 32, off, u.s.n) : 0u;
       };
       const float slope = MODS && p.slopes != nullptr && valid ? p.slopes[head] : 0.f;
       float m = -1e30f, l = 0.f;                   // m: the reference of z + log2 value scale
@@ -611,8 +640,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
           part = tree_plan(p.meta, gridDim.x, p.c.B).parts +
                  static_cast<int64_t>(u.slot) * (kPromptRows * (D + 1));
           if (valid) part[kPromptRows * D + row - u.row0] = l == 0.f ? -1e30f : m + log2f(l);
-          part += static_cast<int64_t>(row - u.row0) * D;
         }
+        // (trees: staged in shared memory that the products no longer read, and stored by rows)
+        const uint32_t stage = base + (t == 0 ? L::kQ : L::kK) + (warp & 3) * (32 * D * 4);
         const int tq_out = valid ? tq : 0;
         uint16_t* dst = p.out + ((u.s.row + static_cast<int64_t>(tq_out)) * p.q_heads + head) * D;
         const bool nans = bars->nan_any != 0u;
@@ -628,7 +658,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
               bad |= nan_bits[(tok - edge0) * (D / 32) + q];
             }
           }
-          if (valid) {
+          if (TREE || valid) {
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
               float o[8];
@@ -637,12 +667,38 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
                 o[k] = inv == 0.f ? 0.f : __uint_as_float(r[e + k]) * inv;
                 if ((bad >> (e + k)) & 1u) o[k] = __uint_as_float(0x7FC00000u);
               }
-              if (TREE && part != nullptr) {
-                *reinterpret_cast<float4*>(part + 32 * q + e) = make_float4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<float4*>(part + 32 * q + e + 4) = make_float4(o[4], o[5], o[6], o[7]);
+              if constexpr (TREE) {
+                const int chunk = 8 * q + e / 4;               // 16-byte units of the row, xor-ed by it
+                st_shared16(stage + lane * (D * 4) + ((chunk ^ (lane & 7)) << 4), __float_as_uint(o[0]),
+                            __float_as_uint(o[1]), __float_as_uint(o[2]), __float_as_uint(o[3]));
+                st_shared16(stage + lane * (D * 4) + (((chunk + 1) ^ (lane & 7)) << 4), __float_as_uint(o[4]),
+                            __float_as_uint(o[5]), __float_as_uint(o[6]), __float_as_uint(o[7]));
               } else {
                 *reinterpret_cast<uint4*>(dst + 32 * q + e) = p.is_bf16 ? narrow8<true>(o) : narrow8<false>(o);
               }
+            }
+          }
+        }
+        if constexpr (TREE) {
+          __syncwarp();
+          const int first = row - lane;                        // the warp's first row
+          if (part != nullptr) {
+            for (int i = lane; i < 32 * D / 4; i += 32) {
+              const int r = i / (D / 4), chunk = i % (D / 4);
+              if (first + r >= u.rows) break;
+              const float4 v = ld_shared_f4(stage + r * (D * 4) + ((chunk ^ (r & 7)) << 4));
+              *reinterpret_cast<float4*>(part + static_cast<int64_t>(first + r - u.row0) * D + 4 * chunk) = v;
+            }
+          } else {
+            for (int i = lane; i < 32 * D / 8; i += 32) {
+              const int r = i / (D / 8), chunk = 2 * (i % (D / 8)), at = first + r;
+              if (at >= u.rows) break;
+              const float4 a = ld_shared_f4(stage + r * (D * 4) + ((chunk ^ (r & 7)) << 4));
+              const float4 z = ld_shared_f4(stage + r * (D * 4) + (((chunk + 1) ^ (r & 7)) << 4));
+              const float o[8] = {a.x, a.y, a.z, a.w, z.x, z.y, z.z, z.w};
+              const int tok = at / p.group, mine = u.h * p.group + (at - tok * p.group);
+              *reinterpret_cast<uint4*>(p.out + ((u.s.row + static_cast<int64_t>(tok)) * p.q_heads + mine) * D +
+                                        4 * chunk) = p.is_bf16 ? narrow8<true>(o) : narrow8<false>(o);
             }
           }
         }
@@ -808,7 +864,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
 // `ctas`: one per unit, or for drafted trees at least one per piece.
 template <int D, bool TREE>
 cudaError_t launch_prompt_d(const AttendParams& p, int row_tiles, int64_t ctas, cudaStream_t s) {
-  constexpr int smem = PromptSmem<D>::kAlloc;
+  constexpr int smem = TREE ? PromptSmem<D>::kTreeAlloc : PromptSmem<D>::kAlloc;
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
   const bool mods = p.softcap > 0.f || p.slopes != nullptr;
   auto* fn = mods ? prompt_kernel<D, true, TREE> : prompt_kernel<D, false, TREE>;

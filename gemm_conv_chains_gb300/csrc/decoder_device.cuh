@@ -54,15 +54,16 @@ __device__ __forceinline__ Sequence load_sequence(const CacheView& c, int b, uin
 }
 
 // Which of the 16 tokens from the new token `off` on a row of a tree sees, as bits: its mask's, and
-// every older token (off < 0, above -16).  Nothing at or past the n new ones (off < n).
-__device__ __forceinline__ uint32_t tree_window(const uint32_t* mask, int words, int off, int n) {
+// every older token (off < 0, above -16).  Nothing at or past the n new ones (off < n).  The mask's words
+// are `stride` apart.
+__device__ __forceinline__ uint32_t tree_window(const uint32_t* mask, int stride, int words, int off, int n) {
   uint32_t w;
   if (off < 0) {
     w = (mask[0] << -off) | ((1u << -off) - 1u);
   } else {
     const int i = off >> 5, sh = off & 31;
-    w = mask[i] >> sh;
-    if (sh > 16 && i + 1 < words) w |= mask[i + 1] << (32 - sh);
+    w = mask[i * stride] >> sh;
+    if (sh > 16 && i + 1 < words) w |= mask[(i + 1) * stride] << (32 - sh);
   }
   const int left = n - off;
   return w & (left < 16 ? (1u << left) - 1u : 0xFFFFu);

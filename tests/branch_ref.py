@@ -67,11 +67,13 @@ def tree_attention(cache, q, blocks, scale, softcap=0.0, slopes=None, positions=
             delta = (D + 16) * 2.0 ** -24 * size
             # (a row that sees nothing has no largest score: its weights are zeros)
             z = torch.where(seen, z, -math.inf)
-            e = torch.exp(z - z.amax(-1, keepdim=True).clamp_min(-1e30))
+            e = torch.exp(z - z.amax(-1, keepdim=True).clamp_min(-1e30))     # (of a NaN: all NaN)
             p = torch.where(seen, e, 0) / e.sum(-1, keepdim=True).clamp_min(1e-300)
             # what a row does not see does not enter it, a NaN neither
             vs = torch.where(seen.any(0)[:, None], vh, 0)
             one = torch.stack([p[i, seen[i]] @ vh[seen[i]] for i in range(n)])
+            # (NaN scores and codes make NaN outputs; the others' bounds are what counts)
+            p, delta = torch.nan_to_num(p), torch.nan_to_num(delta)
             mag = torch.where(seen, p * (2.0 ** -11 + 2.0 ** -18 + 2 * delta), 0)
             clean = torch.nan_to_num(vs.abs())
             out[at: at + n, h] = one

@@ -197,6 +197,66 @@ def test_many_sequences(B, most):
     _check(out, c, q, blocks, 0.125)
 
 
+# Enough rows and room for the kernel that takes wide trees (256 query rows per block, contexts cut in
+# pieces): uncut units beside cut ones, row tiles of one row, masks of several words, most new tokens.
+WIDE = [
+    ([1500, 7, 0, 300], [40, 33, 64, 1], 2, 4, 64, 32), ([2000, 100], [65, 128], 1, 2, 96, 16),
+    ([3000], [257], 1, 1, 128, 64), ([1100, 1, 5000], [384, 70, 200], 1, 3, 128, 128),
+    ([1300, 40], [100, 0], 4, 8, 64, 256), ([900, 600, 2, 1200, 0], [70, 3, 90, 33, 12], 2, 5, 128, 16),
+]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("older,new,heads,group,D,page", WIDE)
+def test_wide_trees(dt, older, new, heads, group, D, page):
+    c = ref.Cache(older, new, heads, D, page, seed=D + len(older), fill=0xFF)
+    assert max(new) * group > 64 and c.table.shape[1] * page > 1024
+    blocks = _blocks(new, D, 11)
+    Hq = heads * group
+    rows = _randn(D, c.T, Hq + 1, D).to(DT[dt])
+    q = rows.cuda()[:, :Hq]
+    out = _run(c, q, blocks)
+    _check(out, c, rows[:, :Hq], blocks, D ** -0.5)
+    assert torch.equal(out, _run(c, q, blocks))
+    back = _run(c, (-rows).cuda()[:, :Hq], blocks, scale=-D ** -0.5)
+    assert torch.equal(out, back)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("older,new,heads,group,D,page", WIDE)
+def test_wide_trees_with_cap_and_bias(dt, older, new, heads, group, D, page):
+    c = ref.Cache(older, new, heads, D, page, seed=D, fill=0x7F)
+    blocks = _blocks(new, 5)
+    Hq = heads * group
+    q = (_randn(D + 1, c.T, Hq, D) * 3).to(DT[dt])
+    slopes = torch.rand(Hq, generator=torch.Generator().manual_seed(2)) * 0.3
+    depth = torch.cat([b.sum(-1) - 1 for b in blocks if b.numel()]).int()
+    at = depth + torch.repeat_interleave(torch.tensor(older), torch.tensor(new)).int()
+    out = _run(c, q.cuda(), blocks, softcap=20.0, slopes=slopes.cuda(), positions=at.cuda())
+    _check(out, c, q, blocks, D ** -0.5, softcap=20.0, slopes=slopes, positions=at)
+
+
+def test_wide_sets_that_hide_and_nans_that_are_hidden():
+    """Rows that see no new token or nothing at all; NaN codes of new tokens reach who sees them only."""
+    for D, page in ((64, 16), (128, 64), (96, 32)):
+        older, new = [1200, 0, 700], [90, 70, 80]
+        c = ref.Cache(older, new, 2, D, page, seed=4, fill=0x7F)
+        g = torch.Generator().manual_seed(7)
+        blocks = [torch.rand(n, n, generator=g) < 0.2 for n in new]
+        blocks[1][5], blocks[1][69], blocks[0][3] = False, False, False
+        for tok, pool in ((10, c.k), (50, c.v), (79, c.v)):
+            at = older[2] + tok
+            pool.view(torch.uint8)[c.table[2, at // page], 1, at % page, 9] = 0x7F
+        q = _randn(3, c.T, 6, D).bfloat16()
+        out = _run(c, q.cuda(), blocks).cpu()
+        assert (out[90 + 5] == 0).all() and (out[90 + 69] == 0).all()
+        want, tol = br.tree_attention(c, q, blocks, D ** -0.5)
+        assert torch.equal(out.isnan(), want.isnan())
+        assert out.isnan().any() and not out[:160].isnan().any()
+        tol = tol + UNIT[q.dtype] * (want.abs() + tol) + TINY[q.dtype]
+        assert (((out.double() - want).abs() <= tol) | want.isnan()).all()
+
+
 def test_long_context_and_wide_tree():
     for older, new, group, D in ([20011], [64], 4, 128), ([30001], [3], 2, 64), ([9000], [90], 2, 256):
         c = ref.Cache(older, new, 2, D, 128, seed=7, fill=0x7F)
