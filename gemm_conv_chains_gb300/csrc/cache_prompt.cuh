@@ -70,7 +70,8 @@ struct PromptSmem {
   static constexpr int kBytes = kBar + 256;
   static constexpr int kAlloc = kBytes + 1024;                  // the tiles start 1 KB aligned
   static constexpr int kMasks = kBytes;                         // trees: [words][256 rows]
-  static constexpr int kTreeAlloc = kAlloc + (kEdgeTokens - kPromptKeys) / 32 * kPromptRows * 4;
+  static constexpr int kUnits = kMasks + (kEdgeTokens - kPromptKeys) / 32 * kPromptRows * 4;   // [256 rows]
+  static constexpr int kTreeAlloc = kUnits + kPromptRows * 4 + 1024;
 };
 
 struct PromptBars {
@@ -186,10 +187,14 @@ __device__ __forceinline__ bool prompt_unit(const AttendParams& p, int b, int h,
 }
 
 // Drafted trees.  All rows of a sequence see its older tokens, few of them new ones, so that a
-// sequence's units all walk the same key tiles, and one sequence may have nearly all of them.  Units of
-// more than L key tiles are cut into equal pieces of at most L, with a CTA each, and a further kernel
-// joins their parts; L is what an even share of all key tiles over the SMs comes to, at least
-// kMinPieceTiles.  A small kernel ahead writes the pieces down from the lengths.
+// sequence's units all walk the same key tiles, and one sequence may have nearly all of them.  Where the
+// units do not fill the SMs, those of more than L key tiles are cut into equal pieces of at most L, with
+// a CTA each, and a further kernel joins their parts; L is what an even share of all key tiles over the SMs
+// comes to, at least kMinPieceTiles.  A small kernel ahead writes the pieces down from the lengths.  A CTA's
+// own start and end are ~20 us, its tiles 1.45 (one row tile) to 1.95 us at 128 channels: 1 sequence of 64
+// nodes over 131072 tokens, 16 query heads on 2: 76 us (1919 uncut; pieces of half the share 98, of one
+// and a half 102); 16 sequences of up to 60 nodes over up to 4096 tokens, 32 on 8, 128 units: 82 us uncut,
+// 82 to 95 cut.
 constexpr int kMinPieceTiles = 4;
 // The most new tokens of a sequence: what some rows see and others do not has to fit kEdgeTokens.
 constexpr int kMostTreeTokens = kEdgeTokens - kPromptKeys;
@@ -330,6 +335,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
   float2* scales = reinterpret_cast<float2*>(smem + L::kScales);
   uint32_t* nan_bits = reinterpret_cast<uint32_t*>(smem + L::kNan);
   [[maybe_unused]] uint32_t* masks = reinterpret_cast<uint32_t*>(smem + L::kMasks);
+  [[maybe_unused]] float* units = reinterpret_cast<float*>(smem + L::kUnits);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   PromptUnit u;
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
     int order = static_cast<int>(blockIdx.x) / p.c.heads;
     grid_launch_dependents();
     grid_dependency_wait();                                // launched early
-    if constexpr (TREE) {
+    if (TREE && p.whole == 0) {
       const TreePlan plan = tree_plan(p.meta, gridDim.x, p.c.B);
       if (!tree_unit(p, plan, static_cast<int>(blockIdx.x), u)) return;                // the whole CTA
     } else {
@@ -347,6 +353,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       }
       plain_pair(p, row_tiles, order, b, rt);
       if (!prompt_unit(p, b, static_cast<int>(blockIdx.x) % p.c.heads, rt, u)) return; // the whole CTA
+      if constexpr (TREE) {                                // every row may see every new token
+        u.kv_end = u.s.len;
+        u.tiles = (u.kv_end + kPromptKeys - 1) / kPromptKeys;
+        u.t0 = 0;
+        u.slot = -1;
+      }
     }
   }
   const int first_tile = TREE ? u.t0 : 0;
@@ -402,64 +414,100 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
         const uint16_t* src = p.q + (u.s.row + static_cast<int64_t>(tq)) * p.ldq +
                               static_cast<int64_t>(head) * D;
         float inv = 1.f, unit = 1.f;
-        // (a piece of a tree's unit is short: its whole row, and its mask, on their way at once)
-        uint4 held[TREE ? D / 8 : 1];
         if constexpr (TREE) {
+          // A piece of a tree's unit is short: its rows come whole (D / 8 lanes each) and all at once, the
+          // row's thread gets its unit through shared memory, and its mask.  (A thread per row, as below:
+          // 8.5 us of a piece's 30.)
+          constexpr int kPer = D / 8, kRows = 32 / kPer, kLoads = (32 + kRows - 1) / kRows;
+          const int sub = lane / kPer, at = lane % kPer, warp_row = (threadIdx.x & 127) - lane;
+          uint4 held[kLoads];
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            held[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (valid) held[i] = reinterpret_cast<const uint4*>(src)[i];
+          for (int k = 0; k < kLoads; ++k) {
+            const int in_warp = k * kRows + sub, r = u.row0 + 128 * t + warp_row + in_warp;
+            held[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (sub < kRows && in_warp < 32 && r < u.rows) {
+              const int tok = r / p.group;
+              held[k] = *reinterpret_cast<const uint4*>(
+                  p.q + (u.s.row + static_cast<int64_t>(tok)) * p.ldq +
+                  static_cast<int64_t>(u.h * p.group + (r - tok * p.group)) * D + 8 * at);
+            }
           }
           const uint32_t* mask = p.masks + (u.s.row + static_cast<int64_t>(tq)) * p.mask_words;
-          for (int i = 0; i < (u.s.n + 31) / 32; ++i) masks[i * kPromptRows + (threadIdx.x & 255)] = mask[i];
-        }
-        if (p.is_bf16) {
-          float amax = 0.f;
-          auto most = [&](const uint4& w) {
-            float f[8];
-            widen8<true>(w, f);
+          const int words = (u.s.n + 31) / 32;
+          for (int i = 0; i < words; i += 4) {
+            uint32_t word[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
-          };
-          if constexpr (TREE) {
+            for (int k = 0; k < 4; ++k) word[k] = i + k < words ? mask[i + k] : 0u;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) most(held[i]);
-          } else {
+            for (int k = 0; k < 4; ++k) masks[(i + k) * kPromptRows + (threadIdx.x & 255)] = word[k];
+          }
+#pragma unroll
+          for (int k = 0; k < kLoads; ++k) {
+            const int in_warp = k * kRows + sub, row_in = warp_row + in_warp;
+            uint4 w = held[k];
+            if (p.is_bf16) {
+              float f[8], most = 0.f, row_inv;
+              widen8<true>(w, f);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(f[e]));
+              // (kPer lanes: not always a power of two)
+#pragma unroll
+              for (int o = 8; o > 0; o >>= 1) {
+                const float other = __shfl_down_sync(0xffffffffu, most, o);
+                if (at + o < kPer) most = fmaxf(most, other);
+              }
+              most = __shfl_sync(0xffffffffu, most, sub < kRows ? sub * kPer : 0);
+              const float row_whole = row_unit<true>(most, row_inv);
+              if (p.scale < 0.f) row_inv = -row_inv;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] *= row_inv;
+              w = narrow8<false>(f);
+              if (at == 0 && sub < kRows && in_warp < 32) units[128 * t + row_in] = row_whole;
+            } else if (p.scale < 0.f) {
+              w.x ^= 0x80008000u;
+              w.y ^= 0x80008000u;
+              w.z ^= 0x80008000u;
+              w.w ^= 0x80008000u;
+            }
+            if (sub < kRows && in_warp < 32)
+              st_shared16(base + L::kQ + t * L::kTile + row_in * 128 + (at / 8) * 16384 + (((at % 8) ^ (row_in & 7)) << 4),
+                          w.x, w.y, w.z, w.w);
+          }
+          __syncwarp();
+          if (p.is_bf16) unit = units[threadIdx.x & 255];
+        } else {
+          if (p.is_bf16) {
+            float amax = 0.f;
 #pragma unroll 4
             for (int i = 0; i < D / 8; ++i) {
               uint4 w = make_uint4(0u, 0u, 0u, 0u);
               if (valid) w = reinterpret_cast<const uint4*>(src)[i];
-              most(w);
+              float f[8];
+              widen8<true>(w, f);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
             }
+            unit = row_unit<true>(amax, inv);
           }
-          unit = row_unit<true>(amax, inv);
-        }
-        if (p.scale < 0.f) inv = -inv;             // the maximum below wants positive factors
-        const uint32_t dst = base + L::kQ + t * L::kTile + (threadIdx.x & 127) * 128;
-        auto put = [&](int i, uint4 w) {
-          if (p.is_bf16) {
-            float f[8];
-            widen8<true>(w, f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] *= inv;
-            w = narrow8<false>(f);
-          } else if (p.scale < 0.f) {
-            w.x ^= 0x80008000u;
-            w.y ^= 0x80008000u;
-            w.z ^= 0x80008000u;
-            w.w ^= 0x80008000u;
-          }
-          st_shared16(dst + (i / 8) * 16384 + (((i % 8) ^ (threadIdx.x & 7)) << 4), w.x, w.y, w.z, w.w);
-        };
-        if constexpr (TREE) {
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) put(i, held[i]);
-        } else {
+          if (p.scale < 0.f) inv = -inv;           // the maximum below wants positive factors
+          const uint32_t dst = base + L::kQ + t * L::kTile + (threadIdx.x & 127) * 128;
 #pragma unroll 4
           for (int i = 0; i < D / 8; ++i) {
             uint4 w = make_uint4(0u, 0u, 0u, 0u);
             if (valid) w = reinterpret_cast<const uint4*>(src)[i];
-            put(i, w);
+            if (p.is_bf16) {
+              float f[8];
+              widen8<true>(w, f);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] *= inv;
+              w = narrow8<false>(f);
+            } else if (p.scale < 0.f) {
+              w.x ^= 0x80008000u;
+              w.y ^= 0x80008000u;
+              w.z ^= 0x80008000u;
+              w.w ^= 0x80008000u;
+            }
+            st_shared16(dst + (i / 8) * 16384 + (((i % 8) ^ (threadIdx.x & 7)) << 4), w.x, w.y, w.z, w.w);
           }
         }
         fac = unit * fabsf(p.scale) * (MODS ? 1.f : kLog2e);
@@ -636,7 +684,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
         tc_fence_after_sync();
         const float inv = l == 0.f || l > kNoValues ? 0.f : 1.f / l;
         float* part = nullptr;
-        if (TREE && u.slot >= 0) {
+        if (TREE && u.slot >= 0) {               // (a plan that cuts units has given it the slot)
           part = tree_plan(p.meta, gridDim.x, p.c.B).parts +
                  static_cast<int64_t>(u.slot) * (kPromptRows * (D + 1));
           if (valid) part[kPromptRows * D + row - u.row0] = l == 0.f ? -1e30f : m + log2f(l);

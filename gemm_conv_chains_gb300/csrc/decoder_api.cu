@@ -193,6 +193,29 @@ bool prompt_pays(int32_t D, int64_t rows, int64_t heads, bool few_keys, int num_
   return pieces * split_ns >= 0.85 * waves * (rows <= 128 ? 1450.0 : 1850.0);
 }
 
+// The same for drafted trees, where the tcgen05 kernel cuts long contexts if its units do not fill the
+// SMs.  Split kernel: 15 us, and 11.8 ns (7.8 at head size 64) per 32 rows and 128 keys.  tcgen05: 20 us
+// and 1.95 us (1.45 with one row tile; 1.4 at head size 64) per 128 keys of a unit and wave of units; cut,
+// 28 us and the even share of that.  Measured on 8 kv heads of 128, 4 query heads each:
+//   1 sequence,   16 nodes, 16000 cached: split  40 us, tcgen05 31      4000 cached: 26.5 and 23
+//   1 sequence,   64 nodes,  1000 cached: split  30 us, tcgen05 29       300 cached: 15.7 and 23
+//   16 sequences, 60 nodes, up to 4096:   split 222 us, tcgen05 82
+//   32 sequences, 16 nodes, up to 4000:   split 127 us, tcgen05 119      8 nodes: 92 and 139
+//   8 sequences,  12 nodes, up to 8000:   split  54 us, tcgen05 70
+bool tree_pays(const CacheView& c, int64_t rows, int num_sms) {
+  if (rows <= 32) return false;
+  const int64_t units = (rows + 255) / 256 * c.heads * c.B;
+  const double tiles = static_cast<double>(((static_cast<int64_t>(c.max_pages) << c.page_shift) + 127) / 128);
+  const double split_ns = c.D == 64 ? 7.8 : c.D == 96 ? 9.0 : 11.8;
+  const double tile_ns = (c.D == 64 ? 1400.0 : c.D == 96 ? 1700.0 : 1950.0) * (rows <= 128 ? 0.75 : 1.0);
+  const double split = 15000.0 + split_ns * static_cast<double>((rows + 31) / 32) * c.heads * c.B * tiles;
+  const bool cut = 4 * units < 3 * num_sms && tiles > 4;
+  const double share = units * tiles / num_sms;
+  const double waves = static_cast<double>((units + num_sms - 1) / num_sms);
+  const double other = cut ? 28000.0 + tile_ns * (share > 4 ? share : 4) : waves * (20000.0 + tile_ns * tiles);
+  return other < 0.95 * split;
+}
+
 // The limit of each on-chip wait of the tcgen05 kernel.
 constexpr uint64_t kDecoderWaitNs = 1000000000ull;
 
@@ -208,9 +231,7 @@ SplitChoice split_of(const b2b_cache* c, int32_t q_heads, bool tree, int num_sms
   const int64_t runs = s.whole ? pieces : pieces * ((most / 64 + kMinTiles - 1) / kMinTiles);
   if (runs < s.grid) s.grid = static_cast<int>(runs);
   const CacheView view = view_of(c, 0, nullptr);
-  // (drafted trees, D = 128, 32 query heads on 8: 1 sequence, 64 nodes over 32000 cached 58 us for the split
-  // kernel's 171; 300 cached 23 for 16; 32 sequences, 16 nodes (64 rows) over up to 4000 143 for 127)
-  s.prompt = tree ? tree_fits(view) && rows > 64 && most > 1024
+  s.prompt = tree ? tree_fits(view) && tree_pays(view, rows, num_sms)
                   : prompt_pays(c->head_dim, rows, static_cast<int64_t>(c->batch) * c->heads, most <= 512,
                                 num_sms);
   s.bytes = s.prompt  ? (tree ? tree_workspace(rows, view, num_sms) : prompt_workspace(rows, c->batch))

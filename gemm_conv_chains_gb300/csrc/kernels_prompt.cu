@@ -31,16 +31,18 @@ int64_t prompt_workspace(int64_t rows, int32_t B) {
   return B > 1 && row_tiles > 1 && row_tiles * B <= kRankedPairs ? 4 * kRankedPairs : 0;
 }
 
+int64_t prompt_order_bytes(int64_t pairs) { return pairs <= kRankedPairs ? 4 * kRankedPairs : 0; }
+cudaError_t launch_prompt_order(const AttendParams& p, int row_tiles, cudaStream_t s) {
+  return launch_early(prompt_order_kernel, 1, kRankedPairs, 0, s, p, row_tiles, reinterpret_cast<int*>(p.meta));
+}
+
 cudaError_t launch_prompt(const AttendParams& p, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.c.max_new) * p.group;
   const int64_t row_tiles = (rows + kPromptRows - 1) / kPromptRows;
   const int64_t ctas = row_tiles * p.c.heads * p.c.B;
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   if (p.meta != nullptr) {
-    if (cudaError_t e = launch_early(prompt_order_kernel, 1, kRankedPairs, 0, s, p,
-                                     static_cast<int>(row_tiles), reinterpret_cast<int*>(p.meta));
-        e != cudaSuccess)
-      return e;
+    if (cudaError_t e = launch_prompt_order(p, static_cast<int>(row_tiles), s); e != cudaSuccess) return e;
   }
   switch (p.c.D) {
     case 64: return launch_prompt_d<64, false>(p, static_cast<int>(row_tiles), ctas, s);

@@ -17,8 +17,7 @@ __device__ __forceinline__ TreeWork tree_work(const AttendParams& p, int b, int&
 }
 
 // Every block sums all sequences up and writes down its share of the pieces.
-__global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const AttendParams p, int64_t most, int num_sms,
-                                                                 int cut) {
+__global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const AttendParams p, int64_t most, int num_sms) {
   __shared__ unsigned long long sums[kPlanThreads / 32];
   __shared__ int piece_at[kPlanThreads + 1], slot_at[kPlanThreads], count_of[kPlanThreads], rows_of[kPlanThreads];
   grid_launch_dependents();
@@ -27,23 +26,21 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const AttendPar
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   // ---- the longest piece ----
   int row_tiles;
-  int length = 0x7FFFFFFF;
-  if (cut) {
-    unsigned long long total = 0;
-    for (int b = t; b < p.c.B; b += kPlanThreads) {
-      const TreeWork w = tree_work(p, b, row_tiles);
-      total += static_cast<unsigned long long>(w.units) * w.tiles;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) sums[warp] = total;
-    __syncthreads();
-    total = 0;
-    for (int i = 0; i < kPlanThreads / 32; ++i) total += sums[i];
-    const unsigned long long share = (total + num_sms - 1) / num_sms;
-    length = share < kMinPieceTiles ? kMinPieceTiles : share > 0x7FFFFFFF ? 0x7FFFFFFF : static_cast<int>(share);
-    __syncthreads();
+  unsigned long long total = 0;
+  for (int b = t; b < p.c.B; b += kPlanThreads) {
+    const TreeWork w = tree_work(p, b, row_tiles);
+    total += static_cast<unsigned long long>(w.units) * w.tiles;
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) sums[warp] = total;
+  __syncthreads();
+  total = 0;
+  for (int i = 0; i < kPlanThreads / 32; ++i) total += sums[i];
+  const unsigned long long share = (total + num_sms - 1) / num_sms;
+  const int length =
+      share < kMinPieceTiles ? kMinPieceTiles : share > 0x7FFFFFFF ? 0x7FFFFFFF : static_cast<int>(share);
+  __syncthreads();
   // ---- 256 sequences at a time: where their pieces and slots begin ----
   int pieces = 0, slots = 0;
   for (int b0 = 0; b0 < p.c.B; b0 += kPlanThreads) {
@@ -115,12 +112,11 @@ struct TreeShape {
   int64_t pieces, slots;               // at most
   bool cut;
 };
-// With many units there is little to gain from cutting them.
 TreeShape tree_shape(int64_t rows, const CacheView& c, int num_sms) {
   TreeShape s;
   const int64_t units = (rows + kPromptRows - 1) / kPromptRows * c.heads * c.B;
   const int64_t tiles = ((static_cast<int64_t>(c.max_pages) << c.page_shift) + kPromptKeys - 1) / kPromptKeys;
-  s.cut = units < 4 * num_sms && tiles > kMinPieceTiles;
+  s.cut = 4 * units < 3 * num_sms && tiles > kMinPieceTiles;
   // pieces of at most L tiles, L >= all tiles / SMs: fewer than SMs besides one per unit, and fewer
   // than 2 SMs in units that are cut
   s.pieces = units + (s.cut ? num_sms : 0);
@@ -132,22 +128,30 @@ TreeShape tree_shape(int64_t rows, const CacheView& c, int num_sms) {
 
 int64_t tree_workspace(int64_t rows, const CacheView& c, int num_sms) {
   const TreeShape s = tree_shape(rows, c, num_sms);
+  // uncut, of ragged sequences in more than one wave: the longest first
+  if (!s.cut) return c.B > 1 && s.pieces > num_sms ? prompt_order_bytes(s.pieces / c.heads) : 0;
   return tree_plan_bytes(s.pieces, c.B) + s.slots * kPromptRows * (c.D + 1) * 4;
 }
 bool tree_fits(const CacheView& c) { return c.D <= 128 && c.max_new <= kMostTreeTokens; }
 
-cudaError_t launch_tree(const AttendParams& p, int num_sms, cudaStream_t s) {
+cudaError_t launch_tree(AttendParams p, int num_sms, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.c.max_new) * p.group;
   const TreeShape shape = tree_shape(rows, p.c, num_sms);
   if (shape.pieces > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  const int64_t plan_blocks = (shape.pieces + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
-  cudaError_t e = launch_early(tree_plan_kernel, plan_blocks, kPlanThreads, 0, s, p, shape.pieces, num_sms,
-                               shape.cut ? 1 : 0);
+  const int row_tiles = static_cast<int>((rows + kPromptRows - 1) / kPromptRows);
+  p.whole = shape.cut ? 0 : 1;
+  cudaError_t e = cudaSuccess;
+  if (shape.cut) {
+    const int64_t plan_blocks = (shape.pieces + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+    e = launch_early(tree_plan_kernel, plan_blocks, kPlanThreads, 0, s, p, shape.pieces, num_sms);
+  } else if (p.meta != nullptr) {
+    e = launch_prompt_order(p, row_tiles, s);
+  }
   if (e != cudaSuccess) return e;
   switch (p.c.D) {
-    case 64: e = launch_prompt_d<64, true>(p, 0, shape.pieces, s); break;
-    case 96: e = launch_prompt_d<96, true>(p, 0, shape.pieces, s); break;
-    case 128: e = launch_prompt_d<128, true>(p, 0, shape.pieces, s); break;
+    case 64: e = launch_prompt_d<64, true>(p, row_tiles, shape.pieces, s); break;
+    case 96: e = launch_prompt_d<96, true>(p, row_tiles, shape.pieces, s); break;
+    case 128: e = launch_prompt_d<128, true>(p, row_tiles, shape.pieces, s); break;
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess || !shape.cut) return e;
