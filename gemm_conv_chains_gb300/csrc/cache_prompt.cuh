@@ -70,8 +70,7 @@ struct PromptSmem {
   static constexpr int kBytes = kBar + 256;
   static constexpr int kAlloc = kBytes + 1024;                  // the tiles start 1 KB aligned
   static constexpr int kMasks = kBytes;                         // trees: [words][256 rows]
-  static constexpr int kUnits = kMasks + (kEdgeTokens - kPromptKeys) / 32 * kPromptRows * 4;   // [256 rows]
-  static constexpr int kTreeAlloc = kUnits + kPromptRows * 4 + 1024;
+  static constexpr int kTreeAlloc = kAlloc + (kEdgeTokens - kPromptKeys) / 32 * kPromptRows * 4;
 };
 
 struct PromptBars {
@@ -191,10 +190,10 @@ __device__ __forceinline__ bool prompt_unit(const AttendParams& p, int b, int h,
 // units do not fill the SMs, those of more than L key tiles are cut into equal pieces of at most L, with
 // a CTA each, and a further kernel joins their parts; L is what an even share of all key tiles over the SMs
 // comes to, at least kMinPieceTiles.  A small kernel ahead writes the pieces down from the lengths.  A CTA's
-// own start and end are ~20 us, its tiles 1.45 (one row tile) to 1.95 us at 128 channels: 1 sequence of 64
-// nodes over 131072 tokens, 16 query heads on 2: 76 us (1919 uncut; pieces of half the share 98, of one
-// and a half 102); 16 sequences of up to 60 nodes over up to 4096 tokens, 32 on 8, 128 units: 82 us uncut,
-// 82 to 95 cut.
+// own start and end are ~11 us, its tiles 1.55 (one row tile) to 2.05 us at 128 channels: 1 sequence of 64
+// nodes over 131072 tokens, 16 query heads on 2: 68 us, 1.0 PFLOP/s (1919 us uncut; pieces of half the share
+// and of one and a half were 30 % slower); 16 sequences of up to 60 nodes over up to 4096 tokens, 32 on 8,
+// 128 units: 79 us uncut, 6 us more cut.
 constexpr int kMinPieceTiles = 4;
 // The most new tokens of a sequence: what some rows see and others do not has to fit kEdgeTokens.
 constexpr int kMostTreeTokens = kEdgeTokens - kPromptKeys;
@@ -324,10 +323,97 @@ struct PromptProducer {
   }
 };
 
-template <int D, bool MODS, bool TREE>
+// A warp's 32 query rows of a drafted tree (r0 .. r0 + 31 of `rows`) as fp16 at q_at + 128 row_in .., and
+// each thread's mask: a piece of a tree's unit is short, so its rows come whole (D / 8 lanes each) and
+// all at once, straight to where the products want them; then each thread turns its row there.  Returns the
+// power of two that goes back into its scores.  (Loads by a thread per row, 16 in registers: 8.5 us of a
+// piece's 30; by whole rows, 16 times unrolled: 5.5, mostly instructions that are not in the cache yet.  A
+// function of its own, since inlined it cost the loops registers.)
+template <int D>
+__device__ __forceinline__ float stage_tree_rows(const uint16_t* q, const uint16_t* any, int64_t ldq, int group, int r0,
+                                              int rows, uint32_t q_at, int row_in, const uint32_t* mask,
+                                              uint32_t* mask_to, int words, int is_bf16, bool negative) {
+  constexpr int kPer = D / 8, kRows = 32 / kPer;
+  const int lane = threadIdx.x & 31, sub = lane / kPer, at = lane % kPer;
+  {
+    int r = r0 + sub, tok = r / group, in_tok = r - tok * group;
+#pragma unroll 1
+    for (int k = sub; k < 32; k += kRows, r += kRows) {
+      const int in = row_in + k;
+      const bool take = sub < kRows && r < rows;
+      const uint16_t* from = q + tok * ldq + in_tok * D + 8 * at;
+      const int bytes = take ? 16 : 0;               // 0: zeros
+      if (sub < kRows)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         q_at + in * 128 + (at / 8) * 16384 + (((at % 8) ^ (in & 7)) << 4)),
+                     "l"(take ? from : any), "r"(bytes)
+                     : "memory");
+      in_tok += kRows;
+      while (in_tok >= group) {
+        in_tok -= group;
+        ++tok;
+      }
+    }
+  }
+  for (int i = 0; i < words; i += 4) {
+    uint32_t word[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) word[k] = i + k < words ? mask[i + k] : 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mask_to[(i + k) * kPromptRows] = word[k];
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  float unit = 1.f, inv = 1.f;
+  if (!is_bf16 && !negative) return unit;
+  const int mine = row_in + lane;
+  auto place = [&](int i) -> uint32_t {
+    return q_at + mine * 128 + (i / 8) * 16384 + (((i % 8) ^ (mine & 7)) << 4);
+  };
+  auto load = [&](int i) -> uint4 {
+    const float4 v = ld_shared_f4(place(i));
+    return make_uint4(__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w));
+  };
+  if (is_bf16) {
+    // the largest magnitude: 16-bit patterns without their signs order like it
+    uint32_t most = 0u;
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+      const uint4 w = load(i);
+      most = __vmaxu2(most, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                     __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
+    }
+    const uint32_t hi = most & 0xFFFF0000u, lo = most << 16;
+    unit = row_unit<true>(__uint_as_float(hi > lo ? hi : lo), inv);
+  }
+  if (negative) inv = -inv;                          // the softmax's maximum wants positive factors
+#pragma unroll 2
+  for (int i = 0; i < D / 8; ++i) {
+    uint4 w = load(i);
+    if (is_bf16) {
+      float f[8];
+      widen8<true>(w, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] *= inv;
+      w = narrow8<false>(f);
+    } else {
+      w.x ^= 0x80008000u;
+      w.y ^= 0x80008000u;
+      w.z ^= 0x80008000u;
+      w.w ^= 0x80008000u;
+    }
+    st_shared16(place(i), w.x, w.y, w.z, w.w);
+  }
+  return unit;
+}
+
+// TREE: drafted trees, their units whole (kTreeWhole) or cut in pieces.
+enum PromptKind { kCausal, kTreeWhole, kTreeCut };
+template <int D, bool MODS, PromptKind KIND>
 __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendParams p,
                                                                    int row_tiles) {
   using L = PromptSmem<D>;
+  constexpr bool TREE = KIND != kCausal, CUT = KIND == kTreeCut;
   extern __shared__ uint8_t raw_smem[];
   const uint32_t base = (smem_u32(raw_smem) + 1023u) & ~1023u;
   uint8_t* smem = raw_smem + (base - smem_u32(raw_smem));
@@ -335,7 +421,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
   float2* scales = reinterpret_cast<float2*>(smem + L::kScales);
   uint32_t* nan_bits = reinterpret_cast<uint32_t*>(smem + L::kNan);
   [[maybe_unused]] uint32_t* masks = reinterpret_cast<uint32_t*>(smem + L::kMasks);
-  [[maybe_unused]] float* units = reinterpret_cast<float*>(smem + L::kUnits);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   PromptUnit u;
@@ -344,7 +429,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
     int order = static_cast<int>(blockIdx.x) / p.c.heads;
     grid_launch_dependents();
     grid_dependency_wait();                                // launched early
-    if (TREE && p.whole == 0) {
+    if constexpr (CUT) {
       const TreePlan plan = tree_plan(p.meta, gridDim.x, p.c.B);
       if (!tree_unit(p, plan, static_cast<int>(blockIdx.x), u)) return;                // the whole CTA
     } else {
@@ -356,12 +441,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       if constexpr (TREE) {                                // every row may see every new token
         u.kv_end = u.s.len;
         u.tiles = (u.kv_end + kPromptKeys - 1) / kPromptKeys;
-        u.t0 = 0;
-        u.slot = -1;
       }
     }
   }
-  const int first_tile = TREE ? u.t0 : 0;
+  const int first_tile = CUT ? u.t0 : 0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -415,66 +498,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
                               static_cast<int64_t>(head) * D;
         float inv = 1.f, unit = 1.f;
         if constexpr (TREE) {
-          // A piece of a tree's unit is short: its rows come whole (D / 8 lanes each) and all at once, the
-          // row's thread gets its unit through shared memory, and its mask.  (A thread per row, as below:
-          // 8.5 us of a piece's 30.)
-          constexpr int kPer = D / 8, kRows = 32 / kPer, kLoads = (32 + kRows - 1) / kRows;
-          const int sub = lane / kPer, at = lane % kPer, warp_row = (threadIdx.x & 127) - lane;
-          uint4 held[kLoads];
-#pragma unroll
-          for (int k = 0; k < kLoads; ++k) {
-            const int in_warp = k * kRows + sub, r = u.row0 + 128 * t + warp_row + in_warp;
-            held[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (sub < kRows && in_warp < 32 && r < u.rows) {
-              const int tok = r / p.group;
-              held[k] = *reinterpret_cast<const uint4*>(
-                  p.q + (u.s.row + static_cast<int64_t>(tok)) * p.ldq +
-                  static_cast<int64_t>(u.h * p.group + (r - tok * p.group)) * D + 8 * at);
-            }
-          }
-          const uint32_t* mask = p.masks + (u.s.row + static_cast<int64_t>(tq)) * p.mask_words;
-          const int words = (u.s.n + 31) / 32;
-          for (int i = 0; i < words; i += 4) {
-            uint32_t word[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) word[k] = i + k < words ? mask[i + k] : 0u;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) masks[(i + k) * kPromptRows + (threadIdx.x & 255)] = word[k];
-          }
-#pragma unroll
-          for (int k = 0; k < kLoads; ++k) {
-            const int in_warp = k * kRows + sub, row_in = warp_row + in_warp;
-            uint4 w = held[k];
-            if (p.is_bf16) {
-              float f[8], most = 0.f, row_inv;
-              widen8<true>(w, f);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(f[e]));
-              // (kPer lanes: not always a power of two)
-#pragma unroll
-              for (int o = 8; o > 0; o >>= 1) {
-                const float other = __shfl_down_sync(0xffffffffu, most, o);
-                if (at + o < kPer) most = fmaxf(most, other);
-              }
-              most = __shfl_sync(0xffffffffu, most, sub < kRows ? sub * kPer : 0);
-              const float row_whole = row_unit<true>(most, row_inv);
-              if (p.scale < 0.f) row_inv = -row_inv;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] *= row_inv;
-              w = narrow8<false>(f);
-              if (at == 0 && sub < kRows && in_warp < 32) units[128 * t + row_in] = row_whole;
-            } else if (p.scale < 0.f) {
-              w.x ^= 0x80008000u;
-              w.y ^= 0x80008000u;
-              w.z ^= 0x80008000u;
-              w.w ^= 0x80008000u;
-            }
-            if (sub < kRows && in_warp < 32)
-              st_shared16(base + L::kQ + t * L::kTile + row_in * 128 + (at / 8) * 16384 + (((at % 8) ^ (row_in & 7)) << 4),
-                          w.x, w.y, w.z, w.w);
-          }
-          __syncwarp();
-          if (p.is_bf16) unit = units[threadIdx.x & 255];
+          const int64_t first_row = u.s.row;
+          unit = stage_tree_rows<D>(p.q + first_row * p.ldq + static_cast<int64_t>(u.h * p.group) * D, p.q, p.ldq, p.group,
+                                    u.row0 + 128 * t + (warp & 3) * 32, u.rows, base + L::kQ + t * L::kTile,
+                                    (threadIdx.x & 127) - lane, p.masks + (first_row + tq) * p.mask_words,
+                                    masks + (threadIdx.x & 255), (u.s.n + 31) / 32, p.is_bf16, p.scale < 0.f);
         } else {
           if (p.is_bf16) {
             float amax = 0.f;
@@ -525,7 +553,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       auto window = [&](int tok) -> uint32_t {
         const int off = tok - u.start;
         if (off <= -kGranule) return 0xFFFFu;
-        return off < u.s.n ? tree_window(masks + (threadIdx.x & 255), kPromptRows, (u.s.n + 31) / 32, off, u.s.n) : 0u;
+        return off < u.s.n ? tree_window(masks + (threadIdx.x & 255), kPromptRows, (kEdgeTokens - kPromptKeys) / 32, off, u.s.n) : 0u;
       };
       const float slope = MODS && p.slopes != nullptr && valid ? p.slopes[head] : 0.f;
       float m = -1e30f, l = 0.f;                   // m: the reference of z + log2 value scale
@@ -684,7 +712,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
         tc_fence_after_sync();
         const float inv = l == 0.f || l > kNoValues ? 0.f : 1.f / l;
         float* part = nullptr;
-        if (TREE && u.slot >= 0) {               // (a plan that cuts units has given it the slot)
+        if (CUT && u.slot >= 0) {
           part = tree_plan(p.meta, gridDim.x, p.c.B).parts +
                  static_cast<int64_t>(u.slot) * (kPromptRows * (D + 1));
           if (valid) part[kPromptRows * D + row - u.row0] = l == 0.f ? -1e30f : m + log2f(l);
@@ -730,7 +758,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
         if constexpr (TREE) {
           __syncwarp();
           const int first = row - lane;                        // the warp's first row
-          if (part != nullptr) {
+          if (CUT && part != nullptr) {
             for (int i = lane; i < 32 * D / 4; i += 32) {
               const int r = i / (D / 4), chunk = i % (D / 4);
               if (first + r >= u.rows) break;
@@ -910,12 +938,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
 }
 
 // `ctas`: one per unit, or for drafted trees at least one per piece.
-template <int D, bool TREE>
+template <int D, PromptKind KIND>
 cudaError_t launch_prompt_d(const AttendParams& p, int row_tiles, int64_t ctas, cudaStream_t s) {
-  constexpr int smem = TREE ? PromptSmem<D>::kTreeAlloc : PromptSmem<D>::kAlloc;
+  constexpr int smem = KIND != kCausal ? PromptSmem<D>::kTreeAlloc : PromptSmem<D>::kAlloc;
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
   const bool mods = p.softcap > 0.f || p.slopes != nullptr;
-  auto* fn = mods ? prompt_kernel<D, true, TREE> : prompt_kernel<D, false, TREE>;
+  auto* fn = mods ? prompt_kernel<D, true, KIND> : prompt_kernel<D, false, KIND>;
   static thread_local int set_on[2] = {-1, -1};
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);

@@ -171,7 +171,7 @@ int64_t prompt_workspace(int64_t rows, int32_t B);
 cudaError_t launch_prompt_order(const AttendParams& p, int row_tiles, cudaStream_t s);
 int64_t prompt_order_bytes(int64_t pairs);
 // The same over drafted trees, contexts cut between CTAs where that fills the SMs (p.meta).
-cudaError_t launch_tree(AttendParams p, int num_sms, cudaStream_t s);
+cudaError_t launch_tree(const AttendParams& p, int num_sms, cudaStream_t s);
 int64_t tree_workspace(int64_t rows, const CacheView& c, int num_sms);
 bool tree_fits(const CacheView& c);
 cudaError_t launch_tree_join(const AttendParams& p, int64_t pieces, int num_sms, cudaStream_t s);

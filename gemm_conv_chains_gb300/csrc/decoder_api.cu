@@ -194,26 +194,25 @@ bool prompt_pays(int32_t D, int64_t rows, int64_t heads, bool few_keys, int num_
 }
 
 // The same for drafted trees, where the tcgen05 kernel cuts long contexts if its units do not fill the
-// SMs.  Split kernel: 15 us, and 11.8 ns (7.8 at head size 64) per 32 rows and 128 keys.  tcgen05: 20 us
-// and 1.95 us (1.45 with one row tile; 1.4 at head size 64) per 128 keys of a unit and wave of units; cut,
-// 28 us and the even share of that.  Measured on 8 kv heads of 128, 4 query heads each:
-//   1 sequence,   16 nodes, 16000 cached: split  40 us, tcgen05 31      4000 cached: 26.5 and 23
-//   1 sequence,   64 nodes,  1000 cached: split  30 us, tcgen05 29       300 cached: 15.7 and 23
-//   16 sequences, 60 nodes, up to 4096:   split 222 us, tcgen05 82
-//   32 sequences, 16 nodes, up to 4000:   split 127 us, tcgen05 119      8 nodes: 92 and 139
-//   8 sequences,  12 nodes, up to 8000:   split  54 us, tcgen05 70
+// SMs.  Split kernel: 15 us, and 11.8 ns (7.8 at head size 64) per 32 rows and 128 keys.  tcgen05: 14 us
+// and 2.05 us (1.55 with one row tile; 1.35 at head size 64) per 128 keys of a unit and wave of units; cut,
+// 20 us and the even share of that.  Measured on 8 kv heads of 128, 4 query heads each:
+//   1 sequence,   17 nodes, 16000 cached: split  41 us, tcgen05 29
+//   1 sequence,   64 nodes,  4000 cached: split  43 us, tcgen05 27      1000 cached: 30 and 26
+//   16 sequences, 60 nodes, up to 4096:   split 222 us, tcgen05 79
+//   32 sequences, 17 nodes, up to 4000:   split 127 us, tcgen05 80      8 nodes: 92 and 93
 bool tree_pays(const CacheView& c, int64_t rows, int num_sms) {
   if (rows <= 32) return false;
   const int64_t units = (rows + 255) / 256 * c.heads * c.B;
   const double tiles = static_cast<double>(((static_cast<int64_t>(c.max_pages) << c.page_shift) + 127) / 128);
   const double split_ns = c.D == 64 ? 7.8 : c.D == 96 ? 9.0 : 11.8;
-  const double tile_ns = (c.D == 64 ? 1400.0 : c.D == 96 ? 1700.0 : 1950.0) * (rows <= 128 ? 0.75 : 1.0);
+  const double tile_ns = (c.D == 64 ? 1350.0 : c.D == 96 ? 1750.0 : 2050.0) * (rows <= 128 ? 0.75 : 1.0);
   const double split = 15000.0 + split_ns * static_cast<double>((rows + 31) / 32) * c.heads * c.B * tiles;
   const bool cut = 4 * units < 3 * num_sms && tiles > 4;
   const double share = units * tiles / num_sms;
   const double waves = static_cast<double>((units + num_sms - 1) / num_sms);
-  const double other = cut ? 28000.0 + tile_ns * (share > 4 ? share : 4) : waves * (20000.0 + tile_ns * tiles);
-  return other < 0.95 * split;
+  const double other = cut ? 20000.0 + tile_ns * (share > 4 ? share : 4) : waves * (14000.0 + tile_ns * tiles);
+  return other < 0.9 * split;
 }
 
 // The limit of each on-chip wait of the tcgen05 kernel.

@@ -45,9 +45,9 @@ cudaError_t launch_prompt(const AttendParams& p, cudaStream_t s) {
     if (cudaError_t e = launch_prompt_order(p, static_cast<int>(row_tiles), s); e != cudaSuccess) return e;
   }
   switch (p.c.D) {
-    case 64: return launch_prompt_d<64, false>(p, static_cast<int>(row_tiles), ctas, s);
-    case 96: return launch_prompt_d<96, false>(p, static_cast<int>(row_tiles), ctas, s);
-    case 128: return launch_prompt_d<128, false>(p, static_cast<int>(row_tiles), ctas, s);
+    case 64: return launch_prompt_d<64, kCausal>(p, static_cast<int>(row_tiles), ctas, s);
+    case 96: return launch_prompt_d<96, kCausal>(p, static_cast<int>(row_tiles), ctas, s);
+    case 128: return launch_prompt_d<128, kCausal>(p, static_cast<int>(row_tiles), ctas, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -134,12 +134,21 @@ int64_t tree_workspace(int64_t rows, const CacheView& c, int num_sms) {
 }
 bool tree_fits(const CacheView& c) { return c.D <= 128 && c.max_new <= kMostTreeTokens; }
 
-cudaError_t launch_tree(AttendParams p, int num_sms, cudaStream_t s) {
+template <PromptKind KIND>
+static cudaError_t launch_kind(const AttendParams& p, int row_tiles, int64_t ctas, cudaStream_t s) {
+  switch (p.c.D) {
+    case 64: return launch_prompt_d<64, KIND>(p, row_tiles, ctas, s);
+    case 96: return launch_prompt_d<96, KIND>(p, row_tiles, ctas, s);
+    case 128: return launch_prompt_d<128, KIND>(p, row_tiles, ctas, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_tree(const AttendParams& p, int num_sms, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.c.max_new) * p.group;
   const TreeShape shape = tree_shape(rows, p.c, num_sms);
   if (shape.pieces > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   const int row_tiles = static_cast<int>((rows + kPromptRows - 1) / kPromptRows);
-  p.whole = shape.cut ? 0 : 1;
   cudaError_t e = cudaSuccess;
   if (shape.cut) {
     const int64_t plan_blocks = (shape.pieces + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
@@ -148,12 +157,8 @@ cudaError_t launch_tree(AttendParams p, int num_sms, cudaStream_t s) {
     e = launch_prompt_order(p, row_tiles, s);
   }
   if (e != cudaSuccess) return e;
-  switch (p.c.D) {
-    case 64: e = launch_prompt_d<64, true>(p, row_tiles, shape.pieces, s); break;
-    case 96: e = launch_prompt_d<96, true>(p, row_tiles, shape.pieces, s); break;
-    case 128: e = launch_prompt_d<128, true>(p, row_tiles, shape.pieces, s); break;
-    default: return cudaErrorInvalidValue;
-  }
+  e = shape.cut ? launch_kind<kTreeCut>(p, row_tiles, shape.pieces, s)
+                : launch_kind<kTreeWhole>(p, row_tiles, shape.pieces, s);
   if (e != cudaSuccess || !shape.cut) return e;
   return launch_tree_join(p, shape.pieces, num_sms, s);
 }
