@@ -407,9 +407,11 @@ __device__ __forceinline__ float stage_tree_rows(const uint16_t* q, const uint16
   return unit;
 }
 
-// TREE: drafted trees, their units whole (kTreeWhole) or cut in pieces.
+// KIND: prompts, or drafted trees, their units whole (kTreeWhole) or cut in pieces.  LO (fp16 outputs of
+// trees): P V is formed of P and of what its rounding to fp16 leaves, so that only the output's own rounding
+// is left (error of 64 nodes over 131072 tokens against 64 bits 3.2e-4 without, 2.1e-4 with it).
 enum PromptKind { kCausal, kTreeWhole, kTreeCut };
-template <int D, bool MODS, PromptKind KIND>
+template <int D, bool MODS, PromptKind KIND, bool LO>
 __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendParams p,
                                                                    int row_tiles) {
   using L = PromptSmem<D>;
@@ -566,8 +568,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
         ok = wait(&bars->sfull[t], i & 1, PS_SFULL);
         if (!ok) break;
         tc_fence_after_sync();
-        auto tile = [&](auto scores) {
-        constexpr bool SCORES = decltype(scores)::value;
+        // the reference, and what O and the row's sum have to be scaled by for it
+        auto move_reference = [&](float top, uint32_t (&r)[32]) -> float {
+          float f = 1.f;
+          if (top > m + 15.f) {
+            f = exp2_fast(m - (top - 7.f));
+            m = top - 7.f;
+            l *= f;
+          }
+          if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              tmem_load32(tm + o_col + 32 * q, r);
+              tmem_wait32(r);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+              tmem_st32(tm + o_col + 32 * q, r);
+            }
+          }
+          return f;
+        };
         // a score in the log2 domain
         auto score = [&](uint32_t raw, float f, int tok) -> float {
           float z = __uint_as_float(raw) * f;
@@ -580,6 +600,108 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
           }
           return z;
         };
+        // LO: 64 keys at a time, whose P and rest (32 columns each) take the place of their scores.  As
+        // below, inner tiles take one pass and a second two only if some exponent turns out above 15; where
+        // the reference then moves for the second 64 keys, the first ones' P and rest are scaled too.
+        [[maybe_unused]] auto half_with_rest = [&](auto half, auto scores) {
+          constexpr int kHalf = decltype(half)::value, kFirst = 4 * kHalf;
+          constexpr bool SCORES = decltype(scores)::value;
+          const uint32_t at = tm + s_col + 64 * kHalf;
+          uint32_t r[2][16], hi[32], lo[32];
+          // P, its rest and the sums; false, and nothing done, where an exponent is above 15 and that was not
+          // ruled out before
+          auto take = [&](auto masked, bool ruled_out) -> bool {
+            constexpr bool MASKED = decltype(masked)::value;
+            float high = -INFINITY, more = 0.f;
+            tmem_ld16(at, r[0]);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              tmem_wait_ld(r[g & 1]);
+              if (g + 1 < 4) tmem_ld16(at + 16 * (g + 1), r[(g + 1) & 1]);
+              const float2 s2 = sc[kFirst + g];
+              const float fg = MASKED ? 1.f : fac * s2.x;
+              // (a page that the row does not reach may have any scale, a NaN too)
+              const bool past = MASKED && window(tok0 + 16 * (kFirst + g)) == 0u;
+              const float back = past ? 0.f : exp2_fast(-s2.y), c = past ? 0.f : s2.y - m;
+              const float2 f2 = make_float2(fg, fg), c2 = make_float2(c, c);
+              float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                const uint32_t* x = &r[g & 1][e];
+                float2 y = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), f2, c2);
+                high = max3(high, y.x, y.y);
+                y.x = exp2_fast(y.x);
+                y.y = exp2_fast(y.y);
+                sum = add2(sum, y);
+                const uint32_t h = narrow2<false>(y.x, y.y);
+                const float2 kept = widen2<false>(h);
+                hi[8 * g + e / 2] = h;
+                lo[8 * g + e / 2] = narrow2<false>(y.x - kept.x, y.y - kept.y);
+              }
+              more = fmaf(sum.x + sum.y, back, more);
+            }
+            if (!ruled_out && __any_sync(0xffffffffu, high > 15.f)) return false;
+            l += more;
+            tmem_st32(at, hi);
+            tmem_st32(at + 32, lo);
+            return true;
+          };
+          if (!SCORES && __all_sync(0xffffffffu, m > -1e29f) && take(std::false_type{}, false)) return;
+          // ---- the largest z + log2 value scale; capped, biased or masked scores go back to TMEM ----
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int g = 0; g < 4; ++g) {
+            uint32_t (&x)[16] = r[0];
+            tmem_ld16(at + 16 * g, x);
+            tmem_wait_ld(x);
+            const float2 s2 = sc[kFirst + g];
+            const float f = fac * s2.x;
+            float most = -INFINITY;                  // of the granule's tokens that the row sees
+            if constexpr (SCORES) {
+              const uint32_t sees = window(tok0 + 16 * (kFirst + g));
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float z =
+                    ((sees >> e) & 1u) == 0u ? -INFINITY : score(x[e], f, tok0 + 16 * (kFirst + g) + e);
+                x[e] = __float_as_uint(z);
+                most = fmaxf(most, z);
+              }
+              tmem_store16(at + 16 * g, x);
+            } else {
+              float a = __uint_as_float(x[0]);
+#pragma unroll
+              for (int e = 1; e + 1 < 16; e += 2) a = max3(a, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+              most = fmaxf(a, __uint_as_float(x[15])) * f;
+            }
+            top = fmaxf(top, most + s2.y);
+          }
+          if constexpr (SCORES) tmem_wait_st();
+          const float f = move_reference(top, hi);
+          if (kHalf == 1 && __any_sync(0xffffffffu, f != 1.f)) {
+            tmem_load32(tm + s_col, hi);
+            tmem_wait32(hi);
+            tmem_load32(tm + s_col + 32, lo);
+            tmem_wait32(lo);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float2 a = widen2<false>(hi[e]), b = widen2<false>(lo[e]);
+              const float x = (a.x + b.x) * f, y = (a.y + b.y) * f;
+              hi[e] = narrow2<false>(x, y);
+              const float2 kept = widen2<false>(hi[e]);
+              lo[e] = narrow2<false>(x - kept.x, y - kept.y);
+            }
+            tmem_st32(tm + s_col, hi);
+            tmem_st32(tm + s_col + 32, lo);
+            tmem_wait_st();
+          }
+          (void)take(std::integral_constant<bool, SCORES>{}, true);
+        };
+        [[maybe_unused]] auto tile_with_rest = [&](auto scores) {
+          half_with_rest(std::integral_constant<int, 0>{}, scores);
+          half_with_rest(std::integral_constant<int, 1>{}, scores);
+        };
+        auto tile = [&](auto scores) {
+        constexpr bool SCORES = decltype(scores)::value;
         // ---- the tile's largest z + log2 value scale; capped, biased or masked scores go back to TMEM ----
         uint32_t r[32];
         float top = -INFINITY;
@@ -615,23 +737,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
           if constexpr (SCORES) tmem_st32(tm + s_col + 32 * q, r);
         }
         if constexpr (SCORES) tmem_wait_st();
-        // ---- the reference, and what O and the row's sum have to be scaled by for it ----
-        float f = 1.f;
-        if (top > m + 15.f) {
-          f = exp2_fast(m - (top - 7.f));
-          m = top - 7.f;
-          l *= f;
-        }
-        if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
-            tmem_load32(tm + o_col + 32 * q, r);
-            tmem_wait32(r);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-            tmem_st32(tm + o_col + 32 * q, r);
-          }
-        }
+        (void)move_reference(top, r);
         // ---- P, and the row's sum ----
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
@@ -666,7 +772,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
         // formed while the columns arrive, and only if some exponent turns out above 15 is the tile
         // done again in two passes.
         bool done = false;
-        if (!MODS && !edge && __all_sync(0xffffffffu, m > -1e29f)) {
+        if constexpr (LO) {
+          if (MODS || edge) tile_with_rest(std::true_type{});
+          else tile_with_rest(std::false_type{});
+          done = true;
+        }
+        if (!LO && !MODS && !edge && __all_sync(0xffffffffu, m > -1e29f)) {
           uint32_t r[2][16], pk[4][16];
           float high = -INFINITY, more = 0.f;
           tmem_ld16(tm + s_col, r[0]);
@@ -697,9 +808,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
             done = true;
           }
         }
-        if (!done) {
-          if (MODS || edge) tile(std::true_type{});
-          else tile(std::false_type{});
+        if constexpr (!LO) {
+          if (!done) {
+            if (MODS || edge) tile(std::true_type{});
+            else tile(std::false_type{});
+          }
         }
         tmem_wait_st();
         tc_fence_before_sync();
@@ -913,10 +1026,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
         if (!ok) break;
         tc_fence_after_sync();
 #pragma unroll
-        for (int ks = 0; ks < kPromptKeys / 16; ++ks)
-          mma_f16_ts(lead, tmem + 256u * t + 128u, tmem + 256u * t + 8u * ks,
-                     v_desc + slot * (L::kTile >> 4) + ks * (2048u >> 4), idesc_o,
-                     i == 0 && ks == 0 ? 0u : 1u);
+        for (int ks = 0; ks < kPromptKeys / 16; ++ks) {
+          const uint32_t at = tmem + 256u * t + 8u * ks + (LO && ks >= 4 ? 32u : 0u);
+          const uint64_t v = v_desc + slot * (L::kTile >> 4) + ks * (2048u >> 4);
+          mma_f16_ts(lead, tmem + 256u * t + 128u, at, v, idesc_o, i == 0 && ks == 0 ? 0u : 1u);
+          if constexpr (LO) mma_f16_ts(lead, tmem + 256u * t + 128u, at + 32u, v, idesc_o, 1u);
+        }
         if (more) issue_s(t, next);
         else mma_commit(lead, smem_u32(&bars->ofull[t]));
       }
@@ -938,12 +1053,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
 }
 
 // `ctas`: one per unit, or for drafted trees at least one per piece.
-template <int D, PromptKind KIND>
+template <int D, PromptKind KIND, bool LO = false>
 cudaError_t launch_prompt_d(const AttendParams& p, int row_tiles, int64_t ctas, cudaStream_t s) {
   constexpr int smem = KIND != kCausal ? PromptSmem<D>::kTreeAlloc : PromptSmem<D>::kAlloc;
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
   const bool mods = p.softcap > 0.f || p.slopes != nullptr;
-  auto* fn = mods ? prompt_kernel<D, true, KIND> : prompt_kernel<D, false, KIND>;
+  auto* fn = mods ? prompt_kernel<D, true, KIND, LO> : prompt_kernel<D, false, KIND, LO>;
   static thread_local int set_on[2] = {-1, -1};
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
@@ -954,6 +1069,14 @@ cudaError_t launch_prompt_d(const AttendParams& p, int row_tiles, int64_t ctas, 
     set_on[mods] = dev;
   }
   return launch_early(fn, ctas, kPromptThreads, smem, s, p, row_tiles);
+}
+
+template <int D>
+cudaError_t launch_tree_d(bool cut, const AttendParams& p, int row_tiles, int64_t ctas, cudaStream_t s) {
+  if (p.is_bf16)
+    return cut ? launch_prompt_d<D, kTreeCut>(p, row_tiles, ctas, s) : launch_prompt_d<D, kTreeWhole>(p, row_tiles, ctas, s);
+  return cut ? launch_prompt_d<D, kTreeCut, true>(p, row_tiles, ctas, s)
+             : launch_prompt_d<D, kTreeWhole, true>(p, row_tiles, ctas, s);
 }
 
 }  // namespace b2b

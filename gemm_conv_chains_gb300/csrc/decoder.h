@@ -172,6 +172,9 @@ cudaError_t launch_prompt_order(const AttendParams& p, int row_tiles, cudaStream
 int64_t prompt_order_bytes(int64_t pairs);
 // The same over drafted trees, contexts cut between CTAs where that fills the SMs (p.meta).
 cudaError_t launch_tree(const AttendParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_tree_units_64(bool cut, const AttendParams& p, int row_tiles, int64_t ctas, cudaStream_t s);
+cudaError_t launch_tree_units_96(bool cut, const AttendParams& p, int row_tiles, int64_t ctas, cudaStream_t s);
+cudaError_t launch_tree_units_128(bool cut, const AttendParams& p, int row_tiles, int64_t ctas, cudaStream_t s);
 int64_t tree_workspace(int64_t rows, const CacheView& c, int num_sms);
 bool tree_fits(const CacheView& c);
 cudaError_t launch_tree_join(const AttendParams& p, int64_t pieces, int num_sms, cudaStream_t s);

@@ -1,5 +1,5 @@
-// kernels_tree.cu -- the tcgen05 cache attention for wide drafted trees, head sizes 64, 96 and 128, and
-// the plan of its pieces.
+// kernels_tree.cu -- the tcgen05 cache attention for wide drafted trees: the plan of its pieces and its
+// launches.
 #include "cache_prompt.cuh"
 
 namespace b2b {
@@ -134,16 +134,6 @@ int64_t tree_workspace(int64_t rows, const CacheView& c, int num_sms) {
 }
 bool tree_fits(const CacheView& c) { return c.D <= 128 && c.max_new <= kMostTreeTokens; }
 
-template <PromptKind KIND>
-static cudaError_t launch_kind(const AttendParams& p, int row_tiles, int64_t ctas, cudaStream_t s) {
-  switch (p.c.D) {
-    case 64: return launch_prompt_d<64, KIND>(p, row_tiles, ctas, s);
-    case 96: return launch_prompt_d<96, KIND>(p, row_tiles, ctas, s);
-    case 128: return launch_prompt_d<128, KIND>(p, row_tiles, ctas, s);
-    default: return cudaErrorInvalidValue;
-  }
-}
-
 cudaError_t launch_tree(const AttendParams& p, int num_sms, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.c.max_new) * p.group;
   const TreeShape shape = tree_shape(rows, p.c, num_sms);
@@ -157,8 +147,12 @@ cudaError_t launch_tree(const AttendParams& p, int num_sms, cudaStream_t s) {
     e = launch_prompt_order(p, row_tiles, s);
   }
   if (e != cudaSuccess) return e;
-  e = shape.cut ? launch_kind<kTreeCut>(p, row_tiles, shape.pieces, s)
-                : launch_kind<kTreeWhole>(p, row_tiles, shape.pieces, s);
+  switch (p.c.D) {
+    case 64: e = launch_tree_units_64(shape.cut, p, row_tiles, shape.pieces, s); break;
+    case 96: e = launch_tree_units_96(shape.cut, p, row_tiles, shape.pieces, s); break;
+    case 128: e = launch_tree_units_128(shape.cut, p, row_tiles, shape.pieces, s); break;
+    default: return cudaErrorInvalidValue;
+  }
   if (e != cudaSuccess || !shape.cut) return e;
   return launch_tree_join(p, shape.pieces, num_sms, s);
 }

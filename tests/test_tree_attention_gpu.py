@@ -236,6 +236,38 @@ def test_wide_trees_with_cap_and_bias(dt, older, new, heads, group, D, page):
     _check(out, c, q, blocks, D ** -0.5, softcap=20.0, slopes=slopes, positions=at)
 
 
+def test_fp16_outputs_lose_their_own_rounding_only():
+    """Over all rows, the error is that of rounding the exact result to fp16: fp32 sums and 22 bits of
+    each probability leave less than a tenth of it (P in 11 bits alone would add as much again)."""
+    for older, new, heads, group, D in (([3000, 500], [60, 33], 2, 4, 128), ([1500], [80], 2, 2, 64),
+                                        ([700, 1200], [90, 12], 2, 3, 96), ([900], [12], 2, 2, 128)):
+        c = ref.Cache(older, new, heads, D, 32, seed=D)
+        blocks = _blocks(new, D)
+        q = (_randn(D, c.T, heads * group, D) * 0.5).half()
+        out = _run(c, q.cuda(), blocks).cpu().double()
+        want, _ = br.tree_attention(c, q, blocks, D ** -0.5)
+        assert (out - want).norm() <= 1.1 * (want.half().double() - want).norm()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 96, 128])
+def test_wide_trees_whose_scores_and_scales_grow(dt, D):
+    """Every few tokens larger than all before them, in either half of a key tile: references move again and
+    again, P and the sums that are there already are scaled; value scales far apart, some zero."""
+    c = ref.Cache([1500, 900], [70, 40], 2, D, 16, seed=6)
+    g = torch.Generator().manual_seed(9)
+    for b in range(2):
+        n = -(-c.lens[b] // 16)
+        ids = c.table[b, :n].long()
+        c.ks[ids] *= torch.exp2(torch.linspace(-4, 6, n))[:, None]
+        c.vs[ids] *= torch.exp2(torch.rand(n, 1, generator=g) * 24 - 12)
+        c.vs[ids[5]] = 0
+    blocks = _blocks(c.new, 3)
+    q = _randn(8, c.T, 6, D).to(DT[dt])
+    out = _run(c, q.cuda(), blocks)
+    _check(out, c, q, blocks, D ** -0.5)
+
+
 def test_wide_sets_that_hide_and_nans_that_are_hidden():
     """Rows that see no new token or nothing at all; NaN codes of new tokens reach who sees them only."""
     for D, page in ((64, 16), (128, 64), (96, 32)):
