@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
   uint32_t* all_words = ONE ? reinterpret_cast<uint32_t*>(kept + p.rows) : p.owners;
   uint32_t* words = all_words + lo;                    // this CTA's
 
+  if constexpr (!ONE) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   begin();
   if constexpr (ONE) {
     for (uint32_t i = threadIdx.x; i < n; i += kPagesThreads) words[i] = kNobody;
@@ -181,6 +182,8 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
   if constexpr (ONE) {
     if (threadIdx.x == 0) free_of[0] = here;
   } else {
+    // (the others' shared memory may be written once they have started, which this tells)
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     if (threadIdx.x < ctas) cluster_store(mapa_shared(smem_u32(&free_of[rank]), threadIdx.x), here);
   }
   // ---- what the rows need, and the rank of each one's first page ----

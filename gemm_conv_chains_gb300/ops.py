@@ -563,7 +563,7 @@ def cache_tree_attention(q, masks, k_cache, v_cache, k_scale, v_scale, page_tabl
     [T, words], usually a node's ancestors and itself; a row that sees nothing is zero).  positions
     [T] (int32): the new tokens' positions for `slopes`' distances (None: their slots').  The tokens
     are appended in any order (cache_append), their keys turned before by `rotary` with those
-    positions (b2b_cache_tree_attention)."""
+    positions (b2b_cache_tree_attention).  It has no gradient: the output requires none."""
     got = (_native or _binding()).cache_tree_attention(
         q, masks, k_cache, v_cache, k_scale, v_scale, page_table, lens, starts, max_new, positions,
         scale, softcap, slopes, out, workspace, stream)

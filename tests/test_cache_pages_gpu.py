@@ -319,6 +319,31 @@ def test_kept_in_place_and_equal_scales():
     assert (ks == 0.5).all() and (vs == 0.25).all()
 
 
+def test_compact_past_32_bit_offsets():
+    """Pages whose bytes lie past 4 GB of their pools."""
+    heads, D, page = 8, 128, 256
+    pages = 2 ** 32 // (heads * page * D) + 12
+    c = ref.Cache([3], [1500], heads, D, page, seed=4, spare=0)
+    n = c.pages
+    far = torch.arange(pages - n, pages)
+    kc = torch.zeros(pages, heads, page, D, dtype=torch.uint8, device="cuda").view(F8)
+    vc = torch.zeros_like(kc)
+    ks, vs = torch.zeros(pages, heads, device="cuda"), torch.zeros(pages, heads, device="cuda")
+    for small, large in ((c.k, kc), (c.v, vc)):
+        large.view(torch.uint8)[far.cuda()] = small.view(torch.uint8).cuda()
+    ks[far.cuda()], vs[far.cuda()] = c.ks.cuda(), c.vs.cuda()
+    table = torch.where(c.table >= 0, c.table + pages - n, -1)
+    tokens = _kept(c, [3], [700], 5)
+    ops.cache_compact(kc, vc, ks, vs, table.cuda(), _ints(c.lens), _ints([3]), _ints(tokens), _ints([700]))
+    for codes, scale, g, gs in ((c.k, c.ks, kc, ks), (c.v, c.vs, vc, vs)):
+        want, s = br.compact(codes, scale, c.table.tolist(), page, [3], tokens, [700])
+        assert torch.equal(gs[far.cuda()].cpu().double(), s)
+        got = g[far.cuda()].cpu().double()
+        for j in range(703):
+            assert torch.equal(got[c.table[0, j // page], :, j % page], want[c.table[0, j // page], :, j % page])
+        assert (g.view(torch.uint8)[: pages - n] == 0).all()
+
+
 def test_compact_of_zero_scales_and_nan_codes():
     c = ref.Cache([10], [100], 2, 64, 16, seed=5)
     c.ks[c.table[0, 2]] = 0                          # a page of zeros

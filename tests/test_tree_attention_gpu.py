@@ -298,6 +298,37 @@ def test_long_context_and_wide_tree():
         _check(out, c, q, blocks, D ** -0.5)
 
 
+def test_more_nodes_than_the_wide_kernel_takes():
+    """700 and 1030 drafted tokens: masks of 17 words, on the kernel that splits along the context."""
+    c = ref.Cache([1200, 3], [700, 1030], 1, 64, 64, seed=2, fill=0x7F)
+    blocks = _blocks(c.new, 8, 40)
+    q = _randn(4, c.T, 2, 64).half()
+    out = _run(c, q.cuda(), blocks)
+    _check(out, c, q, blocks, 0.125)
+
+
+@pytest.mark.parametrize("new,D", [(3, 64), (40, 128), (5, 256)])
+def test_past_32_bit_offsets(new, D):
+    """Pages whose bytes, and scales, lie past 4 GB of their pools."""
+    heads, page, older = 8, 256, 1300
+    pages = 2 ** 32 // (heads * page * D) + 12
+    c = ref.Cache([older], [new], heads, D, page, seed=3)
+    used = c.table[0, : -(-c.lens[0] // page)].long()
+    far = torch.arange(pages - len(used), pages).flip(0)
+    kc = torch.zeros(pages, heads, page, D, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    vc = torch.zeros_like(kc)
+    ks, vs = torch.zeros(pages, heads, device="cuda"), torch.zeros(pages, heads, device="cuda")
+    for small, large in ((c.k, kc), (c.v, vc), (c.ks, ks), (c.vs, vs)):
+        raw = torch.uint8 if large is kc or large is vc else torch.float32
+        large.view(raw)[far.cuda()] = small.view(raw)[used].cuda()
+    table = far.to(torch.int32)[None].cuda()
+    blocks = _blocks(c.new, 4)
+    q = _randn(5, new, 2 * heads, D).half()
+    out = ops.cache_tree_attention(q.cuda(), br.words(blocks).cuda(), kc, vc, ks, vs, table,
+                                   torch.tensor(c.lens, dtype=torch.int32).cuda())
+    _check(out, c, q, blocks, D ** -0.5)
+
+
 def test_graph_and_stream():
     c = ref.Cache([1200, 90], [9, 30], 2, 128, 32, seed=9)
     blocks = _blocks(c.new, 9)
