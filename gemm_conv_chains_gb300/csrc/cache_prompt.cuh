@@ -54,7 +54,7 @@ constexpr int kGranules = kPromptKeys / kGranule;
 constexpr int kEdgeTokens = 512;
 
 enum PromptSite : uint32_t {
-  PS_QFULL = 48, PS_KFULL, PS_KEMPTY, PS_VFULL, PS_VEMPTY, PS_SFULL, PS_PREADY, PS_OFULL, PS_DRAIN
+  PS_QFULL = 48, PS_KFULL, PS_KEMPTY, PS_VFULL, PS_VEMPTY, PS_SFULL, PS_PREADY, PS_OFULL, PS_DRAIN, PS_MERGE
 };
 
 template <int D>
@@ -74,7 +74,7 @@ struct PromptSmem {
 };
 
 struct PromptBars {
-  uint64_t qfull[2], kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pready[2], ofull[2], drain;
+  uint64_t qfull[2], kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pready[2], ofull[2], drain, merge;
   uint32_t tmem, abort_flag, nan_any;
 };
 static_assert(sizeof(PromptBars) <= 256, "barrier block");
@@ -187,13 +187,22 @@ __device__ __forceinline__ bool prompt_unit(const AttendParams& p, int b, int h,
 
 // Drafted trees.  All rows of a sequence see its older tokens, few of them new ones, so that a
 // sequence's units all walk the same key tiles, and one sequence may have nearly all of them.  Where the
-// units do not fill the SMs, those of more than L key tiles are cut into equal pieces of at most L, with
-// a CTA each, and a further kernel joins their parts; L is what an even share of all key tiles over the SMs
-// comes to, at least kMinPieceTiles.  A small kernel ahead writes the pieces down from the lengths.  A CTA's
-// own start and end are ~11 us, its tiles 1.55 (one row tile) to 2.05 us at 128 channels: 1 sequence of 64
-// nodes over 131072 tokens, 16 query heads on 2: 68 us, 1.0 PFLOP/s (1919 us uncut; pieces of half the share
-// and of one and a half were 30 % slower); 16 sequences of up to 60 nodes over up to 4096 tokens, 32 on 8,
-// 128 units: 79 us uncut, 6 us more cut.
+// units leave SMs idle, those of more than L key tiles are cut into equal pieces of at most L, with
+// a CTA each, and a further kernel joins their parts; L is an even share of all key tiles over the SMs or up
+// to three of them, whichever takes the least time in whole waves, at least kMinPieceTiles.  A small kernel
+// ahead writes the pieces down from the lengths.
+//
+// A unit of one row tile (`pairs`) gives every other key tile to the second softmax, with S, P and O of its
+// own over a second copy of Q, so that two chains are on their way; at the end the two are merged.  Warps
+// whose 32 rows are all past the unit's pass.  The codes of the tile after next are asked for into L2.
+// 32 sequences of up to 8 nodes over up to 4096 tokens, 32 heads on 8 of 128, bf16: 92 us without the three,
+// 86 with pairs, 80 with L2 ahead too, 74 with all.
+//
+// A CTA's own start and end are ~11 us.  A tile of 128 channels is 1.2 us in pairs and 1.5 us with two row tiles
+// (bf16; 0.67 and 1.34 at the library's dense rate), 2.0 and 2.4 us in fp16 (LO below; 1.0 and 2.0): with two
+// row tiles the products are the bound, in pairs the chain of hand-offs.  16 sequences of up to 60 nodes over up
+// to 4096 tokens, 32 heads on 8, bf16: 71 us.  1 sequence of 64 nodes over 131072 tokens, 16 heads on 2: 73 us in
+// bf16, 0.94 PFLOP/s, 97 in fp16 (1919 us uncut; pieces of half the share 30 % slower).
 constexpr int kMinPieceTiles = 4;
 // The most new tokens of a sequence: what some rows see and others do not has to fit kEdgeTokens.
 constexpr int kMostTreeTokens = kEdgeTokens - kPromptKeys;
@@ -265,6 +274,7 @@ struct PromptProducer {
   static constexpr int kEach = kLanes;                // loads per thread and tile
   uint32_t tid;
   int page;                                           // number of granule lane & 7's page, next tile
+  int later;                                          // trees: of the tile behind it
 
   // The thread's run in load j: token j kTokens + tid / kLanes.  A load's tokens lie in one 16-token
   // granule (two with kTokens = 32, one per half of the warpgroup), and so in one page.
@@ -280,6 +290,27 @@ struct PromptProducer {
     page = at < u.kv_end ? p.c.page_table[static_cast<int64_t>(u.b) * p.c.max_pages +
                                           (at >> p.c.page_shift)]
                          : 0;
+  }
+  // The same two tiles ahead; its codes are asked for into L2 by `ahead`.
+  __device__ __forceinline__ void locate_later(const AttendParams& p, const PromptUnit& u, int tile) {
+    const int at = tile * kPromptKeys + static_cast<int>(tid & 7) * kGranule;
+    later = at < u.kv_end ? p.c.page_table[static_cast<int64_t>(u.b) * p.c.max_pages +
+                                           (at >> p.c.page_shift)]
+                          : -1;
+  }
+  // Asks for the codes of `tile`, a 128-byte line per thread, and moves on by a tile.
+  __device__ __forceinline__ void ahead(const AttendParams& p, const PromptUnit& u, int tile, const uint8_t* pool) {
+    constexpr int kLines = D * kGranule / 128;
+    const CacheView& c = p.c;
+    const int g = static_cast<int>(tid) / kLines, line = static_cast<int>(tid) % kLines;
+    const int id = __shfl_sync(0xffffffffu, later, g & 7);
+    if (g < kGranules && static_cast<uint32_t>(id) < static_cast<uint32_t>(c.pages)) {
+      const int slot = (tile * kPromptKeys + g * kGranule) & ((1 << c.page_shift) - 1);
+      const uint8_t* at = pool + (((static_cast<int64_t>(id) * c.heads + u.h) << c.page_shift) + slot) * D + line * 128;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+    }
+    page = later;
+    locate_later(p, u, tile + 1);
   }
   // Starts the loads of this thread's runs of the located tile.  A number outside the pool is
   // replaced (it is recorded with the scales, which become NaN); slots at or past kv_end are read
@@ -447,6 +478,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
     }
   }
   const int first_tile = CUT ? u.t0 : 0;
+  // One row tile: both softmaxes work on it, on every other key tile each, and are merged at the end.  A softmax
+  // that has only seen pages of no value has its sum in units of 2^-96 or less, and so its weight.
+  const bool pairs = TREE && u.row_tiles == 1 && u.tiles > 1;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -460,6 +494,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       mbar_init(smem_u32(&bars->ofull[i]), 1);
     }
     mbar_init(smem_u32(&bars->drain), 1);
+    mbar_init(smem_u32(&bars->merge), 4);
     bars->abort_flag = 0u;
     bars->nan_any = 0u;
     fence_barrier_init();
@@ -486,9 +521,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
     more_registers<kSoftmaxRegs>();
     // ================= softmax =================
     const int t = warp >> 2;
-    const int row = u.row0 + 128 * t + (threadIdx.x & 127);
+    const int tile_row = u.row0 + (pairs ? 0 : 128 * t);
+    const int row = tile_row + (threadIdx.x & 127);
     const bool valid = row < u.rows;
-    if (t < u.row_tiles) {
+    if (t < u.row_tiles || pairs) {
       const uint32_t tm = tmem + ((warp & 3) << 21);          // this warp's 32 lanes
       const uint32_t s_col = 256u * t, o_col = 256u * t + 128u;
       const int tq = valid ? row / p.group : 0;
@@ -502,7 +538,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
         if constexpr (TREE) {
           const int64_t first_row = u.s.row;
           unit = stage_tree_rows<D>(p.q + first_row * p.ldq + static_cast<int64_t>(u.h * p.group) * D, p.q, p.ldq, p.group,
-                                    u.row0 + 128 * t + (warp & 3) * 32, u.rows, base + L::kQ + t * L::kTile,
+                                    tile_row + (warp & 3) * 32, u.rows, base + L::kQ + t * L::kTile,
                                     (threadIdx.x & 127) - lane, p.masks + (first_row + tq) * p.mask_words,
                                     masks + (threadIdx.x & 255), (u.s.n + 31) / 32, p.is_bf16, p.scale < 0.f);
         } else {
@@ -561,12 +597,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       float m = -1e30f, l = 0.f;                   // m: the reference of z + log2 value scale
       bool ok = true;
 
-      for (int i = 0; i < u.tiles && ok; ++i) {
+      const int first = pairs ? t : 0;
+      const bool idle = TREE && tile_row + 32 * (warp & 3) >= u.rows;      // no rows
+      for (int i = first; i < u.tiles && ok; i += pairs ? 2 : 1) {
         const float2* sc = scales + (i & 3) * kGranules;
         const int tok0 = (first_tile + i) * kPromptKeys;
         const bool edge = tok0 + kPromptKeys - 1 > low_limit;
-        ok = wait(&bars->sfull[t], i & 1, PS_SFULL);
+        ok = wait(&bars->sfull[t], (pairs ? i >> 1 : i) & 1, PS_SFULL);
         if (!ok) break;
+        if (idle) {                                // whatever P is: it stays in its row
+          if (lane == 0) mbar_arrive(smem_u32(&bars->pready[t]));
+          continue;
+        }
         tc_fence_after_sync();
         // the reference, and what O and the row's sum have to be scaled by for it
         auto move_reference = [&](float top, uint32_t (&r)[32]) -> float {
@@ -576,7 +618,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
             m = top - 7.f;
             l *= f;
           }
-          if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+          if (i > first && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
               tmem_load32(tm + o_col + 32 * q, r);
@@ -821,9 +863,43 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       }
 
       // ---- the output row ----
-      if (ok && wait(&bars->ofull[t], 0, PS_OFULL)) {
-        tc_fence_after_sync();
+      ok = ok && wait(&bars->ofull[t], 0, PS_OFULL);
+      if (ok) tc_fence_after_sync();
+      // (all products with Q and K have been issued before the last P V of either softmax)
+      const uint32_t merge_at = base + L::kK + (warp & 3) * (32 * D * 4) + lane * (D * 4);
+      if (pairs && t == 1) {
+        if (ok) {
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t r[32];
+            tmem_load32(tm + o_col + 32 * q, r);
+            tmem_wait32(r);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              st_shared16(merge_at + (((8 * q + e / 4) ^ (lane & 7)) << 4), r[e], r[e + 1], r[e + 2], r[e + 3]);
+          }
+          masks[threadIdx.x & 255] = __float_as_uint(m);
+          masks[kPromptRows + (threadIdx.x & 255)] = __float_as_uint(l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->merge));
+        }
+      } else if (ok && (!pairs || wait(&bars->merge, 0, PS_MERGE))) {
+        float mine = 1.f, other = 0.f;             // what the sums of the two are multiplied by
+        bool seen = true, other_seen = false;
+        if (pairs) {
+          const float m1 = __uint_as_float(masks[128 + threadIdx.x]);
+          const float l1 = __uint_as_float(masks[kPromptRows + 128 + threadIdx.x]);
+          seen = l != 0.f;
+          other_seen = l1 != 0.f;
+          const float top = fmaxf(m, m1);
+          mine = exp2_fast(m - top);
+          other = exp2_fast(m1 - top);
+          l = (seen ? mine * l : 0.f) + (other_seen ? other * l1 : 0.f);
+          m = top;
+        }
         const float inv = l == 0.f || l > kNoValues ? 0.f : 1.f / l;
+        mine *= inv;
+        other *= inv;
         float* part = nullptr;
         if (CUT && u.slot >= 0) {
           part = tree_plan(p.meta, gridDim.x, p.c.B).parts +
@@ -850,10 +926,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
           if (TREE || valid) {
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
-              float o[8];
+              float o[8], more[8];
+              if (pairs) {
+                const int chunk = 8 * q + e / 4;
+                const float4 a = ld_shared_f4(merge_at + ((chunk ^ (lane & 7)) << 4));
+                const float4 z = ld_shared_f4(merge_at + (((chunk + 1) ^ (lane & 7)) << 4));
+                more[0] = a.x, more[1] = a.y, more[2] = a.z, more[3] = a.w;
+                more[4] = z.x, more[5] = z.y, more[6] = z.z, more[7] = z.w;
+              }
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                o[k] = inv == 0.f ? 0.f : __uint_as_float(r[e + k]) * inv;
+                o[k] = inv == 0.f || !seen ? 0.f : __uint_as_float(r[e + k]) * mine;
+                if (pairs && other_seen && inv != 0.f) o[k] = fmaf(more[k], other, o[k]);
                 if ((bad >> (e + k)) & 1u) o[k] = __uint_as_float(0x7FC00000u);
               }
               if constexpr (TREE) {
@@ -915,6 +999,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
     prod.fetch(p, u, first_tile, p.c.k, raw);
     float2 s2 = scales_of(first_tile, prod.page);
     prod.locate(p, u, first_tile + 1);
+    if constexpr (TREE) prod.locate_later(p, u, first_tile + 2);
     bool ok = true;
     for (int i = 0; i < u.tiles && ok; ++i) {
       const int slot = i & 1;
@@ -928,7 +1013,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       if (i + 1 < u.tiles) {
         prod.fetch(p, u, first_tile + i + 1, p.c.k, raw);
         s2 = scales_of(first_tile + i + 1, prod.page);
-        prod.locate(p, u, first_tile + i + 2);
+        if constexpr (TREE) prod.ahead(p, u, first_tile + i + 2, p.c.k);
+        else prod.locate(p, u, first_tile + i + 2);
       }
     }
   } else if (warp < 16) {
@@ -941,6 +1027,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
     prod.locate(p, u, first_tile);
     prod.fetch(p, u, first_tile, p.c.v, raw);
     prod.locate(p, u, first_tile + 1);
+    if constexpr (TREE) prod.locate_later(p, u, first_tile + 2);
     bool ok = true;
     for (int i = 0; i < u.tiles && ok; ++i) {
       const int slot = i & 1;
@@ -981,7 +1068,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       if (lane == 0) mbar_arrive(smem_u32(&bars->vfull[slot]));
       if (i + 1 < u.tiles) {
         prod.fetch(p, u, first_tile + i + 1, p.c.v, raw);
-        prod.locate(p, u, first_tile + i + 2);
+        if constexpr (TREE) prod.ahead(p, u, first_tile + i + 2, p.c.v);
+        else prod.locate(p, u, first_tile + i + 2);
       }
     }
   } else {
@@ -1007,16 +1095,47 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
       }
       mma_commit(lead, smem_u32(&bars->sfull[t]));
     };
+    auto issue_o = [&](int t, int slot, bool fresh) {
+#pragma unroll
+      for (int ks = 0; ks < kPromptKeys / 16; ++ks) {
+        const uint32_t at = tmem + 256u * t + 8u * ks + (LO && ks >= 4 ? 32u : 0u);
+        const uint64_t v = v_desc + slot * (L::kTile >> 4) + ks * (2048u >> 4);
+        mma_f16_ts(lead, tmem + 256u * t + 128u, at, v, idesc_o, fresh && ks == 0 ? 0u : 1u);
+        if constexpr (LO) mma_f16_ts(lead, tmem + 256u * t + 128u, at + 32u, v, idesc_o, 1u);
+      }
+    };
     bool ok = wait(&bars->kfull[0], 0, PS_KFULL);
-    for (int t = 0; t < u.row_tiles && ok; ++t) {
+    if (pairs) {
+      // key tile i has operands and softmax i & 1: S of tile i + 2 follows P V of tile i
+      for (int i = 0; i < u.tiles + 2 && ok; ++i) {
+        const int t = i & 1, n = i >> 1;                   // tile i - 2 leaves the softmax, tile i enters
+        if (i >= 2) {
+          ok = wait(&bars->vfull[t], (n - 1) & 1, PS_VFULL) && wait(&bars->pready[t], (n - 1) & 1, PS_PREADY);
+          if (!ok) break;
+          tc_fence_after_sync();
+          issue_o(t, t, i < 4);
+          mma_commit(lead, smem_u32(&bars->vempty[t]));
+          if (i >= u.tiles) mma_commit(lead, smem_u32(&bars->ofull[t]));
+        }
+        if (i < u.tiles) {
+          if (i > 0) ok = wait(&bars->kfull[t], n & 1, PS_KFULL);
+          if (ok && i < 2) ok = wait(&bars->qfull[t], 0, PS_QFULL);
+          if (!ok) break;
+          tc_fence_after_sync();
+          issue_s(t, t);
+          mma_commit(lead, smem_u32(&bars->kempty[t]));
+        }
+      }
+    }
+    for (int t = 0; t < u.row_tiles && ok && !pairs; ++t) {
       ok = wait(&bars->qfull[t], 0, PS_QFULL);
       if (ok) {
         tc_fence_after_sync();
         issue_s(t, 0);
       }
     }
-    if (ok) mma_commit(lead, smem_u32(&bars->kempty[0]));
-    for (int i = 0; i < u.tiles && ok; ++i) {
+    if (ok && !pairs) mma_commit(lead, smem_u32(&bars->kempty[0]));
+    for (int i = 0; i < u.tiles && ok && !pairs; ++i) {
       const int slot = i & 1, next = slot ^ 1;
       const bool more = i + 1 < u.tiles;
       ok = wait(&bars->vfull[slot], (i >> 1) & 1, PS_VFULL);
@@ -1025,13 +1144,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
         ok = wait(&bars->pready[t], i & 1, PS_PREADY);
         if (!ok) break;
         tc_fence_after_sync();
-#pragma unroll
-        for (int ks = 0; ks < kPromptKeys / 16; ++ks) {
-          const uint32_t at = tmem + 256u * t + 8u * ks + (LO && ks >= 4 ? 32u : 0u);
-          const uint64_t v = v_desc + slot * (L::kTile >> 4) + ks * (2048u >> 4);
-          mma_f16_ts(lead, tmem + 256u * t + 128u, at, v, idesc_o, i == 0 && ks == 0 ? 0u : 1u);
-          if constexpr (LO) mma_f16_ts(lead, tmem + 256u * t + 128u, at + 32u, v, idesc_o, 1u);
-        }
+        issue_o(t, slot, i == 0);
         if (more) issue_s(t, next);
         else mma_commit(lead, smem_u32(&bars->ofull[t]));
       }

@@ -177,6 +177,11 @@ cudaError_t launch_tree_units_96(bool cut, const AttendParams& p, int row_tiles,
 cudaError_t launch_tree_units_128(bool cut, const AttendParams& p, int row_tiles, int64_t ctas, cudaStream_t s);
 int64_t tree_workspace(int64_t rows, const CacheView& c, int num_sms);
 bool tree_fits(const CacheView& c);
+// Whether contexts are cut: the units leave SMs idle, and an even share of all key tiles is shorter than
+// a unit's by more than the 8 tiles that the plan and the joining kernel cost.
+inline bool tree_cuts(int64_t units, int64_t tiles, int num_sms) {
+  return 4 * units < 3 * num_sms && tiles - units * tiles / num_sms > 8;
+}
 cudaError_t launch_tree_join(const AttendParams& p, int64_t pieces, int num_sms, cudaStream_t s);
 // Joins what the split kernel left in parts.
 cudaError_t launch_attend_combine(const AttendParams& p, int nt, int num_sms, cudaStream_t s);

@@ -194,25 +194,29 @@ bool prompt_pays(int32_t D, int64_t rows, int64_t heads, bool few_keys, int num_
 }
 
 // The same for drafted trees, where the tcgen05 kernel cuts long contexts if its units do not fill the
-// SMs.  Split kernel: 15 us, and 11.8 ns (7.8 at head size 64) per 32 rows and 128 keys.  tcgen05: 14 us
-// and 2.05 us (1.55 with one row tile; 1.35 at head size 64) per 128 keys of a unit and wave of units; cut,
-// 20 us and the even share of that.  Measured on 8 kv heads of 128, 4 query heads each:
-//   1 sequence,   17 nodes, 16000 cached: split  41 us, tcgen05 29
-//   1 sequence,   64 nodes,  4000 cached: split  43 us, tcgen05 27      1000 cached: 30 and 26
-//   16 sequences, 60 nodes, up to 4096:   split 222 us, tcgen05 79
-//   32 sequences, 17 nodes, up to 4000:   split 127 us, tcgen05 80      8 nodes: 92 and 93
+// SMs.  Split kernel: 15 us, and 14.5 ns (8.5 at head size 64) per 32 rows and 128 keys.  tcgen05: 6 us and,
+// per wave of units, 13 us and 1.55 us (1.25 at head size 64) for each 128 keys, a quarter less with one row
+// tile; cut, 22 us and the even share of that.  Over 9000 drawn shapes of 12 to 700 rows the choice costs 1.0 %
+// over the better kernel, more than 30 % in 30 of them.  Measured on 8 kv heads of 128, 4 query heads each, bf16:
+//   16 sequences,  6 nodes, up to 4000: split  52 us, tcgen05 50
+//   32 sequences,  8 nodes, up to 4096: split  92 us, tcgen05 74      fp16: 110 and 103
+//   32 sequences, 17 nodes, up to 4000: split 139 us, tcgen05 77      fp16: 160 and 83
+//   16 sequences, 64 nodes, up to 4000: split 230 us, tcgen05 68      fp16: 268 and 95
+//   1 sequence,   64 nodes,  4000 cached: split 43 us, tcgen05 28      600 cached: 21 and 24
+//   1 sequence,   17 nodes, 16000 cached: split 47 us, tcgen05 27      4 nodes: 19 and 26
 bool tree_pays(const CacheView& c, int64_t rows, int num_sms) {
-  if (rows <= 32) return false;
+  if (rows <= 16) return false;
   const int64_t units = (rows + 255) / 256 * c.heads * c.B;
-  const double tiles = static_cast<double>(((static_cast<int64_t>(c.max_pages) << c.page_shift) + 127) / 128);
-  const double split_ns = c.D == 64 ? 7.8 : c.D == 96 ? 9.0 : 11.8;
-  const double tile_ns = (c.D == 64 ? 1350.0 : c.D == 96 ? 1750.0 : 2050.0) * (rows <= 128 ? 0.75 : 1.0);
+  const int64_t tiles = ((static_cast<int64_t>(c.max_pages) << c.page_shift) + 127) / 128;
+  const double split_ns = c.D == 64 ? 8.5 : c.D == 96 ? 9.5 : 14.5;
+  const double tile_ns = (c.D == 64 ? 1250.0 : c.D == 96 ? 1500.0 : 1550.0) * (rows <= 128 ? 0.8 : 1.0);
   const double split = 15000.0 + split_ns * static_cast<double>((rows + 31) / 32) * c.heads * c.B * tiles;
-  const bool cut = 4 * units < 3 * num_sms && tiles > 4;
-  const double share = units * tiles / num_sms;
+  const double share = static_cast<double>(units) * tiles / num_sms;
   const double waves = static_cast<double>((units + num_sms - 1) / num_sms);
-  const double other = cut ? 20000.0 + tile_ns * (share > 4 ? share : 4) : waves * (14000.0 + tile_ns * tiles);
-  return other < 0.9 * split;
+  const double other = tree_cuts(units, tiles, num_sms)
+                           ? 22000.0 + tile_ns * (share > 4 ? share : 4)
+                           : 6000.0 + waves * ((rows <= 128 ? 10000.0 : 13000.0) + tile_ns * tiles);
+  return other < 0.95 * split;
 }
 
 // The limit of each on-chip wait of the tcgen05 kernel.

@@ -16,94 +16,100 @@ __device__ __forceinline__ TreeWork tree_work(const AttendParams& p, int b, int&
   return TreeWork{p.c.heads * row_tiles, (s.len + kPromptKeys - 1) / kPromptKeys};
 }
 
-// Every block sums all sequences up and writes down its share of the pieces.
+// How many key tiles a CTA's own start and end cost.
+constexpr int kPieceStart = 8;
+
+// Every block sums all sequences up, one per thread (tree_shape), and writes down its share of the pieces.
+// Their longest is between one and three even shares: eight warps compare two lengths each by the waves that
+// they take, since a few pieces more than SMs take twice as long as a few less.
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const AttendParams p, int64_t most, int num_sms) {
-  __shared__ unsigned long long sums[kPlanThreads / 32];
-  __shared__ int piece_at[kPlanThreads + 1], slot_at[kPlanThreads], count_of[kPlanThreads], rows_of[kPlanThreads];
+  constexpr int kWarps = kPlanThreads / 32, kLengths = 2 * kWarps;
+  __shared__ unsigned long long sums[kWarps];
+  __shared__ int units_of[kPlanThreads], tiles_of[kPlanThreads], piece_at[kPlanThreads + 1], slot_at[kPlanThreads],
+      count_of[kPlanThreads];
+  __shared__ long long cost_of[kLengths];
   grid_launch_dependents();
   grid_dependency_wait();
   const TreePlan plan = tree_plan(p.meta, most, p.c.B);
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  // ---- the longest piece ----
-  int row_tiles;
-  unsigned long long total = 0;
-  for (int b = t; b < p.c.B; b += kPlanThreads) {
-    const TreeWork w = tree_work(p, b, row_tiles);
-    total += static_cast<unsigned long long>(w.units) * w.tiles;
-  }
+  TreeWork w{0, 0};
+  int row_tiles = 0;
+  if (t < p.c.B) w = tree_work(p, t, row_tiles);
+  units_of[t] = w.units;
+  tiles_of[t] = w.tiles;
+  // ---- an even share ----
+  unsigned long long total = static_cast<unsigned long long>(w.units) * w.tiles;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   if (lane == 0) sums[warp] = total;
   __syncthreads();
   total = 0;
-  for (int i = 0; i < kPlanThreads / 32; ++i) total += sums[i];
-  const unsigned long long share = (total + num_sms - 1) / num_sms;
-  const int length =
-      share < kMinPieceTiles ? kMinPieceTiles : share > 0x7FFFFFFF ? 0x7FFFFFFF : static_cast<int>(share);
+  for (int i = 0; i < kWarps; ++i) total += sums[i];
+  const long long share = static_cast<long long>((total + num_sms - 1) / num_sms);
+  auto length_of = [&](int k) -> int {
+    const long long l = share + share * k / 8;
+    return l < kMinPieceTiles ? kMinPieceTiles : l > 0x7FFFFFFF ? 0x7FFFFFFF : static_cast<int>(l);
+  };
+  // ---- the longest piece ----
+  for (int k = warp; k < kLengths; k += kWarps) {
+    const int l = length_of(k);
+    int pieces = 0;
+    for (int b = lane; b < p.c.B; b += 32)
+      if (units_of[b] > 0) pieces += units_of[b] * ((tiles_of[b] - 1) / l + 1);
+    pieces = __reduce_add_sync(0xffffffffu, pieces);
+    if (lane == 0)
+      cost_of[k] = static_cast<long long>((pieces + num_sms - 1) / num_sms) * (static_cast<long long>(l) + kPieceStart);
+  }
   __syncthreads();
-  // ---- 256 sequences at a time: where their pieces and slots begin ----
-  int pieces = 0, slots = 0;
-  for (int b0 = 0; b0 < p.c.B; b0 += kPlanThreads) {
-    const int b = b0 + t;
-    int units = 0, per_unit = 0, tiles = 0;
-    row_tiles = 0;
-    if (b < p.c.B) {
-      const TreeWork w = tree_work(p, b, row_tiles);
-      units = w.units;
-      tiles = w.tiles;
-      per_unit = units > 0 ? (tiles - 1) / length + 1 : 0;
-    }
-    const int mine = units * per_unit, cut_here = per_unit > 1 ? mine : 0;
-    unsigned long long upto = static_cast<unsigned long long>(mine) | static_cast<unsigned long long>(cut_here) << 32;
+  int best = 0;
+  for (int k = 1; k < kLengths; ++k)
+    if (cost_of[k] < cost_of[best]) best = k;
+  const int length = length_of(best);
+  // ---- where the sequences' pieces and slots begin ----
+  const int per_unit = w.units > 0 ? (w.tiles - 1) / length + 1 : 0;
+  const int mine = w.units * per_unit, cut_here = per_unit > 1 ? mine : 0;
+  unsigned long long upto = static_cast<unsigned long long>(mine) | static_cast<unsigned long long>(cut_here) << 32;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  unsigned long long ahead = 0, all = 0;
+  for (int i = 0; i < kWarps; ++i) {
+    ahead += i < warp ? sums[i] : 0ull;
+    all += sums[i];
+  }
+  upto += ahead;
+  const int first_slot = static_cast<int>(upto >> 32) - cut_here;
+  piece_at[t] = static_cast<int>(upto & 0xFFFFFFFFu) - mine;
+  slot_at[t] = per_unit > 1 ? first_slot : -1;
+  count_of[t] = per_unit;
+  if (t == 0) piece_at[kPlanThreads] = static_cast<int>(all & 0xFFFFFFFFu);
+  if (blockIdx.x == 0 && t < p.c.B) plan.cuts[t] = make_int2(first_slot, per_unit);
+  __syncthreads();
+  // ---- the pieces ----
+  const int pieces = piece_at[kPlanThreads];
+  for (int i = static_cast<int>(blockIdx.x) * kPlanThreads + t; i < pieces;
+       i += static_cast<int>(gridDim.x) * kPlanThreads) {
+    int a = 0, z = kPlanThreads - 1;                 // the last sequence whose first piece is at most i
+    while (a < z) {
+      const int mid = (a + z + 1) / 2;
+      if (piece_at[mid] <= i) a = mid;
+      else z = mid - 1;
     }
-    if (lane == 31) sums[warp] = upto;
-    __syncthreads();
-    unsigned long long ahead = 0, all = 0;
-    for (int i = 0; i < kPlanThreads / 32; ++i) {
-      ahead += i < warp ? sums[i] : 0ull;
-      all += sums[i];
-    }
-    upto += ahead;
-    const int first_slot = slots + static_cast<int>(upto >> 32) - cut_here;
-    piece_at[t] = pieces + static_cast<int>(upto & 0xFFFFFFFFu) - mine;
-    slot_at[t] = per_unit > 1 ? first_slot : -1;
-    count_of[t] = per_unit;
-    rows_of[t] = tiles;
-    if (t == 0) piece_at[kPlanThreads] = pieces + static_cast<int>(all & 0xFFFFFFFFu);
-    if (blockIdx.x == 0 && b < p.c.B) plan.cuts[b] = make_int2(first_slot, per_unit);
-    __syncthreads();
-    // ---- their pieces ----
-    const int end = piece_at[kPlanThreads];
-    for (int i = pieces + static_cast<int>(blockIdx.x) * kPlanThreads + t; i < end;
-         i += static_cast<int>(gridDim.x) * kPlanThreads) {
-      int a = 0, z = kPlanThreads - 1;               // the last sequence whose first piece is at most i
-      while (a < z) {
-        const int mid = (a + z + 1) / 2;
-        if (piece_at[mid] <= i) a = mid;
-        else z = mid - 1;
-      }
-      const int n = count_of[a], k = i - piece_at[a], unit = k / n, at = k - unit * n;
-      TreePiece piece;
-      piece.b = b0 + a;
-      piece.h = unit % p.c.heads;
-      piece.rt = unit / p.c.heads;
-      piece.slot = -1;
-      if (slot_at[a] >= 0) {
-        const int row_tiles_a = (piece_at[a + 1] - piece_at[a]) / (n * p.c.heads);
-        piece.slot = slot_at[a] + (piece.h * row_tiles_a + piece.rt) * n + at;
-      }
-      piece.t0 = static_cast<int>(static_cast<int64_t>(rows_of[a]) * at / n);
-      piece.t1 = static_cast<int>(static_cast<int64_t>(rows_of[a]) * (at + 1) / n);
-      piece.pad[0] = piece.pad[1] = 0;
-      if (i < most) plan.pieces[i] = piece;
-    }
-    pieces = end;
-    slots += static_cast<int>(all >> 32);
-    __syncthreads();
+    const int n = count_of[a], k = i - piece_at[a], unit = k / n, at = k - unit * n;
+    TreePiece piece;
+    piece.b = a;
+    piece.h = unit % p.c.heads;
+    piece.rt = unit / p.c.heads;
+    piece.slot = -1;
+    if (slot_at[a] >= 0) piece.slot = slot_at[a] + (piece.h * (units_of[a] / p.c.heads) + piece.rt) * n + at;
+    piece.t0 = static_cast<int>(static_cast<int64_t>(tiles_of[a]) * at / n);
+    piece.t1 = static_cast<int>(static_cast<int64_t>(tiles_of[a]) * (at + 1) / n);
+    piece.pad[0] = piece.pad[1] = 0;
+    if (i < most) plan.pieces[i] = piece;
   }
   if (blockIdx.x == 0 && t == 0) *plan.count = pieces < most ? pieces : static_cast<int>(most);
 }
@@ -116,7 +122,7 @@ TreeShape tree_shape(int64_t rows, const CacheView& c, int num_sms) {
   TreeShape s;
   const int64_t units = (rows + kPromptRows - 1) / kPromptRows * c.heads * c.B;
   const int64_t tiles = ((static_cast<int64_t>(c.max_pages) << c.page_shift) + kPromptKeys - 1) / kPromptKeys;
-  s.cut = 4 * units < 3 * num_sms && tiles > kMinPieceTiles;
+  s.cut = tree_cuts(units, tiles, num_sms) && c.B <= kPlanThreads;
   // pieces of at most L tiles, L >= all tiles / SMs: fewer than SMs besides one per unit, and fewer
   // than 2 SMs in units that are cut
   s.pieces = units + (s.cut ? num_sms : 0);

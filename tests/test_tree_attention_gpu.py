@@ -289,6 +289,55 @@ def test_wide_sets_that_hide_and_nans_that_are_hidden():
         assert (((out.double() - want).abs() <= tol) | want.isnan()).all()
 
 
+# Shapes that go to the wide kernel: cut and whole units; of one row tile, whose key tiles two softmaxes
+# share, and of two; both in one sequence.
+TAKEN = [
+    (True, [2600, 700], [60, 33], 8, 2, 128, 64), (True, [2600, 900], [64, 20], 8, 4, 64, 16),
+    (True, [1800, 5, 0, 2000], [70, 128, 90, 1], 4, 3, 96, 32), (True, [20000], [64], 2, 2, 128, 128),
+    (False, [400, 120, 0, 800, 300, 64, 1, 511], [30, 12, 40, 7, 25, 32, 40, 1], 4, 3, 128, 32),
+    (False, [400, 120, 0, 800, 300, 64, 1, 511], [30, 12, 32, 7, 25, 32, 32, 1], 8, 8, 64, 256),
+    (False, [400, 120, 0, 800, 300, 64, 1, 511], [30, 12, 32, 7, 25, 32, 32, 1], 8, 3, 96, 16),
+]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("what", ["plain", "cap and bias", "growing", "hidden"])
+@pytest.mark.parametrize("cut,older,new,heads,group,D,page", TAKEN)
+def test_the_wide_kernel(what, dt, cut, older, new, heads, group, D, page):
+    c = ref.Cache(older, new, heads, D, page, seed=D + len(older), fill=0x7F)
+    Hq = heads * group
+    blocks, kw, ref_kw = _blocks(new, D, 5), {}, {}
+    g = torch.Generator().manual_seed(3)
+    if what == "cap and bias":
+        slopes = torch.rand(Hq, generator=g) * 0.3
+        depth = torch.cat([b.sum(-1) - 1 for b in blocks]).int()
+        at = depth + torch.repeat_interleave(torch.tensor(older), torch.tensor(new)).int()
+        ref_kw = dict(softcap=15.0, slopes=slopes, positions=at)
+        kw = dict(softcap=15.0, slopes=slopes.cuda(), positions=at.cuda())
+    if what == "growing":                            # and whole key tiles of no value, and of no weight
+        for b in range(len(new)):
+            n = -(-c.lens[b] // page)
+            ids = c.table[b, :n].long()
+            c.ks[ids] *= torch.exp2(torch.linspace(-4, 5, n))[:, None]
+            c.vs[ids] *= torch.exp2(torch.rand(n, 1, generator=g) * 20 - 10)
+            c.vs[ids[(torch.arange(n) * page // 128) % 2 == b % 2]] = 0
+    if what == "hidden":
+        blocks = [torch.rand(n, n, generator=g) < 0.2 for n in new]
+        for b in range(len(new)):
+            blocks[b][new[b] // 2] = False
+            at = older[b] + new[b] - 1
+            c.v.view(torch.uint8)[c.table[b, at // page], heads - 1, at % page, 9] = 0x7F
+    q = _randn(D, c.T, Hq, D).to(DT[dt])
+    space = ops.cache_tree_attention_workspace(c.T, Hq, *c.args())
+    # (the split kernel's is a few MB, or none for contexts of at most 768 tokens)
+    assert space > 2e7 if cut else space <= 1024 and c.table.shape[1] * page > 768
+    out = _run(c, q.cuda(), blocks, **kw)
+    _check(out, c, q, blocks, D ** -0.5, **ref_kw)
+    assert torch.equal(out.nan_to_num(7.0), _run(c, q.cuda(), blocks, **kw).nan_to_num(7.0))
+    if what == "plain":
+        assert torch.equal(out, _run(c, -q.cuda(), blocks, scale=-D ** -0.5))
+
+
 def test_long_context_and_wide_tree():
     for older, new, group, D in ([20011], [64], 4, 128), ([30001], [3], 2, 64), ([9000], [90], 2, 256):
         c = ref.Cache(older, new, 2, D, 128, seed=7, fill=0x7F)
