@@ -259,6 +259,12 @@ b2b_status check_attention(const b2b_cache* c, int64_t T, int32_t q_heads, float
   return B2B_OK;
 }
 
+bool apart(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a == nullptr || b == nullptr || x + static_cast<uint64_t>(a_bytes) <= y ||
+         y + static_cast<uint64_t>(b_bytes) <= x;
+}
+
 // What tells the attention of drafted trees from the causal one: mask null for that.
 struct TreeArgs {
   const uint64_t* masks;
@@ -294,9 +300,12 @@ b2b_status attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, const void
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(slopes, 4) || !aligned(workspace, 16))
     return B2B_ERR_ALIGN;
   if (tree != nullptr && (!aligned(tree->masks, 8) || !aligned(tree->positions, 4))) return B2B_ERR_ALIGN;
+  const int64_t row = static_cast<int64_t>(q_heads) * cache->head_dim;
+  if (tree != nullptr && (!apart(tree->masks, 8 * T * tree->words, out, 2 * T * row) ||
+                          !apart(tree->positions, 4 * T, out, 2 * T * row)))
+    return B2B_ERR_UNSUPPORTED;
   DecoderDevice* d = decoder_device();
   if (d == nullptr) return B2B_ERR_CUDA;
-  const int64_t row = static_cast<int64_t>(q_heads) * cache->head_dim;
   if (overlap(RowSet{q, ldq, row}, RowSet{out, row, row}, T)) return B2B_ERR_UNSUPPORTED;
   const SplitChoice sc = split_of(cache, q_heads, tree != nullptr, d->num_sms);
   if (sc.bytes > 0 && workspace == nullptr) return B2B_ERR_NULL;
@@ -338,12 +347,6 @@ b2b_status attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, const void
   }
   if (e != cudaSuccess || sc.whole) return launched(e);
   return launched(launch_attend_combine(p, sc.nt, d->num_sms, s));
-}
-
-bool apart(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a == nullptr || b == nullptr || x + static_cast<uint64_t>(a_bytes) <= y ||
-         y + static_cast<uint64_t>(b_bytes) <= x;
 }
 
 b2b_status check_pages(int64_t pages, int32_t rows) {

@@ -323,8 +323,9 @@ b2b_status b2b_cache_attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, 
  * itself, but any set will do, an empty one too (a row that sees no key at all is zero); bits from n on
  * are ignored.  masks: device uint64 [T][mask_words], mask_words * 64 >= max_new.  positions: device
  * int32 [T], the position of each new token for the distance bias (a token's depth in the tree, counted
- * from lens[s] - n), or NULL: its slot's.  Older tokens have their slots' positions.  The rest as there,
- * with a workspace of its own size. */
+ * from lens[s] - n), or NULL: its slot's.  Older tokens have their slots' positions.  out over masks or
+ * positions is refused (B2B_ERR_UNSUPPORTED).  With an fp16 output the probabilities keep 22 bits whatever
+ * the number of rows.  The rest as there, with a workspace of its own size. */
 b2b_status b2b_cache_tree_attention_workspace(const b2b_cache* cache, int64_t T, int32_t q_heads,
                                               int64_t* bytes);
 b2b_status b2b_cache_tree_attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, const void* q,

@@ -40,6 +40,12 @@ def test_tree_refusals(L, kw, expect):
     assert tree(L, **kw) == expect
 
 
+@pytest.mark.parametrize("kw", [dict(masks=0x90000), dict(masks=0x8FFF8), dict(masks=0x90008, words=3),
+                                dict(positions=0x90000), dict(positions=0x8FFFC)])
+def test_tree_output_over_what_is_read(L, kw):
+    assert tree(L, **kw) == UNSUP
+
+
 def test_tree_masks_need_a_bit_per_new_token(L):
     c = cache(batch=1, max_new=65)
     assert tree(L, c, T=65, words=1) == SHAPE
