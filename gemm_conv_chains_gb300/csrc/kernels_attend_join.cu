@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, 
 
 // Of the tcgen05 kernel over drafted trees: the pieces of a unit have neighbouring slots.  `each` warps
 // per row take every so-many-th piece, four on their way, and are joined in shared memory.  (16 sequences
-// of 60 nodes, 30720 rows of 2 or 3 pieces: 36 us with a block of four warps per row, as above.)
+// of 60 nodes, each row of 2 or 3 pieces: 36 us with a block of four warps per row, as above.)
 constexpr int kTreeJoinWarps = 8;
 
 template <int D>
