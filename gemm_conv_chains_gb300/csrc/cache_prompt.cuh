@@ -200,7 +200,12 @@ __device__ __forceinline__ bool prompt_unit(const AttendParams& p, int b, int h,
 //
 // A CTA's own start and end are ~11 us.  A tile of 128 channels is 1.2 us in pairs and 1.5 us with two row tiles
 // (bf16; 0.67 and 1.34 at the library's dense rate), 2.0 and 2.4 us in fp16 (LO below; 1.0 and 2.0): with two
-// row tiles the products are the bound, in pairs the chain of hand-offs.  16 sequences of up to 60 nodes over up
+// row tiles the products are the bound.  In pairs a tile takes ~2300 clocks, and three parts take 2200 to 2400 each,
+// by clocks read in every role: the key warps (1000 to 1600 until the tile is stored, 1000 for its scales, the next
+// tile's loads and the line ahead), the issuing warp (waits of ~200, P V 350, S 570) and half of a softmax's chain
+// (of ~2000 of its own and 2400 of hand-offs and products).  Without the exponentials, the conversion or the memory's
+// latency the time stays the same.  The scales and the lines ahead on an idle warp: 74 -> 82 us below; the next
+// tile's loads inside the store loop with all waits of the issuing warp ahead of P V: 74.5.  16 sequences of up to 60 nodes over up
 // to 4096 tokens, 32 heads on 8, bf16: 71 us.  1 sequence of 64 nodes over 131072 tokens, 16 heads on 2: 73 us in
 // bf16, 0.94 PFLOP/s, 97 in fp16 (1919 us uncut; pieces of half the share 30 % slower).
 constexpr int kMinPieceTiles = 4;
