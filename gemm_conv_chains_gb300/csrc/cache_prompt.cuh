@@ -722,7 +722,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const AttendP
             }
             top = fmaxf(top, most + s2.y);
           }
-          if constexpr (SCORES) tmem_wait_st();
+          // (also for what the first half has stored: its P and rest, and O where the reference moved there)
+          if constexpr (SCORES || kHalf == 1) tmem_wait_st();
           const float f = move_reference(top, hi);
           if (kHalf == 1 && __any_sync(0xffffffffu, f != 1.f)) {
             tmem_load32(tm + s_col, hi);
