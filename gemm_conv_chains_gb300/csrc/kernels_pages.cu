@@ -321,6 +321,9 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p) 
 // than a wave later (looked at as they arrive: 62 -> 114 us on the batch below).  Tokens that stay in
 // place are read only where their page's scale grows.  Many tokens: instructions and barriers of the waves,
 // 4.3 TB/s; few: the chain of five dependent loads.
+//
+// A token that is refused (out of order, or on a page that is none) is recorded, and the slot's own token
+// stays in its place as one that is kept: what the page holds keeps its values, whatever its scale becomes.
 constexpr int kCompactThreads = 256;
 constexpr int kMostWave = 256;                         // a page or several
 constexpr int kMostCompactCluster = 16;
@@ -370,8 +373,8 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
 
   // Three dependent loads, each looked at no earlier than a wave after it was asked for.
   struct Token { int from, before; };                  // its position, and the last token's
-  struct Pages { int from, id, to; };                  // the position (-1: none), its page, the page it goes to
-  struct Scale { int id, to; float s; };               // checked pages, -1: none
+  struct Pages { int from, id, to; };                  // the position, its page, the page it goes to
+  struct Scale { int to, id; float s; };               // checked pages, -1: none
   auto ask_token = [&](int w) -> Token {
     const int64_t dst = goes_to(w);
     Token m{static_cast<int>(dst), -1};
@@ -389,25 +392,25 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
     m.from = token.from;
     if (m.from < dst || m.from >= len || token.before >= m.from) {
       index_error(c.err, DK_COMPACT, DEC_ERR_TOKEN, static_cast<uint32_t>(b));
-      m.from = -1;
+      m.from = static_cast<int>(dst);
     }
     m.to = table[dst >> c.page_shift];
-    if (m.from >= 0) m.id = table[m.from >> c.page_shift];
+    m.id = table[m.from >> c.page_shift];
     return m;
   };
   // the tokens of wave w on their way to its buffer; their scales
   auto ask_codes = [&](int w, const Pages& at) -> Scale {
     const int64_t dst = goes_to(w);
     Scale m{-1, -1, 0.f};
+    bool moves = false;
     if (dst < end) {
-      const bool known = at.to >= 0 && at.to < c.pages, comes = at.from >= 0 && at.id >= 0 && at.id < c.pages;
-      if (!known || (at.from >= 0 && !comes)) index_error(c.err, DK_COMPACT, DEC_ERR_PAGE, static_cast<uint32_t>(b));
-      if (known) m.to = at.to;
-      if (known && comes) m.id = at.id;
+      const bool known = at.to >= 0 && at.to < c.pages, comes = at.id >= 0 && at.id < c.pages;
+      if (!known || !comes) index_error(c.err, DK_COMPACT, DEC_ERR_PAGE, static_cast<uint32_t>(b));
+      moves = comes && at.from != dst;
+      if (known) m = Scale{at.to, moves ? at.id : at.to, 0.f};
     }
     int64_t off = -1;
-    if (m.id >= 0)
-      off = at.from == dst ? -2 : (static_cast<int64_t>(m.id) * c.heads + h) * part + (at.from & mask) * D;
+    if (m.id >= 0) off = moves ? (static_cast<int64_t>(m.id) * c.heads + h) * part + (at.from & mask) * D : -2;
     if (t < wave) source[w & 1][t] = off;
     if (m.id >= 0) m.s = scales[static_cast<int64_t>(m.id) * c.heads + h];
     return m;

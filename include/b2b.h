@@ -374,7 +374,10 @@ b2b_status b2b_cache_copy(const b2b_cache* cache, int64_t n, const int32_t* copi
  * eviction: first = 0, tokens all that stay.  A page that receives tokens takes the largest scale s'
  * of the pages that its tokens come from (its own among them if it keeps some), and codes of a
  * smaller scale s become e4m3(code * (s / s')), in fp32, to nearest even; others are moved as they are.
- * Slots past the sequence's new end are unspecified.  Pages that are written belong to one sequence.
+ * Slots past the sequence's new end are unspecified.  A token outside its sequence, out of order or on a
+ * page outside the pool is recorded, and the one at the position that it would go to stays there; a sequence
+ * whose first, count or length does not fit is recorded and left as it is.  Pages that are written belong to
+ * one sequence.
  * Of cache, the pool, page_table and lens are used.  A second call moves tokens again. */
 b2b_status b2b_cache_compact(const b2b_cache* cache, const int32_t* first, const int32_t* tokens,
                              int32_t max_tokens, const int32_t* counts, void* stream);
