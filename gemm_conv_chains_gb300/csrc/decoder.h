@@ -192,5 +192,13 @@ constexpr int32_t kMostPageRows = 4096;
 cudaError_t launch_pages(PagesParams p, void* workspace, int num_sms, cudaStream_t s);
 cudaError_t launch_copy(const CopyParams& p, int num_sms, cudaStream_t s);
 cudaError_t launch_compact(const CompactParams& p, int num_sms, cudaStream_t s);
+constexpr int kMostCompactCluster = 16;
+// CTAs per (sequence, kv head, pool) of the compaction, a power of two of at most `most`, what the device
+// holds in one cluster: more than one where the items leave SMs idle and a wave of each has tokens.
+inline int compact_ctas(int64_t items, int wave, int max_tokens, int num_sms, int most) {
+  int ctas = 1;
+  while (2 * ctas <= most && items * ctas < num_sms && static_cast<int64_t>(ctas) * wave < max_tokens) ctas *= 2;
+  return ctas;
+}
 
 }  // namespace b2b

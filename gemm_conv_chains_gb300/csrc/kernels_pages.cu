@@ -326,7 +326,6 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p) 
 // stays in its place as one that is kept: what the page holds keeps its values, whatever its scale becomes.
 constexpr int kCompactThreads = 256;
 constexpr int kMostWave = 256;                         // a page or several
-constexpr int kMostCompactCluster = 16;
 
 template <int D>
 __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactParams p, int wave, int buffers) {
@@ -544,6 +543,28 @@ cudaError_t launch_copy(const CopyParams& p, int num_sms, cudaStream_t s) {
   return launch_early(copy_kernel, items < most ? items : most, kCopyThreads, 0, s, p);
 }
 
+// The largest cluster of at most `most` CTAs that the current device holds at all: above 8 that is not the
+// same on every one, and a launch of a larger cluster fails.
+template <class... P>
+static int resident_cluster(void (*fn)(P...), int most, int block, int smem) {
+  for (; most > 1; most /= 2) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(most));
+    cfg.blockDim = dim3(static_cast<unsigned>(block));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(most);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg) == cudaSuccess && clusters > 0) break;
+    cudaGetLastError();
+  }
+  return most;
+}
+
 template <int D>
 static cudaError_t launch_compact_d(const CompactParams& p, int num_sms, cudaStream_t s) {
   const int64_t items = static_cast<int64_t>(p.c.B) * p.c.heads * 2;
@@ -552,11 +573,7 @@ static cudaError_t launch_compact_d(const CompactParams& p, int num_sms, cudaStr
   // per sequence, head and pool, 74 of 128, 68 of 128 and two CTAs, 83 of 256 and two.  30011 of 100001
   // tokens, 2 heads of 64, 16 CTAs: 18.8 us of 256, 27.5 of 128; 33 with 8 CTAs.
   const int wave = p.max_tokens > 64 ? kMostWave : page > 64 ? page : 64;
-  int ctas = 1;
-  while (ctas < kMostCompactCluster && items * ctas < num_sms && ctas * wave < p.max_tokens) ctas *= 2;
-  const int buffers = page - 1 + static_cast<int64_t>(p.max_tokens) > static_cast<int64_t>(wave) * ctas ? 2 : 1;
-  const int smem = buffers * wave * D;
-  static thread_local int set_on = -1;
+  static thread_local int set_on = -1, most = 1;
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -565,8 +582,12 @@ static cudaError_t launch_compact_d(const CompactParams& p, int num_sms, cudaStr
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(compact_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
+    most = resident_cluster(compact_kernel<D>, kMostCompactCluster, kCompactThreads, 2 * kMostWave * D);
     set_on = dev;
   }
+  const int ctas = compact_ctas(items, wave, p.max_tokens, num_sms, most);
+  const int buffers = page - 1 + static_cast<int64_t>(p.max_tokens) > static_cast<int64_t>(wave) * ctas ? 2 : 1;
+  const int smem = buffers * wave * D;
   return launch_early_clusters(compact_kernel<D>, items * ctas, ctas, kCompactThreads, smem, s, p, wave, buffers);
 }
 
