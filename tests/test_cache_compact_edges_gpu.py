@@ -1,4 +1,6 @@
 """Kept tokens moved together: what is left where a token is refused, sequences that share pages."""
+import threading
+
 import pytest
 import torch
 
@@ -58,3 +60,34 @@ def test_what_a_refused_token_leaves(what, D, page):
         for j in range(end):
             at = int(c.table[0, j // page])
             assert bool((got[at, :, j % page] == want[at, :, j % page]).all()), j
+
+
+def test_the_first_call_of_a_thread_in_a_graph():
+    """Whatever a thread's first call asks of the device, it may ask while a graph is captured."""
+    c = ref.Cache([4], [5000], 1, 64, 64, seed=2)
+    tokens = list(range(5, 5004, 3))
+    kc, vc, ks, vs, table, lens = c.args(starts=False)
+    lists = _ints([4]), _ints([tokens]), _ints([len(tokens)])
+    before = [t.clone() for t in (kc, vc, ks, vs)]
+    ops.cache_compact(kc, vc, ks, vs, table, lens, *lists)
+    want = [t.clone() for t in (kc, vc, ks, vs)]
+    for t, b in zip((kc, vc, ks, vs), before):
+        t.copy_(b)
+    graph, failed = torch.cuda.CUDAGraph(), []
+
+    def capture():
+        try:
+            with torch.cuda.graph(graph):
+                ops.cache_compact(kc, vc, ks, vs, table, lens, *lists)
+        except Exception as e:                       # noqa: BLE001 (shown by the assertion below)
+            failed.append(e)
+
+    torch.cuda.synchronize()
+    thread = threading.Thread(target=capture)
+    thread.start()
+    thread.join()
+    assert not failed, failed
+    graph.replay()
+    torch.cuda.synchronize()
+    for got, w in zip((kc, vc, ks, vs), want):
+        assert bool((got.view(torch.uint8) == w.view(torch.uint8)).all())
