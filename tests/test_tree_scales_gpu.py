@@ -45,8 +45,8 @@ def _queries(c, Hq, dt, seed):
     return torch.randn(c.T, Hq, c.D, generator=torch.Generator().manual_seed(seed)).to(DT[dt])
 
 
-def _check(out, c, q, blocks):
-    want, tol = br.tree_attention(c, q, blocks, c.D ** -0.5)
+def _check(out, c, q, blocks, **kw):
+    want, tol = br.tree_attention(c, q, blocks, c.D ** -0.5, **kw)
     tol = tol + UNIT[q.dtype] * (want.abs() + tol) + TINY[q.dtype]
     got = out.cpu().double()
     assert torch.equal(got.isnan(), want.isnan())
@@ -87,3 +87,38 @@ def test_references_move_in_both_halves_of_a_key_tile(cut, older, new, heads, gr
     out = ops.cache_tree_attention(*args)
     _check(out, c, q, blocks)
     assert torch.equal(out, ops.cache_tree_attention(*args))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("softcap", [0.0, 15.0])
+@pytest.mark.parametrize("of", ["keys", "values"])
+@pytest.mark.parametrize("page", [16, 32])
+@pytest.mark.parametrize("cut,older,new,heads,group,D", [(None, *s) for s in SPLIT] + WIDE)
+def test_a_page_whose_scale_is_no_number(cut, older, new, heads, group, D, page, of, softcap, dt):
+    """Pages of drafted tokens alone, a NaN as one head's scale: the rows that see any of their tokens are
+    NaN, and those whose masks hide the whole page are not."""
+    older = [n // page * page for n in older]
+    c = ref.Cache(older, new, heads, D, page, seed=D + len(older), fill=0x7F)
+    Hq = heads * group
+    g = torch.Generator().manual_seed(11)
+    blocks = [torch.rand(n, n, generator=g) < 0.3 for n in new]
+    scales = c.ks if of == "keys" else c.vs
+    for b, n in enumerate(new):
+        at = page if n > page else 0                 # the second page of drafted tokens where there is one
+        scales[c.table[b, (older[b] + at) // page], heads - 1] = math.nan
+        mine = slice(at, min(at + page, n))
+        blocks[b][0::3, mine] = False
+        blocks[b][1::3, mine] = False                # and rows that see the page's last token only
+        blocks[b][1::3, mine.stop - 1] = True
+    if cut is not None:
+        _is_wide(c, Hq, cut)
+    q = _queries(c, Hq, dt, 5)
+    out = ops.cache_tree_attention(q.cuda(), br.words(blocks).cuda(), *c.args(), softcap=softcap)
+    _check(out, c, q, blocks, softcap=softcap)
+    nan = out.isnan().cpu()
+    assert not nan[:, : Hq - group].any() and bool((nan.all(-1) == nan.any(-1)).all())
+    row = 0
+    for n in new:
+        assert not nan[row: row + n: 3].any()
+        assert nan[row + 1: row + n: 3, Hq - group:].all()
+        row += n
