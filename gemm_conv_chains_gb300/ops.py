@@ -621,7 +621,13 @@ def cache_compact(k_cache, v_cache, k_scale, v_scale, page_table, lens, first, t
     """Moves the tokens that each sequence keeps together, in place: the token at position
     tokens[b, i] (int32 [B, most], ascending from first[b] on) goes to position first[b] + i, for
     i < counts[b]; lens [B] are the lengths before, first + counts those after.  The accepted path of
-    drafted tokens, or what an eviction leaves (b2b_cache_compact)."""
+    drafted tokens, or what an eviction leaves (b2b_cache_compact).
+
+    Pages from first[b]'s on have to belong to sequence b alone: others that share them (branches of
+    cache_pages) would change too.  An accepted path lies on pages that cache_pages gave its row for
+    its new tokens; before an eviction from shared pages the sequence takes pages of its own: a row of
+    cache_pages with parent -1 and new = its length, its old pages copied there (cache_copy), the
+    eviction from the new row, the old row left out of the next cache_pages."""
     got = (_native or _binding()).cache_compact(k_cache, v_cache, k_scale, v_scale, page_table, lens,
                                                 first, tokens, counts, stream)
     if type(got) is int:

@@ -376,8 +376,12 @@ b2b_status b2b_cache_copy(const b2b_cache* cache, int64_t n, const int32_t* copi
  * smaller scale s become e4m3(code * (s / s')), in fp32, to nearest even; others are moved as they are.
  * Slots past the sequence's new end are unspecified.  A token outside its sequence, out of order or on a
  * page outside the pool is recorded, and the one at the position that it would go to stays there; a sequence
- * whose first, count or length does not fit is recorded and left as it is.  Pages that are written belong to
- * one sequence.
+ * whose first, count or length does not fit is recorded and left as it is.
+ * Every page from first[s]'s on is written and has to belong to that sequence alone: others that share it
+ * would change too, and nothing here can tell.  b2b_cache_pages gives a row the page of its own that its new
+ * tokens begin on, and so an accepted path; an eviction from pages that were shared by branching goes by a
+ * copy: a row with parent -1 and fresh = the sequence's length in that call, the old row's pages copied to its
+ * (b2b_cache_copy), the eviction from the new row, the old one left out of the next call.
  * Of cache, the pool, page_table and lens are used.  A second call moves tokens again. */
 b2b_status b2b_cache_compact(const b2b_cache* cache, const int32_t* first, const int32_t* tokens,
                              int32_t max_tokens, const int32_t* counts, void* stream);

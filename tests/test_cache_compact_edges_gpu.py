@@ -91,3 +91,38 @@ def test_the_first_call_of_a_thread_in_a_graph():
     torch.cuda.synchronize()
     for got, w in zip((kc, vc, ks, vs), want):
         assert bool((got.view(torch.uint8) == w.view(torch.uint8)).all())
+
+
+@pytest.mark.parametrize("D,page,n", [(64, 16, 100), (128, 64, 700), (256, 32, 96)])
+def test_evicting_from_one_of_two_that_share_pages(D, page, n):
+    """A branch gets pages of its own (a row of no parent, its pages copied) before it loses tokens: the
+    other branch keeps every byte, and the evicted one has what it would have had alone."""
+    c = ref.Cache([0], [n], 2, D, page, seed=D, spare=-(-n // page) + 2)
+    c.ks *= torch.exp(torch.randn(c.ks.shape, generator=torch.Generator().manual_seed(1)))
+    kc, vc, ks, vs, table, lens = c.args(starts=False)
+    pool = kc, vc, ks, vs
+    table, lens, copies, left = ops.cache_pages(table, lens, c.pages, page, _ints([0, 0]))
+    assert bool((table[0] == table[1]).all()) and bool((copies[:, 0] == -1).all())
+    mine = [t.clone() for t in pool]
+    # row 2: room for all that row 1 has; then row 1's pages into it
+    table, lens, copies, left = ops.cache_pages(table, lens, c.pages, page, _ints([0, 1, -1]), None, _ints([0, 0, n]))
+    assert left.item() >= 0
+    pages = -(-n // page)
+    each = [min(page, n - j * page) for j in range(pages)]
+    ops.cache_copy(*pool, torch.stack([table[1, :pages], table[2, :pages], _ints(each)], 1).contiguous())
+    tokens = [j for j in range(n) if j < 4 or j % 3 == 1]
+    ops.cache_compact(*pool, table, lens, _ints([n, n, 0]), _ints([tokens] * 3), _ints([0, 0, len(tokens)]))
+    kept = _ints([n, len(tokens)])
+    table, lens, copies, left = ops.cache_pages(table, lens, c.pages, page, _ints([0, 2]), kept)
+    assert lens.tolist() == kept.tolist() and bool((copies[:, 0] == -1).all())
+    assert left.item() == c.pages - pages - -(-len(tokens) // page)
+    for t, b, codes, scale, s in ((kc, mine[0], c.k, c.ks, ks), (vc, mine[1], c.v, c.vs, vs)):
+        own = table[0, :pages].long()
+        assert bool((t.view(torch.uint8)[own] == b.view(torch.uint8)[own]).all())
+        assert bool((s.cpu()[own.cpu()] == scale[own.cpu()]).all())
+        want, ws = br.compact(codes, scale, c.table.tolist(), page, [0], [tokens], [len(tokens)])
+        got, gs = t.cpu().double(), s.cpu().double()
+        for j in range(len(tokens)):
+            at, as_at = int(table[1, j // page]), int(c.table[0, j // page])
+            assert at not in own.tolist() and bool((gs[at] == ws[as_at]).all())
+            assert bool((got[at, :, j % page] == want[as_at, :, j % page]).all()), j
