@@ -627,7 +627,11 @@ def cache_compact(k_cache, v_cache, k_scale, v_scale, page_table, lens, first, t
     cache_pages) would change too.  An accepted path lies on pages that cache_pages gave its row for
     its new tokens; before an eviction from shared pages the sequence takes pages of its own: a row of
     cache_pages with parent -1 and new = its length, its old pages copied there (cache_copy), the
-    eviction from the new row, the old row left out of the next cache_pages."""
+    eviction from the new row, the old row left out of the next cache_pages.
+
+    Moved keys keep the angles that they were turned by.  After an eviction lens, cache_append's own
+    rotation and the distance bias count slots: new tokens are then turned by positions that the program
+    keeps (rotary, then cache_append without a table)."""
     got = (_native or _binding()).cache_compact(k_cache, v_cache, k_scale, v_scale, page_table, lens,
                                                 first, tokens, counts, stream)
     if type(got) is int:

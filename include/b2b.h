@@ -382,6 +382,11 @@ b2b_status b2b_cache_copy(const b2b_cache* cache, int64_t n, const int32_t* copi
  * tokens begin on, and so an accepted path; an eviction from pages that were shared by branching goes by a
  * copy: a row with parent -1 and fresh = the sequence's length in that call, the old row's pages copied to its
  * (b2b_cache_copy), the eviction from the new row, the old one left out of the next call.
+ * Positions after an eviction: a moved key keeps the angle that it was turned by, while lens, an append's
+ * own rotation, the rule j <= i and the distance bias count slots.  A program that wants new tokens to stand
+ * at their distance from what is left turns them by positions that it keeps (b2b_rotary, then an append
+ * without a table); a bias measures the distance of the slots.  An accepted path keeps both where a node's
+ * position was its depth's.
  * Of cache, the pool, page_table and lens are used.  A second call moves tokens again. */
 b2b_status b2b_cache_compact(const b2b_cache* cache, const int32_t* first, const int32_t* tokens,
                              int32_t max_tokens, const int32_t* counts, void* stream);
