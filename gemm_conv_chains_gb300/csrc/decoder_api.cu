@@ -194,10 +194,16 @@ bool prompt_pays(int32_t D, int64_t rows, int64_t heads, bool few_keys, int num_
 }
 
 // The same for drafted trees, where the tcgen05 kernel cuts long contexts if its units do not fill the
-// SMs.  Split kernel: 15 us, and 14.5 ns (8.5 at head size 64) per 32 rows and 128 keys.  tcgen05: 6 us and,
-// per wave of units, 13 us and 1.55 us (1.25 at head size 64) for each 128 keys, a quarter less with one row
-// tile; cut, 22 us and the even share of that.  Over 9000 drawn shapes of 12 to 700 rows the choice costs 1.0 %
-// over the better kernel, more than 30 % in 30 of them.  Measured on 8 kv heads of 128, 4 query heads each, bf16:
+// SMs.  Split kernel: 15 us, and per 32 rows and 128 keys 14.5 ns (head size 96: 9.5, 64: 8.5).  tcgen05, for
+// each 128 keys of a unit: 1.55 us (1.5, 1.25), 0.8 of that with one row tile; a wave of whole units adds 13 us (10 with
+// one row tile), and all of them 6; cut, 22 us and an SM's even share of the key tiles, at least 4.  It has to be 5 %
+// ahead.  Over 9000 drawn shapes of 12 to 700 rows, with tables as wide as the longest sequence, the choice costs
+// 1.0 % over the better kernel, more than 30 % in 30 of them.
+// The host knows a table's width alone.  Tables of 2 to 64 times the longest sequence cost nothing from 2000 to
+// 4096 tokens (32 sequences of up to 8 nodes 70 us, 16 of up to 60 61, one of 64 nodes 29, at every width) and 3 to
+// 9 us on contexts of at most 800, which are then cut or not run whole (one of 64 nodes over 600: 21 -> 28, 4 of 12
+// nodes: 18 -> 25, 32 of 5 nodes: 24 -> 33).
+// Measured on 8 kv heads of 128, 4 query heads each, bf16:
 //   16 sequences,  6 nodes, up to 4000: split  52 us, tcgen05 50
 //   32 sequences,  8 nodes, up to 4096: split  92 us, tcgen05 74      fp16: 110 and 103
 //   32 sequences, 17 nodes, up to 4000: split 139 us, tcgen05 77      fp16: 160 and 83

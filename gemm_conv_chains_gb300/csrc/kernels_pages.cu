@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
 // ------------------------------------------------------------------------------------
 // One block per (copy, pool, head): the first `tokens` tokens of the head's part of a page lie in a row.
 // Bound by memory: 1536 copies of pages of 64 tokens, 8 heads of 128 (two times 201 MB): 65 us, 0.92 of a plain
-// copy's rate.  A few copies: one launch, 1.7 us.
+// copy's rate.  A few copies: one launch, 1.7 us in a graph, 3.4 as calls of their own.
 constexpr int kCopyThreads = 256;
 
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p) {

@@ -325,7 +325,8 @@ b2b_status b2b_cache_attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, 
  * int32 [T], the position of each new token for the distance bias (a token's depth in the tree, counted
  * from lens[s] - n), or NULL: its slot's.  Older tokens have their slots' positions.  out over masks or
  * positions is refused (B2B_ERR_UNSUPPORTED).  With an fp16 output the probabilities keep 22 bits whatever
- * the number of rows.  The rest as there, with a workspace of its own size. */
+ * the number of rows, with a bf16 one 11, an eighth of the output's own rounding.  The rest as there, with a
+ * workspace of its own size. */
 b2b_status b2b_cache_tree_attention_workspace(const b2b_cache* cache, int64_t T, int32_t q_heads,
                                               int64_t* bytes);
 b2b_status b2b_cache_tree_attention(b2b_dtype dt, const b2b_cache* cache, int64_t T, const void* q,
