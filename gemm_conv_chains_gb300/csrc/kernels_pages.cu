@@ -36,9 +36,9 @@ __device__ __forceinline__ void begin() {
 // listed, a run of words per warp; each one that is needed finds its row.  All of it is latency, two to
 // four dependent accesses a step.  Few rows on a small pool run in one CTA, words in shared memory.
 // Otherwise two kernels spread over the card clear and mark words in the workspace, and one cluster,
-// whose CTAs each have a part of the pool and meet once for its counts, does the rest: lowering 125000
-// words of one cluster's shared memory from its eight SMs took 15 us of 25.  64 beams on 4160 pages 5.7 us, 512
-// sequences on 125000 15 us.
+// whose CTAs each have a part of the pool and meet once for its counts, does the rest: lowering the
+// words in one cluster's shared memory from its eight SMs took 15 us of 25.  64 beams on 4160 pages 5.7 us, 512
+// sequences on 102000 15 us.
 constexpr int kPagesThreads = 1024;
 constexpr int kPagesCluster = 8;
 constexpr int kSmallPool = 40 * 1024;                  // words in one CTA's shared memory
